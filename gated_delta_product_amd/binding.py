@@ -57,6 +57,53 @@ class PrepareArgs(ctypes.Structure):
     ]
 
 
+class LinattnArgs(ctypes.Structure):
+    """Mirror of gdp_linattn_args (include/gdp.h)."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("H", _i32), ("HV", _i32), ("K", _i32), ("V", _i32), ("scale", _f32),
+        ("dtype", ctypes.c_int), ("cu_seqlens", _vp), ("num_seqs", _i64),
+        ("q", _vp), ("q_b_stride", _i64), ("q_t_stride", _i64), ("k", _vp), ("k_b_stride", _i64),
+        ("k_t_stride", _i64), ("v", _vp), ("v_b_stride", _i64), ("v_t_stride", _i64),
+        ("g", _vp), ("g_b_stride", _i64), ("g_t_stride", _i64), ("g_head", _vp), ("h0", _vp), ("o", _vp), ("ht", _vp),
+    ]
+
+
+class LinattnGrads(ctypes.Structure):
+    """Mirror of gdp_linattn_grads (include/gdp.h)."""
+    _fields_ = [
+        ("dout", _vp), ("do_b_stride", _i64), ("do_t_stride", _i64), ("dht", _vp), ("dq", _vp), ("dk", _vp),
+        ("dv", _vp), ("dg", _vp), ("dg_head", _vp), ("dh0", _vp),
+    ]
+
+
+class LinattnDecodeArgs(ctypes.Structure):
+    """Mirror of gdp_linattn_decode_args (include/gdp.h)."""
+    _fields_ = [
+        ("n", _i64), ("S", _i64), ("H", _i32), ("HV", _i32), ("K", _i32), ("V", _i32), ("scale", _f32),
+        ("dtype", ctypes.c_int), ("pool", _i64),
+        ("q", _vp), ("q_n_stride", _i64), ("q_t_stride", _i64), ("k", _vp), ("k_n_stride", _i64),
+        ("k_t_stride", _i64), ("v", _vp), ("v_n_stride", _i64), ("v_t_stride", _i64),
+        ("g", _vp), ("g_n_stride", _i64), ("g_t_stride", _i64), ("g_head", _vp), ("state", _vp), ("slots", _vp),
+        ("o", _vp),
+    ]
+
+
+class GroupNormArgs(ctypes.Structure):
+    """Mirror of gdp_group_norm_args (include/gdp.h)."""
+    _fields_ = [
+        ("n", _i64), ("T", _i64), ("groups", _i32), ("D", _i32), ("dtype", ctypes.c_int), ("activation", ctypes.c_int),
+        ("centered", _i32), ("eps", _f32), ("x", _vp), ("x_n_stride", _i64), ("x_t_stride", _i64),
+        ("z", _vp), ("z_n_stride", _i64), ("z_t_stride", _i64), ("w", _vp), ("b", _vp), ("y", _vp),
+    ]
+
+
+class GroupNormGrads(ctypes.Structure):
+    """Mirror of gdp_group_norm_grads (include/gdp.h)."""
+    _fields_ = [
+        ("dy", _vp), ("dy_n_stride", _i64), ("dy_t_stride", _i64), ("dx", _vp), ("dz", _vp), ("dw", _vp), ("db", _vp),
+    ]
+
+
 class GdpError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__("gdp status %d: %s" % (status, msg))
@@ -110,6 +157,20 @@ def lib():
         L.gdp_pipeline_plan.argtypes = [_i64, _i32, ctypes.POINTER(_i64)]
         L.gdp_num_state_chunks.restype = _i64
         L.gdp_num_state_chunks.argtypes = [ctypes.POINTER(_i32), _i64, _i64, _i64, _i32, _i32]
+        L.gdp_linattn_workspace_bytes.restype = _i64
+        L.gdp_linattn_workspace_bytes.argtypes = [ctypes.POINTER(LinattnArgs), _i32]
+        L.gdp_linattn_fwd.restype = ctypes.c_int
+        L.gdp_linattn_fwd.argtypes = [ctypes.POINTER(LinattnArgs), _vp, _i64, _vp]
+        L.gdp_linattn_bwd.restype = ctypes.c_int
+        L.gdp_linattn_bwd.argtypes = [ctypes.POINTER(LinattnArgs), ctypes.POINTER(LinattnGrads), _vp, _i64, _vp]
+        L.gdp_linattn_decode.restype = ctypes.c_int
+        L.gdp_linattn_decode.argtypes = [ctypes.POINTER(LinattnDecodeArgs), _vp]
+        L.gdp_group_norm_fwd.restype = ctypes.c_int
+        L.gdp_group_norm_fwd.argtypes = [ctypes.POINTER(GroupNormArgs), _vp]
+        L.gdp_group_norm_workspace_bytes.restype = _i64
+        L.gdp_group_norm_workspace_bytes.argtypes = [ctypes.POINTER(GroupNormArgs)]
+        L.gdp_group_norm_bwd.restype = ctypes.c_int
+        L.gdp_group_norm_bwd.argtypes = [ctypes.POINTER(GroupNormArgs), ctypes.POINTER(GroupNormGrads), _vp, _i64, _vp]
         L.gdp_last_error.restype = ctypes.c_char_p
         L.gdp_last_error.argtypes = []
         L.gdp_version.restype = ctypes.c_char_p
@@ -556,3 +617,229 @@ def decode_update(q, k, v, beta, g, state, M, slots=None, scale=None, o=None):
                    slots=None if slots is None else _ptr(slots), o=_ptr(o))
     _check(lib().gdp_decode_update(ctypes.byref(a), _stream(dev)))
     return o
+
+
+# ------------------------------------------------------------------ linear attention
+
+def _rows(t, name, shape, dtype, dev):
+    """Checks a [n, T, heads, D] tensor whose rows [heads, D] are contiguous; its batch and token strides."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.dtype != dtype:
+        raise ValueError("q, k, v and %s must share a dtype" % name)
+    if t.device != dev:
+        raise ValueError("tensors on different devices")
+    if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+        raise ValueError("the heads of %s must be contiguous" % name)
+    return t.stride(0), t.stride(1)
+
+
+def _lin_common(q, k, v, g, scale, extra=()):
+    """Dimensions, strides and decay fields shared by the linear-attention calls."""
+    dev = _need_cuda(q, k, v, g, *extra)
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be 4-D")
+    n, T, H, K = q.shape
+    HV, V = v.shape[2], v.shape[3]
+    f = dict(H=H, HV=HV, K=K, V=V, scale=float(scale) if scale is not None else 0.0, dtype=_dtype_code(q.dtype))
+    strides = [_rows(t, nm, s, q.dtype, dev) for t, nm, s in
+               ((q, "q", (n, T, H, K)), (k, "k", (n, T, H, K)), (v, "v", (n, T, HV, V)))]
+    gs = (0, 0)
+    if g is not None:
+        if g.dtype != torch.float32:
+            raise ValueError("g must be float32")
+        if g.dim() == 1:
+            if tuple(g.shape) != (HV,) or not g.is_contiguous():
+                raise ValueError("a decay per head must be a contiguous [HV]")
+            f["g_head"] = g.data_ptr()
+        else:
+            if tuple(g.shape) != (n, T, HV) or (HV > 1 and g.stride(2) != 1):
+                raise ValueError("g must be [n, T, HV] with a contiguous last dimension, or [HV]")
+            gs = (g.stride(0), g.stride(1))
+            f["g"] = g.data_ptr()
+    return dev, n, T, f, strides, gs
+
+
+def _state(t, name, shape, dev):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous()
+                          or t.device != dev):
+        raise ValueError("%s must be a contiguous float32 %s" % (name, list(shape)))
+
+
+def _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, extra=()):
+    dev, B, T, f, (qs, ks, vs), gs = _lin_common(q, k, v, g, scale, (cu_seqlens, initial_state) + tuple(extra))
+    nseq = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+        _contig(cu_seqlens, "cu_seqlens")
+        nseq = cu_seqlens.numel() - 1
+    _state(initial_state, "initial_state", (nseq, f["HV"], f["V"], f["K"]), dev)
+    a = LinattnArgs(B=B, T=T, cu_seqlens=_ptr(cu_seqlens), num_seqs=nseq, q=_ptr(q), q_b_stride=qs[0],
+                    q_t_stride=qs[1], k=_ptr(k), k_b_stride=ks[0], k_t_stride=ks[1], v=_ptr(v), v_b_stride=vs[0],
+                    v_t_stride=vs[1], g_b_stride=gs[0], g_t_stride=gs[1], h0=_ptr(initial_state), **f)
+    return dev, nseq, a
+
+
+def _workspace(need, dev):
+    if need < 0:
+        raise GdpError(GDP_ERR_INVALID, lib().gdp_last_error().decode())
+    # torch's caching allocator returns 512-byte aligned blocks
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def linattn_fwd(q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=None, output_final_state=False, o=None):
+    """gdp_linattn_fwd: linear attention with a decay for each head,
+    S_t = exp(g_t) S_{t-1} + v_t k_t^T and o_t = scale S_t q_t.
+
+    q, k [B, T, H, K], v [B, T, HV, V] (bf16 or f32; heads contiguous, tokens
+    and batch rows may be strided); g float32 [B, T, HV] natural-log decay per
+    token, [HV] per head, or None; cu_seqlens int32 [num_seqs + 1] (B == 1) or
+    None; initial_state [nseq, HV, V, K] float32 or None.  ``o`` may hold a
+    preallocated contiguous output.  Returns (o [B, T, HV, V], ht
+    [nseq, HV, V, K] float32 or None)."""
+    dev, nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, (o,))
+    shape = (a.B, a.T, a.HV, a.V)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=dev)
+    elif tuple(o.shape) != shape or o.dtype != q.dtype or not o.is_contiguous():
+        raise ValueError("o must be a contiguous %s %s" % (q.dtype, list(shape)))
+    ht = torch.empty((nseq, a.HV, a.V, a.K), dtype=torch.float32, device=dev) if output_final_state else None
+    a.o, a.ht = _ptr(o), _ptr(ht)
+    with torch.cuda.device(dev):
+        ws = _workspace(lib().gdp_linattn_workspace_bytes(ctypes.byref(a), 0), dev)
+        _check(lib().gdp_linattn_fwd(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    return o, ht
+
+
+def linattn_bwd(do, q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=None, dht=None):
+    """gdp_linattn_bwd: the gradients of linattn_fwd for those of o (do
+    [B, T, HV, V], strided like v) and of ht (dht, or None).  Returns (dq, dk,
+    dv, dg, dh0): dq, dk [B, T, H, K], summed over the value heads of a key
+    head, dv [B, T, HV, V], dg shaped as g (None without g), dh0
+    [nseq, HV, V, K] float32 (None without initial_state).  Rows of tokens
+    outside every request hold zeros."""
+    dev, nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, (do, dht))
+    dos = _rows(do, "do", v.shape, q.dtype, dev)
+    _state(dht, "dht", (nseq, a.HV, a.V, a.K), dev)
+    new = torch.empty if cu_seqlens is None else torch.zeros
+    dq = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
+    dk = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
+    dv = new((a.B, a.T, a.HV, a.V), dtype=q.dtype, device=dev)
+    per_head = g is not None and g.dim() == 1
+    dg = None
+    if g is not None:
+        dg = (torch.empty if per_head else new)(g.shape, dtype=torch.float32, device=dev)
+    dh0 = None if initial_state is None else torch.empty_like(initial_state)
+    d = LinattnGrads(dout=_ptr(do), do_b_stride=dos[0], do_t_stride=dos[1], dht=_ptr(dht), dq=_ptr(dq), dk=_ptr(dk),
+                     dv=_ptr(dv), dg=None if per_head else _ptr(dg), dg_head=_ptr(dg) if per_head else None,
+                     dh0=_ptr(dh0))
+    with torch.cuda.device(dev):
+        ws = _workspace(lib().gdp_linattn_workspace_bytes(ctypes.byref(a), 1), dev)
+        _check(lib().gdp_linattn_bwd(ctypes.byref(a), ctypes.byref(d), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     _stream(dev)))
+    return dq, dk, dv, dg, dh0
+
+
+def linattn_decode(q, k, v, state, g=None, slots=None, scale=None, o=None):
+    """gdp_linattn_decode: S new tokens of each request through the recurrence
+    of linattn_fwd.  q, k [n, S, H, K], v [n, S, HV, V] (strided as there); g
+    float32 [n, S, HV], [HV] or None; state [pool, HV, V, K] float32, updated
+    in place; slots int32 [n] (outside [0, pool): skipped, its o rows zero) or
+    None.  Returns o [n, S, HV, V]."""
+    dev, n, S, f, (qs, ks, vs), gs = _lin_common(q, k, v, g, scale, (state, slots, o))
+    if state.dim() != 4:
+        raise ValueError("state must be [pool, HV, V, K]")
+    _state(state, "state", (state.shape[0], f["HV"], f["V"], f["K"]), dev)
+    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (n,) or not slots.is_contiguous()):
+        raise ValueError("slots must be a contiguous int32 [n]")
+    if o is None:
+        o = torch.empty((n, S, f["HV"], f["V"]), dtype=q.dtype, device=dev)
+    elif tuple(o.shape) != tuple(v.shape) or o.dtype != q.dtype or not o.is_contiguous():
+        raise ValueError("o must be a contiguous %s %s" % (q.dtype, list(v.shape)))
+    a = LinattnDecodeArgs(n=n, S=S, pool=state.shape[0], q=_ptr(q), q_n_stride=qs[0], q_t_stride=qs[1], k=_ptr(k),
+                          k_n_stride=ks[0], k_t_stride=ks[1], v=_ptr(v), v_n_stride=vs[0], v_t_stride=vs[1],
+                          g_n_stride=gs[0], g_t_stride=gs[1], state=_ptr(state), slots=_ptr(slots), o=_ptr(o), **f)
+    with torch.cuda.device(dev):
+        _check(lib().gdp_linattn_decode(ctypes.byref(a), _stream(dev)))
+    return o
+
+
+# ------------------------------------------------------------------ group norm
+
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _token_rows(t, name, like=None):
+    """[..., C] with a contiguous last dimension as (n, T, n stride, t stride): leading dimensions beyond two
+    have to fold into the first."""
+    if t.dim() < 1 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError("%s must match x: %s %s" % (name, like.dtype, list(like.shape)))
+    lead, strides = list(t.shape[:-1]), list(t.stride()[:-1])
+    while len(lead) < 2:
+        lead.insert(0, 1)
+        strides.insert(0, 0)
+    while len(lead) > 2:
+        if strides[0] != strides[1] * lead[1] and lead[0] > 1:
+            raise ValueError("the leading dimensions of %s must fold into [n, T]" % name)
+        lead[:2], strides[:2] = [lead[0] * lead[1]], [strides[1]]
+    return lead[0], lead[1], strides[0], strides[1]
+
+
+def _norm_args(x, groups, weight, bias, gate, activation, centered, eps, extra=()):
+    dev = _need_cuda(x, weight, bias, gate, *extra)
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % sorted(k for k in ACTIVATIONS if k))
+    C = x.shape[-1]
+    if groups < 1 or C % groups or C < 1:
+        raise ValueError("the %d channels do not split into %d groups" % (C, groups))
+    n, T, ns, ts = _token_rows(x, "x")
+    for t, nm in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous float32 [C]" % nm)
+    a = GroupNormArgs(n=n, T=T, groups=groups, D=C // groups, dtype=_dtype_code(x.dtype),
+                      activation=ACTIVATIONS[activation], centered=1 if centered else 0, eps=float(eps), x=_ptr(x),
+                      x_n_stride=ns, x_t_stride=ts, w=_ptr(weight), b=_ptr(bias))
+    if gate is not None:
+        zn, zT, a.z_n_stride, a.z_t_stride = _token_rows(gate, "gate", x)
+        a.z = _ptr(gate)
+    return dev, a
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="silu", centered=True, eps=1e-5, out=None):
+    """gdp_group_norm_fwd: x [..., C] (bf16 or f32, channels last) normalised per token in ``groups`` groups of
+    neighbouring channels (centered=False: by the root of the mean square alone), times weight plus bias ([C]
+    float32 or None), then times activation(gate), or without a gate through the activation ("silu", "sigmoid",
+    "none").  gate is shaped as x; both may be slices of wider rows.  Returns y, contiguous (``out`` if given; it
+    may be x or gate)."""
+    dev, a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps, (out,))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous %s %s" % (x.dtype, list(x.shape)))
+    a.y = _ptr(out)
+    with torch.cuda.device(dev):
+        _check(lib().gdp_group_norm_fwd(ctypes.byref(a), _stream(dev)))
+    return out
+
+
+def group_norm_bwd(dy, x, groups, weight=None, bias=None, gate=None, activation="silu", centered=True, eps=1e-5):
+    """gdp_group_norm_bwd: the gradients of group_norm_fwd for that of y (dy, shaped as x).  Returns (dx, dz,
+    dweight, dbias): dx and dz as x (dz None without a gate), dweight and dbias [C] float32 (None where there is
+    none)."""
+    dev, a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps, (dy,))
+    _, _, dns, dts = _token_rows(dy, "dy", x)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dz = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    d = GroupNormGrads(dy=_ptr(dy), dy_n_stride=dns, dy_t_stride=dts, dx=_ptr(dx), dz=_ptr(dz), dw=_ptr(dw),
+                       db=_ptr(db))
+    with torch.cuda.device(dev):
+        need = lib().gdp_group_norm_workspace_bytes(ctypes.byref(a)) if dw is not None or db is not None else 0
+        ws = _workspace(need, dev)
+        _check(lib().gdp_group_norm_bwd(ctypes.byref(a), ctypes.byref(d), _ptr(ws), 0 if ws is None else ws.numel(),
+                                        _stream(dev)))
+    return dx, dz, dw, db

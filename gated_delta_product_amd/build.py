@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libgdp.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "prepare.hip", "wy.hip", "chunk_h.hip", "chunk_o.hip", "chunk_ho.hip", "decode.hip",
-           "scan.hip"]
+           "scan.hip", "api_linattn.cpp", "linattn.hip", "lindecode.hip", "groupnorm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -11,11 +11,13 @@
 #include <string>
 #include <vector>
 
+#include "api_common.h"
 #include "gdp_internal.h"
 
-namespace {
+namespace gdp {
+namespace api {
 
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
 gdp_status fail(gdp_status st, const char *fmt, ...) {
     char buf[512];
@@ -32,16 +34,17 @@ gdp_status ok() {
     return GDP_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-size_t dsize(gdp_dtype d) { return d == GDP_BF16 ? 2 : 4; }
-
 gdp_status hip_status(hipError_t e, const char *what) {
     if (e != hipSuccess) return fail(GDP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
     return ok();
 }
+
+}  // namespace api
+}  // namespace gdp
+
+using namespace gdp::api;
+
+namespace {
 
 // Stage masks for validation.
 // stages of a call; ST_WYP is WY with the prepare fused in, which takes its

@@ -1,0 +1,341 @@
+// groupnorm.hip -- group norm with an activation, channels last, every token a
+// sample of its own (the norm per head that follows a token mixer).
+//
+//   xh = (x - mean) rstd  over the D channels of a group (or x rstd),  u = xh w + b
+//   y  = u act(z)  or  act(u)
+// and with du the gradient of u (dy act(z), or dy act'(u)) and dxh = du w:
+//   dx = rstd (dxh - mean(dxh) - xh mean(dxh xh)),  dz = dy u act'(z)
+//   dw = sum over tokens of du xh,  db = sum over tokens of du
+//
+// LPG neighbouring lanes hold a group, NU units of 16 bytes each (of one
+// element where a row is not made of aligned units), so a group is read once
+// and reduced inside a wave; neighbouring groups of a token sit in
+// neighbouring lanes.  Both directions move each tensor once and are bound by
+// that.
+#include "gdp_common.h"
+#include "gdp_internal.h"
+#include "groupnorm.h"
+
+namespace gdp {
+
+namespace {
+
+constexpr int GNT = 256;
+
+template <typename T, int E> struct Unit;
+template <> struct Unit<bf16, 8> { typedef uint4 type; };
+template <> struct Unit<float, 4> { typedef uint4 type; };
+template <> struct Unit<bf16, 1> { typedef bf16 type; };
+template <> struct Unit<float, 1> { typedef float type; };
+
+template <typename T, int E>
+__device__ __forceinline__ void get(const T *p, float *f) {
+    typedef typename Unit<T, E>::type U;
+    const U u = *(const U *)p;
+    const T *e = (const T *)&u;
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = to_f32(e[i]);
+}
+template <typename T, int E>
+__device__ __forceinline__ void put(T *p, const float *f) {
+    typedef typename Unit<T, E>::type U;
+    U u;
+    T *e = (T *)&u;
+#pragma unroll
+    for (int i = 0; i < E; ++i) e[i] = from_f32<T>(f[i]);
+    *(U *)p = u;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+__device__ __forceinline__ float act(int kind, float x) {
+    if (kind == GDP_ACT_NONE) return x;
+    const float s = sigmoid(x);
+    return kind == GDP_ACT_SILU ? x * s : s;
+}
+__device__ __forceinline__ float act_slope(int kind, float x) {
+    if (kind == GDP_ACT_NONE) return 1.0f;
+    const float s = sigmoid(x);
+    return kind == GDP_ACT_SILU ? s * (1.0f + x * (1.0f - s)) : s * (1.0f - s);
+}
+
+__device__ __forceinline__ int64_t row_at(uint32_t row, uint32_t T, int64_t ns, int64_t ts) {
+    const uint32_t n = row / T;
+    return (int64_t)n * ns + (int64_t)(row - n * T) * ts;
+}
+
+// x of one group into xh (normalised) and its rstd
+template <int N, int LPG>
+__device__ __forceinline__ float normalise(float (&x)[N], const bool (&in)[N], int D, float eps, bool centered) {
+    const float inv = 1.0f / (float)D;
+    if (centered) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s += x[i];  // lanes past the group hold zeros
+        const float mean = group_sum<LPG>(s) * inv;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = in[i] ? x[i] - mean : 0.f;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q += x[i] * x[i];
+    const float rstd = 1.0f / sqrtf(group_sum<LPG>(q) * inv + eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= rstd;
+    return rstd;
+}
+
+}  // namespace
+
+template <typename T, int E, int LPG, int NU, bool GATE>
+__global__ void __launch_bounds__(GNT) gdp_group_norm_k(GroupNorm p) {
+    constexpr int N = E * NU;
+    const int64_t set = ((int64_t)blockIdx.x * GNT + threadIdx.x) / LPG;
+    const int l = threadIdx.x % LPG;
+    const uint32_t gi = (uint32_t)(set % p.groups);
+    const int64_t r0 = set / p.groups;
+    if (r0 >= p.split) return;
+    const int col = (int)gi * p.D;
+    bool in[N];
+    float w[N], b[N];
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int d = (l + k * LPG) * E;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            in[k * E + i] = d < p.D;
+            w[k * E + i] = p.w && d < p.D ? p.w[col + d + i] : 1.f;
+            b[k * E + i] = p.b && d < p.D ? p.b[col + d + i] : 0.f;
+        }
+    }
+    for (int64_t row = r0; row < p.rows; row += p.split) {
+        const T *x = (const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col;
+        const T *z = GATE ? (const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col : nullptr;
+        float v[N], zv[GATE ? N : 1];
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[k * E + i] = 0.f;
+            if (d < p.D) {
+                get<T, E>(x + d, v + k * E);
+                if constexpr (GATE) get<T, E>(z + d, zv + k * E);
+            }
+        }
+        normalise<N, LPG>(v, in, p.D, p.eps, p.centered);
+        T *y = (T *)p.y + row * ((int64_t)p.groups * p.D) + col;
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+            if (d >= p.D) continue;
+            float o[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float u = v[k * E + i] * w[k * E + i] + b[k * E + i];
+                o[i] = GATE ? u * act(p.act, zv[GATE ? k * E + i : 0]) : act(p.act, u);
+            }
+            put<T, E>(y + d, o);
+        }
+    }
+}
+
+template <typename T, int E, int LPG, int NU, bool GATE>
+__global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
+    constexpr int N = E * NU;
+    const int64_t set = ((int64_t)blockIdx.x * GNT + threadIdx.x) / LPG;
+    const int l = threadIdx.x % LPG;
+    const uint32_t gi = (uint32_t)(set % p.groups);
+    const int64_t r0 = set / p.groups;
+    if (r0 >= p.split) return;
+    const int col = (int)gi * p.D;
+    const int64_t C = (int64_t)p.groups * p.D;
+    const float inv = 1.0f / (float)p.D;
+    bool in[N];
+    float w[N], b[N], dw[N], db[N];
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int d = (l + k * LPG) * E;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            in[k * E + i] = d < p.D;
+            w[k * E + i] = p.w && d < p.D ? p.w[col + d + i] : 1.f;
+            b[k * E + i] = p.b && d < p.D ? p.b[col + d + i] : 0.f;
+            dw[k * E + i] = db[k * E + i] = 0.f;
+        }
+    }
+    for (int64_t row = r0; row < p.rows; row += p.split) {
+        const T *x = (const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col;
+        const T *dy = (const T *)p.dy + row_at((uint32_t)row, p.T, p.dy_ns, p.dy_ts) + col;
+        const T *z = GATE ? (const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col : nullptr;
+        float v[N], dv[N], zv[GATE ? N : 1];
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                v[k * E + i] = dv[k * E + i] = 0.f;
+                if constexpr (GATE) zv[k * E + i] = 0.f;
+            }
+            if (d < p.D) {
+                get<T, E>(x + d, v + k * E);
+                get<T, E>(dy + d, dv + k * E);
+                if constexpr (GATE) get<T, E>(z + d, zv + k * E);
+            }
+        }
+        const float rstd = normalise<N, LPG>(v, in, p.D, p.eps, p.centered);
+        const int64_t at = row * C + col;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+            float dz[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int j = k * E + i;
+                const float u = v[j] * w[j] + b[j], g = dv[j];
+                float du;
+                if constexpr (GATE) {
+                    du = g * act(p.act, zv[j]);
+                    dz[i] = g * u * act_slope(p.act, zv[j]);
+                } else {
+                    du = g * act_slope(p.act, u);
+                }
+                dw[j] += du * v[j];
+                db[j] += du;
+                dv[j] = du * w[j];  // dxh
+                s1 += dv[j];
+                s2 += dv[j] * v[j];
+            }
+            if constexpr (GATE)
+                if (d < p.D) put<T, E>((T *)p.dz + at + d, dz);
+        }
+        const float m1 = p.centered ? group_sum<LPG>(s1) * inv : 0.f, m2 = group_sum<LPG>(s2) * inv;
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+            if (d >= p.D) continue;
+            float o[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = rstd * (dv[k * E + i] - m1 - v[k * E + i] * m2);
+            put<T, E>((T *)p.dx + at + d, o);
+        }
+    }
+    if (!p.part) return;
+    // this thread's rows, for its channels: [split][2][C]
+    float *part = p.part + r0 * 2 * C + col;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+        const int d = (l + k * LPG) * E;
+        if (d >= p.D) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            part[d + i] = dw[k * E + i];
+            part[C + d + i] = db[k * E + i];
+        }
+    }
+}
+
+// dw and db: the partial sums of every split, in a fixed order.  64 channels
+// a block, its four waves a quarter of the splits each.
+__global__ void __launch_bounds__(GNT) gdp_group_norm_sum_k(const float *part, int64_t split, int64_t C, float *dw,
+                                                            float *db) {
+    __shared__ double s[4][64];
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane_id();
+    const int which = blockIdx.y;
+    float *out = which ? db : dw;
+    if (!out) return;
+    double x = 0.0;
+    if (c < C)
+        for (int64_t i = wave_id(); i < split; i += 4) x += part[(i * 2 + which) * C + c];
+    s[wave_id()][lane_id()] = x;
+    __syncthreads();
+    if (wave_id() == 0 && c < C) {
+        const int l = lane_id();
+        out[c] = (float)((s[0][l] + s[1][l]) + (s[2][l] + s[3][l]));
+    }
+}
+
+namespace {
+
+struct Shape {
+    bool vec;
+    int units, lpg, nu;
+};
+Shape shape_of(const GroupNorm &p, gdp_dtype dtype) {
+    Shape s;
+    const int e = dtype == GDP_BF16 ? 8 : 4;
+    s.vec = p.vec && p.D % e == 0;
+    s.units = s.vec ? p.D / e : p.D;
+    s.lpg = 1;
+    while (s.lpg < 64 && s.lpg < s.units) s.lpg *= 2;
+    s.nu = 1;
+    while (s.nu * s.lpg < s.units) s.nu *= 2;
+    return s;
+}
+
+template <typename T, int E, int LPG, int NU>
+hipError_t launch(const GroupNorm &p, hipStream_t stream) {
+    const int64_t blocks = (p.split * p.groups * LPG + GNT - 1) / GNT;
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    if (blocks == 0) return hipSuccess;
+    const dim3 grid((unsigned)blocks);
+    if (!p.bwd) {
+        if (p.z) hipLaunchKernelGGL((gdp_group_norm_k<T, E, LPG, NU, true>), grid, dim3(GNT), 0, stream, p);
+        else hipLaunchKernelGGL((gdp_group_norm_k<T, E, LPG, NU, false>), grid, dim3(GNT), 0, stream, p);
+    } else {
+        if (p.z) hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, true>), grid, dim3(GNT), 0, stream, p);
+        else hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, false>), grid, dim3(GNT), 0, stream, p);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int E>
+hipError_t launch_shape(const GroupNorm &p, const Shape &s, hipStream_t stream) {
+    if (s.nu == 1) {
+        switch (s.lpg) {
+        case 1: return launch<T, E, 1, 1>(p, stream);
+        case 2: return launch<T, E, 2, 1>(p, stream);
+        case 4: return launch<T, E, 4, 1>(p, stream);
+        case 8: return launch<T, E, 8, 1>(p, stream);
+        case 16: return launch<T, E, 16, 1>(p, stream);
+        case 32: return launch<T, E, 32, 1>(p, stream);
+        case 64: return launch<T, E, 64, 1>(p, stream);
+        }
+    }
+    switch (s.nu) {
+    case 2: return launch<T, E, 64, 2>(p, stream);
+    case 4: return launch<T, E, 64, 4>(p, stream);
+    case 8: return launch<T, E, 64, 8>(p, stream);
+    case 16: if constexpr (E != 8) return launch<T, E, 64, 16>(p, stream); break;
+    case 32: if constexpr (E == 1) return launch<T, E, 64, 32>(p, stream); break;
+    case 64: if constexpr (E == 1) return launch<T, E, 64, 64>(p, stream); break;
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+// Row sets that run side by side: threads of one set walk rows r0, r0 + split, ...
+int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
+    // forward: about 4 rows a thread once the card is full (2048 threads a CU);
+    // backward: as many threads as the card holds and no more, each split
+    // costing 8 bytes a channel of partial sums
+    const int64_t per_row = (int64_t)groups * D / 8 > 0 ? (int64_t)groups * D / 8 : 1;
+    const int64_t fill = (bwd ? 131072 : 524288) / per_row + 1;
+    const int64_t quarter = (rows + 3) / 4;
+    int64_t s = bwd ? fill : (quarter > fill ? quarter : fill);
+    return s < rows ? s : rows;
+}
+
+hipError_t launch_group_norm(const GroupNorm &p, gdp_dtype dtype, hipStream_t stream) {
+    const Shape s = shape_of(p, dtype);
+    hipError_t e;
+    if (dtype == GDP_BF16) e = s.vec ? launch_shape<bf16, 8>(p, s, stream) : launch_shape<bf16, 1>(p, s, stream);
+    else e = s.vec ? launch_shape<float, 4>(p, s, stream) : launch_shape<float, 1>(p, s, stream);
+    if (e != hipSuccess || !(p.dw || p.db)) return e;
+    const int64_t C = (int64_t)p.groups * p.D;
+    hipLaunchKernelGGL(gdp_group_norm_sum_k, dim3((unsigned)((C + 63) / 64), 2), dim3(GNT), 0, stream, p.part, p.split,
+                       C, p.dw, p.db);
+    return hipGetLastError();
+}
+
+}  // namespace gdp

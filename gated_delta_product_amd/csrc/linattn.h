@@ -1,0 +1,77 @@
+// linattn.h -- launcher interface of linattn.hip (host side).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdp.h"
+
+namespace gdp {
+
+// A tensor [B, T, heads, D]: element (b, t, h, d) at p + b*bs + t*ts + h*D + d;
+// value head hv reads head hv / div.
+struct LinRows {
+    const void *p = nullptr;
+    int64_t bs = 0, ts = 0;
+    int div = 1;
+};
+
+enum LinKind { LIN_SEG, LIN_OUT, LIN_DOT };
+
+// One walk (linattn.hip): y_i = sum D(i,j) (a_i.b_j) c_j over every sequence,
+// cut into segments of seg_tok rows.
+struct LinWalk {
+    LinRows a, b, c, x;
+    int da, dc;        // columns of a and b, of c (and x, y)
+    int HV;
+    int64_t B, T, nseq, seg_tok;
+    const int32_t *cu;
+    const float *g;    // log decay of (b, t, hv) at g + b*g_bs + t*g_ts + hv, or NULL
+    int64_t g_bs, g_ts;
+    bool rev;          // backwards in time
+    bool trans;        // states that are read hold element (c, a) at [a][c]
+    bool y32;          // y is float
+    float sb, sy;      // factors of the products a_i.b_j (and c_j b_j^T), and of y
+    void *y;           // [B, T, HV, dc]
+    float *rho;        // [slices, HV, B*T]
+    const float *s0;   // [nseq, HV, dc, da] or NULL: state before the first row of the walk
+    const float *seg_in;  // [slots, HV, dc, da] or NULL: state entering each segment (then s0 is not read)
+    float *s_out;      // [nseq, HV, dc, da] or NULL: state after the walk
+    float *seg_out;    // segment pass: [slots, HV, dc, da] and [slots, HV]
+    float *seg_tot;
+};
+
+struct LinScan {
+    const int32_t *cu;
+    int64_t T, nseq, seg_tok, elems, items;
+    int HV;
+    bool rev;
+    const float *s0;
+    float *seg;
+    const float *tot;
+};
+
+struct LinDg {
+    const int32_t *cu;
+    int64_t B, T, nseq, seg_tok, elems, items;
+    int HV, nq, nk;    // slices of rho_q and rho_k
+    const float *g;
+    int64_t g_bs, g_ts;
+    const float *rho_q, *rho_k;
+    const float *s_in, *r_in;         // states entering each segment, forwards and backwards
+    const float *h0, *dh0;            // [nseq, HV, V, K] (both, or neither is used)
+    bool end_zero;                    // no gradient enters behind the last row
+    float *dg;         // [B, T, HV] or NULL
+    double *part;      // [items, HV] or NULL: sums over each segment
+};
+
+int lin_slice(int da, int dc);
+hipError_t launch_lin_walk(const LinWalk &w, gdp_dtype dtype, LinKind kind, int64_t items, hipStream_t stream);
+hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream);
+hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream);
+// y [B*T, H, D] = sums over r neighbouring heads of x [B*T, H*r, D]; with cu only the tokens of its requests
+hipError_t launch_lin_group(const float *x, void *y, gdp_dtype dtype, int64_t tokens, int H, int r, int D,
+                            const int32_t *cu, int64_t nseq, hipStream_t stream);
+
+hipError_t launch_lin_decode(const gdp_linattn_decode_args &a, hipStream_t stream);
+
+}  // namespace gdp

@@ -1,0 +1,786 @@
+// linattn.hip -- linear attention with a decay for each head, chunked.
+//
+//   S_t = e^{g_t} S_{t-1} + v_t k_t^T   (V x K),     o_t = scale S_t q_t
+//
+// Unrolled over pairs, with D(i,j) = exp(sum of g over (j, i]):
+//   o_i  = scale [ D(i,start) S_0 q_i + sum_{j<=i} D(i,j) (q_i.k_j) v_j ]
+// and its gradients are the same sum with the roles of the tensors changed:
+//   dq_i = scale [ D(i,start) S_0^T do_i + sum_{j<=i} D(i,j) (do_i.v_j) k_j ]
+//   dk_j = D(end,j) dht^T v_j + scale sum_{i>=j} D(i,j) (v_j.do_i) q_i
+//   dv_j = D(end,j) dht k_j   + scale sum_{i>=j} D(i,j) (k_j.q_i) do_i
+// so one kernel, the walk below, runs them all: it takes tensors a, b (DA
+// columns) and c (DC columns), walks the rows forwards or backwards in time
+// and gives y_i = sum_j D(i,j) (a_i.b_j) c_j, keeping the state
+// S = sum D c_j b_j^T of the rows it has passed.
+//
+// A walk takes chunks of CT rows.  Per chunk, with G the inclusive cumulative
+// log decay inside it (a prefix sum in 64 bits, kept as two floats, so that
+// differences hold their bits behind a strong decay):
+//   P[i][j] = (a_i.b_j) 2^(G_i - G_j), j <= i      the masked in-chunk scores
+//   y_i     = 2^G_i S a_i + sum_j P[i][j] c_j
+//   S      <- 2^G_end S + sum_j 2^(G_end - G_j) c_j b_j^T
+// The four waves share the score tiles (through LDS) and then own a quarter
+// of the columns of c each: S^T stays in registers as result tiles of the
+// matrix core, whose lanes hold 4 consecutive rows a of a column c; the
+// columns of b are taken in the order 8g + i, 8g + 4 + i for the two tiles
+// of 32 columns, so those tiles are the operand of S a as they stand.
+#include "gdp_common.h"
+#include "gdp_internal.h"
+#include "linattn.h"
+
+namespace gdp {
+
+constexpr int LNT = 256;  // threads of a walk: four waves
+
+// ---------------------------------------------------------------- LDS tiles
+// Rows of D elements without padding; the 16-byte unit u of row r sits at
+// u ^ swz(r).  16 rows at one unit (operand rows) then fall on 16 units
+// (8 with 8 units a row, two rows to a span of all banks), and 4 rows at 4
+// neighbouring units (the transposed reads) on all banks once.
+template <int UPR>
+__device__ __forceinline__ int swz(int row) {
+    if constexpr (UPR == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    else return ((row & 3) << 2) | ((row >> 2) & 3);
+}
+template <typename T, int D>
+struct Tile {
+    static constexpr int E = 16 / sizeof(T);  // elements of a unit
+    static constexpr int UPR = D / E;
+    static __device__ __forceinline__ int at(int row, int col) {
+        return row * D + (((col / E) ^ swz<UPR>(row)) * E) + col % E;
+    }
+    // 8 elements [row][col .. col + 7], col a multiple of 8
+    static __device__ __forceinline__ typename Frag<T>::type row8(const T *t, int row, int col) {
+        if constexpr (sizeof(T) == 2) return *(const typename Frag<T>::type *)(t + at(row, col));
+        else return join<T>(*(const f32x4 *)(t + at(row, col)), *(const f32x4 *)(t + at(row, col + 4)));
+    }
+    static __device__ __forceinline__ typename Frag<T>::half row4(const T *t, int row, int col) {
+        return *(const typename Frag<T>::half *)(t + at(row, col));
+    }
+    // rows r0 .. r0 + 3 of one column per lane: lane m of 16 gets column
+    // col0 + STEP * (m / 4) + m % 4 (STEP 4: 16 neighbouring columns)
+    template <int STEP>
+    static __device__ __forceinline__ typename Frag<T>::half col4(const T *t, int r0, int col0) {
+        const int s = lane_id() & 15;
+        if constexpr (sizeof(T) == 2) {
+            const T *p = t + at(r0 + (s >> 2), col0 + STEP * (s & 3));
+            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                  (lds_i16x4 *)((__attribute__((address_space(3))) const char *)p)));
+        } else {
+            f32x4 r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = t[at(r0 + i, col0 + STEP * (s >> 2) + (s & 3))];
+            return r;
+        }
+    }
+    // the fragment of 32 rows from r0 (8 rows of lane group g at r0 + 8g)
+    template <int STEP>
+    static __device__ __forceinline__ typename Frag<T>::type col8(const T *t, int r0, int col0) {
+        const int r = r0 + 8 * (lane_id() >> 4);
+        return join<T>(col4<STEP>(t, r, col0), col4<STEP>(t, r + 4, col0));
+    }
+};
+
+// N values x[0..7] as NS parts of the storage type whose sum carries 8 NS
+// bits (bf16); for float storage one part is the value.
+template <typename T, int NS>
+__device__ __forceinline__ void split8(const float *x, typename Frag<T>::type *part) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const T h = from_f32<T>(r[i]);
+            part[p][i] = h;
+            if (p + 1 < NS) r[i] -= to_f32(h);
+        }
+}
+
+// Inclusive prefix sum of a double over the 64 lanes of a wave, on DPP moves.
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ double dpp_or_zero_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROW_MASK, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_inclusive_sum_f64(double x) {
+    x += dpp_or_zero_f64<0x111>(x);
+    x += dpp_or_zero_f64<0x112>(x);
+    x += dpp_or_zero_f64<0x114>(x);
+    x += dpp_or_zero_f64<0x118>(x);
+    x += dpp_or_zero_f64<0x142, 0xA>(x);
+    x += dpp_or_zero_f64<0x143, 0xC>(x);
+    return x;
+}
+
+// A log decay in log2 units.  Anything below -160 empties the state as far
+// as a float can tell (2^-160 is zero), and is held there so that the
+// cumulative sums stay finite (g = -inf is a reset).
+__device__ __forceinline__ double decay_log2(float g) {
+    const double x = (double)g * 1.4426950408889634;
+    return x < -160.0 ? -160.0 : x;
+}
+
+// ---------------------------------------------------------------- items
+// Sequence i owns max(1, ceil(len / seg_tok)) items (segments); an empty one
+// owns an item with no rows, which hands its state through.  Every thread of
+// the block calls it (barriers inside).
+struct LinItem {
+    int64_t seq, seg, slot0, bos, eos;  // slot0: the sequence's first item
+};
+__device__ __forceinline__ int64_t lin_segs(int64_t len, int64_t seg_tok) {
+    return len <= seg_tok ? 1 : ceil_div64(len, seg_tok);
+}
+__device__ __forceinline__ LinItem lin_item(const int32_t *cu, int64_t nseq, int64_t T, int64_t seg_tok, int64_t id) {
+    LinItem r;
+    if (cu == nullptr) {
+        const uint32_t per = (uint32_t)lin_segs(T, seg_tok);
+        const uint32_t q = (uint32_t)id / per;
+        r.seq = q;
+        r.seg = (uint32_t)id - q * per;
+        r.slot0 = (int64_t)q * per;
+        seq_bounds(nullptr, T, r.seq, r.bos, r.eos);
+        return r;
+    }
+    __shared__ int64_t s_item[3];
+    if (wave_id() == 0) {
+        const int lane = lane_id();
+        if (lane == 0) s_item[0] = -1;
+        int64_t carry = 0;
+        for (int64_t i0 = 0; i0 < nseq && carry <= id; i0 += 64) {
+            const int64_t i = i0 + lane;
+            int64_t n = 0;
+            if (i < nseq) {
+                int64_t b, e;
+                seq_bounds(cu, T, i, b, e);
+                n = lin_segs(e - b, seg_tok);
+            }
+            const int64_t incl = carry + wave_inclusive_sum_i64(n);
+            const int64_t excl = incl - n;
+            if (i < nseq && id >= excl && id < incl) {  // at most one lane
+                s_item[0] = i;
+                s_item[1] = id - excl;
+                s_item[2] = excl;
+            }
+            carry = __shfl(incl, 63, 64);
+        }
+    }
+    __syncthreads();
+    r.seq = uniform_i64(s_item[0]);
+    r.seg = uniform_i64(s_item[1]);
+    r.slot0 = uniform_i64(s_item[2]);
+    r.bos = r.eos = 0;
+    if (r.seq >= 0) seq_bounds(cu, T, r.seq, r.bos, r.eos);
+    __syncthreads();
+    return r;
+}
+
+// ---------------------------------------------------------------- the walk
+// OUT: rows y are computed (else only the state: the segment pass).
+// DOT: also rho_i = x_i . (y_i without its own row's term), from unrounded
+//      values: the part of the row that the decays scale.
+// NS:  bf16 parts of the decayed c in the state update (16 or 24 bits).
+// NQ:  parts of the state in S a.
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+struct Walk {
+    static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr int CT = F32 ? 32 : 64;     // rows of a chunk
+    static constexpr int NB = CT / 16;           // 16-row blocks
+    static constexpr int TB = CT / 32;           // 32-row blocks
+    static constexpr int KT = DA / 16;           // 16-row tiles of S^T
+    static constexpr int NW = DC / 64;           // 16-column tiles of a wave
+    static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / LNT, UC = CT * DC * (int)sizeof(T) / 16 / LNT;
+    typedef Tile<T, DA> TA;
+    typedef Tile<T, DC> TC;
+    typedef Tile<T, CT> TP;
+    typedef typename Frag<T>::type frag;
+
+    struct Lds {
+        T b[CT * DA];
+        T c[CT * DC];
+        T a[OUT ? CT * DA : 8];
+        T x[DOT ? CT * DC : 8];
+        T p[OUT ? CT * CT : 8];
+        float gh[2][CT], gl[2][CT];  // G as two floats
+        float eg[2][CT], wg[2][CT];  // 2^G_i and sb 2^(G_end - G_i)
+        float rho[DOT ? 4 * CT : 4];
+    };
+};
+
+template <typename T, int D, int UNITS>
+__device__ __forceinline__ void rows_to_regs(uint4 (&r)[UNITS], const T *base, int32_t ts, int n, bool rev) {
+    constexpr int E = 16 / sizeof(T), UPR = D / E;
+#pragma unroll
+    for (int it = 0; it < UNITS; ++it) {
+        const int u = threadIdx.x + LNT * it, row = u / UPR, col = u % UPR * E;
+        r[it] = make_uint4(0, 0, 0, 0);
+        if (row < n) r[it] = *(const uint4 *)(base + ((rev ? n - 1 - row : row) * ts + col));
+    }
+}
+template <typename T, int D, int UNITS>
+__device__ __forceinline__ void regs_to_tile(T *t, const uint4 (&r)[UNITS]) {
+    constexpr int E = 16 / sizeof(T), UPR = D / E;
+#pragma unroll
+    for (int it = 0; it < UNITS; ++it) {
+        const int u = threadIdx.x + LNT * it;
+        *(uint4 *)(t + Tile<T, D>::at(u / UPR, u % UPR * E)) = r[it];
+    }
+}
+
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+__device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, int slice,
+                                         typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds &sm) {
+    typedef Walk<T, DA, DC, NS, NQ, OUT, DOT> W;
+    typedef typename W::frag frag;
+    typedef typename W::TA TA;
+    typedef typename W::TC TC;
+    typedef typename W::TP TP;
+    constexpr int CT = W::CT;
+    const int lane = lane_id(), wave = wave_id(), m = lane & 15, g4 = lane >> 4;
+
+    const LinItem it = lin_item(w.cu, w.nseq, w.T, w.seg_tok, id);
+    if (it.seq < 0) return;
+    const int64_t t0 = it.bos + it.seg * w.seg_tok;
+    const int64_t t1 = t0 + w.seg_tok < it.eos ? t0 + w.seg_tok : it.eos;
+    const bool at_end = w.rev ? it.seg == 0 : t1 == it.eos;  // the walk's last segment of the sequence
+    if (!OUT && at_end) return;  // no segment is entered from it
+    const int64_t len = t1 - t0;
+    // batch row and the token offset inside it (packed rows are one batch row)
+    const int64_t bi = w.cu ? 0 : it.seq, tb0 = w.cu ? t0 : t0 - it.bos;
+    const int64_t eos_in = w.cu ? it.eos : w.T;
+
+    const T *pa = (const T *)w.a.p + bi * w.a.bs + (int64_t)(hv / w.a.div) * DA;
+    const T *pb = (const T *)w.b.p + bi * w.b.bs + (int64_t)(hv / w.b.div) * DA;
+    const T *pc = (const T *)w.c.p + bi * w.c.bs + (int64_t)(hv / w.c.div) * w.dc + slice * DC;
+    const T *px = DOT ? (const T *)w.x.p + bi * w.x.bs + (int64_t)(hv / w.x.div) * w.dc + slice * DC : nullptr;
+    const float *pg = w.g ? w.g + bi * w.g_bs + hv : nullptr;
+
+    // entering state: S^T tiles [kt][nw], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c = m
+    f32x4 s[W::KT][W::NW];
+    const int c0w = (wave * W::NW) * 16 + m;  // first column of this lane
+    {
+        const float *s0 = nullptr;
+        if (w.seg_in)
+            s0 = w.seg_in + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
+        else if (OUT && w.s0) s0 = w.s0 + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
+#pragma unroll
+        for (int kt = 0; kt < W::KT; ++kt)
+#pragma unroll
+            for (int nw = 0; nw < W::NW; ++nw) {
+                s[kt][nw] = zero4();
+                if (!s0) continue;
+                const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2), c = slice * DC + c0w + 16 * nw;
+                if (w.trans) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[kt][nw][i] = s0[(int64_t)(a + i) * w.dc + c];
+                } else {
+                    s[kt][nw] = *(const f32x4 *)(s0 + (int64_t)c * DA + a);
+                }
+            }
+    }
+
+    uint4 ra[OUT ? W::UA : 1], rb[W::UA], rc[W::UC], rx[DOT ? W::UC : 1];
+    float rg = 0.f;
+    // rows [c0, c0 + n) of the walk into registers (g: one row a lane of every wave)
+    auto fetch = [&](int64_t c0, int n) {
+        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
+        if constexpr (OUT) rows_to_regs<T, DA>(ra, pa + first * w.a.ts, (int32_t)w.a.ts, n, w.rev);
+        rows_to_regs<T, DA>(rb, pb + first * w.b.ts, (int32_t)w.b.ts, n, w.rev);
+        rows_to_regs<T, DC>(rc, pc + first * w.c.ts, (int32_t)w.c.ts, n, w.rev);
+        if constexpr (DOT) rows_to_regs<T, DC>(rx, px + first * w.x.ts, (int32_t)w.x.ts, n, w.rev);
+        rg = 0.f;
+        if (pg && lane < n) {
+            // backwards, a row is entered through the decay of the row after it
+            const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
+            if (t < eos_in) rg = pg[t * w.g_ts];
+        }
+    };
+    float tot = 0.f;  // log2 decay of the whole walk (wave 0), for the segment pass
+    auto decays = [&](int n, int buf) {
+        if (wave != 0) return;
+        const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(rg) : 0.0);
+        const double Gend = __shfl(G, 63, 64);
+        tot += (float)Gend;
+        if (lane < CT) {
+            const float hi = (float)G;
+            sm.gh[buf][lane] = hi;
+            sm.gl[buf][lane] = (float)(G - (double)hi);
+            sm.eg[buf][lane] = __builtin_amdgcn_exp2f((float)G);
+            sm.wg[buf][lane] = w.sb * __builtin_amdgcn_exp2f((float)(Gend - G));
+        }
+    };
+    // tiles above the diagonal of P stay zero (a 32-row contraction of an even block reads one)
+    if constexpr (OUT) {
+        for (int i = threadIdx.x; i < CT * CT; i += LNT) sm.p[i] = from_f32<T>(0.f);
+    }
+
+    const int64_t nch = ceil_div64(len, CT);
+    if (nch > 0) {
+        const int n = len < CT ? (int)len : CT;
+        fetch(0, n);
+        decays(n, 0);
+    }
+    for (int64_t ch = 0; ch < nch; ++ch) {
+        const int64_t c0 = ch * CT;
+        const int n = len - c0 < CT ? (int)(len - c0) : CT;
+        const int n1 = len - c0 - CT < CT ? (int)(len - c0 - CT) : CT;  // rows of the next chunk
+        const int buf = (int)(ch & 1);
+        if constexpr (OUT) regs_to_tile<T, DA>(sm.a, ra);
+        regs_to_tile<T, DA>(sm.b, rb);
+        regs_to_tile<T, DC>(sm.c, rc);
+        if constexpr (DOT) regs_to_tile<T, DC>(sm.x, rx);
+        __syncthreads();
+        if (ch + 1 < nch) fetch(c0 + CT, n1);
+
+        f32x4 y[W::NB][W::NW];
+        if constexpr (OUT) {
+            // S a: S^T tiles as the operand, rounded to NQ parts
+#pragma unroll
+            for (int ib = 0; ib < W::NB; ++ib)
+#pragma unroll
+                for (int nw = 0; nw < W::NW; ++nw) y[ib][nw] = zero4();
+#pragma unroll
+            for (int kb = 0; kb < DA / 32; ++kb) {
+                frag sp[W::NW][NQ];
+#pragma unroll
+                for (int nw = 0; nw < W::NW; ++nw) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = s[2 * kb + i / 4][nw][i % 4];
+                    split8<T, NQ>(v, sp[nw]);
+                }
+#pragma unroll
+                for (int ib = 0; ib < W::NB; ++ib) {
+                    const frag fa = TA::row8(sm.a, 16 * ib + m, 32 * kb + 8 * g4);
+#pragma unroll
+                    for (int nw = 0; nw < W::NW; ++nw)
+#pragma unroll
+                        for (int p = NQ - 1; p >= 0; --p) y[ib][nw] = mma(sp[nw][p], fa, y[ib][nw]);
+                }
+            }
+            float rho[W::NB];
+#pragma unroll
+            for (int ib = 0; ib < W::NB; ++ib) {
+                const float e = sm.eg[buf][16 * ib + m];
+                rho[ib] = 0.f;
+#pragma unroll
+                for (int nw = 0; nw < W::NW; ++nw) {
+                    y[ib][nw] *= e;
+                    if constexpr (DOT) {
+                        const auto xv = TC::row4(sm.x, 16 * ib + m, (wave * W::NW + nw) * 16 + 4 * g4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) rho[ib] += to_f32(xv[i]) * y[ib][nw][i];
+                    }
+                }
+            }
+            if constexpr (DOT) {
+#pragma unroll
+                for (int ib = 0; ib < W::NB; ++ib) {
+                    rho[ib] = xor32_sum(xor16_sum(rho[ib]));
+                    if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] = rho[ib];
+                }
+            }
+            // score tiles at and below the diagonal, four at a time: P^T (rows j, columns i)
+#pragma unroll
+            for (int k = 0; k < (W::NB * (W::NB + 1) / 2 + 3) / 4; ++k) {
+                const int t = 4 * k + wave;
+                if (t >= W::NB * (W::NB + 1) / 2) break;
+                const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
+                f32x4 acc = zero4();
+#pragma unroll
+                for (int kb = 0; kb < DA / 32; ++kb)
+                    acc = mma(TA::row8(sm.b, 16 * jb + m, 32 * kb + 8 * g4),
+                              TA::row8(sm.a, 16 * ib + m, 32 * kb + 8 * g4), acc);
+                const int i = 16 * ib + m, j0 = 16 * jb + 4 * g4;
+                const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
+                const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
+                typename Frag<T>::half pv;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r]));
+                    acc[r] = j0 + r <= i ? acc[r] * (d * w.sb) : 0.f;
+                    pv[r] = from_f32<T>(acc[r]);
+                }
+                *(typename Frag<T>::half *)(sm.p + TP::at(i, j0)) = pv;
+                if constexpr (DOT) {
+                    f32x4 e = zero4();
+#pragma unroll
+                    for (int kb = 0; kb < DC / 32; ++kb)
+                        e = mma(TC::row8(sm.c, 16 * jb + m, 32 * kb + 8 * g4),
+                                TC::row8(sm.x, 16 * ib + m, 32 * kb + 8 * g4), e);
+                    float q = 0.f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) q += j0 + r < i ? acc[r] * e[r] : 0.f;
+                    q = xor32_sum(xor16_sum(q));
+                    if (g4 == 0) sm.rho[wave * CT + i] += q;
+                }
+            }
+            lds_barrier();
+        }
+
+        // the rows c as operands, once for P c and (decayed) for the state
+#pragma unroll
+        for (int kt = 0; kt < W::KT; ++kt)
+#pragma unroll
+            for (int nw = 0; nw < W::NW; ++nw) s[kt][nw] *= sm.eg[buf][CT - 1];
+#pragma unroll
+        for (int tb = 0; tb < W::TB; ++tb) {
+            frag fc[W::NW], fw[W::NW][NS];
+#pragma unroll
+            for (int nw = 0; nw < W::NW; ++nw) {
+                fc[nw] = TC::template col8<4>(sm.c, 32 * tb, (wave * W::NW + nw) * 16);
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = to_f32(fc[nw][i]) * sm.wg[buf][32 * tb + 8 * g4 + i];
+                split8<T, NS>(v, fw[nw]);
+            }
+            if constexpr (OUT) {
+#pragma unroll
+                for (int ib = 2 * tb; ib < W::NB; ++ib) {
+                    const frag fp = TP::row8(sm.p, 16 * ib + m, 32 * tb + 8 * g4);
+#pragma unroll
+                    for (int nw = 0; nw < W::NW; ++nw) y[ib][nw] = mma(fc[nw], fp, y[ib][nw]);
+                }
+            }
+#pragma unroll
+            for (int kt = 0; kt < W::KT; ++kt) {
+                const frag fb = TA::template col8<8>(sm.b, 32 * tb, 32 * (kt / 2) + 4 * (kt % 2));
+#pragma unroll
+                for (int nw = 0; nw < W::NW; ++nw)
+#pragma unroll
+                    for (int p = NS - 1; p >= 0; --p) s[kt][nw] = mma(fb, fw[nw][p], s[kt][nw]);
+            }
+        }
+        if (ch + 1 < nch) decays(n1, buf ^ 1);
+        if constexpr (OUT) {
+#pragma unroll
+            for (int ib = 0; ib < W::NB; ++ib) {
+                const int row = 16 * ib + m;
+                if (row >= n) continue;
+                const int64_t t = w.rev ? tb0 + len - 1 - c0 - row : tb0 + c0 + row;
+                const int64_t e = ((bi * w.T + t) * w.HV + hv) * (int64_t)w.dc + slice * DC + (wave * W::NW) * 16 + 4 * g4;
+#pragma unroll
+                for (int nw = 0; nw < W::NW; ++nw) {
+                    const f32x4 v = y[ib][nw] * w.sy;
+                    if (w.y32) {
+                        *(f32x4 *)((float *)w.y + e + 16 * nw) = v;
+                    } else {
+                        typename Frag<T>::half o;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(v[i]);
+                        *(typename Frag<T>::half *)((T *)w.y + e + 16 * nw) = o;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (DOT) {
+            if (wave == 0 && lane < n) {
+                float q = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q += sm.rho[i * CT + lane];
+                const int64_t t = w.rev ? tb0 + len - 1 - c0 - lane : tb0 + c0 + lane;
+                w.rho[((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + t] = q * w.sy;
+            }
+        }
+    }
+
+    // the state after the walk: the segment's own (segment pass), or the sequence's
+    float *so = nullptr;
+    float f = 1.f;
+    if constexpr (!OUT) {
+        so = w.seg_out + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
+        if (threadIdx.x == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = tot;
+    } else if (at_end && w.s_out) {
+        so = w.s_out + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
+        if (w.rev && pg && it.eos > it.bos)  // through the first row's decay too
+            f = __builtin_amdgcn_exp2f((float)decay_log2(pg[(w.cu ? it.bos : 0) * w.g_ts]));
+    }
+    if (!so) return;
+#pragma unroll
+    for (int kt = 0; kt < W::KT; ++kt)
+#pragma unroll
+        for (int nw = 0; nw < W::NW; ++nw) {
+            const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2), c = slice * DC + c0w + 16 * nw;
+            *(f32x4 *)(so + (int64_t)c * DA + a) = s[kt][nw] * f;
+        }
+}
+
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+__global__ void __launch_bounds__(LNT, DA == 256 && OUT ? 1 : 2) gdp_lin_walk_k(LinWalk w) {
+    __shared__ __align__(16) typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds sm;
+    const int slices = w.dc / DC;
+    const uint32_t b = blockIdx.x, per = (uint32_t)w.HV * slices;
+    const uint32_t id = b / per, r = b - id * per;
+    lin_walk<T, DA, DC, NS, NQ, OUT, DOT>(w, id, (int)(r / slices), (int)(r % slices), sm);
+}
+
+// ---------------------------------------------------------------- the scan over segments
+// Each sequence's segments in walk order: entering state of the first is h0
+// (or zero), then S <- 2^tot S + E.  The E of a segment is replaced by the
+// state entering it.  One thread per 4 state elements.
+__global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
+    const int64_t seq = blockIdx.x / p.HV;
+    const int hv = (int)(blockIdx.x % p.HV);
+    int64_t bos, eos, slot0;
+    seq_bounds(p.cu, p.T, seq, bos, eos);
+    if (p.cu == nullptr) {
+        slot0 = seq * lin_segs(p.T, p.seg_tok);
+    } else {
+        __shared__ int64_t s_part[4];
+        int64_t acc = 0;
+        for (int64_t j = threadIdx.x; j < seq; j += 256) {
+            int64_t b, e;
+            seq_bounds(p.cu, p.T, j, b, e);
+            acc += lin_segs(e - b, p.seg_tok);
+        }
+        acc = wave_sum_i64(acc);
+        if (lane_id() == 0) s_part[threadIdx.x >> 6] = acc;
+        __syncthreads();
+        slot0 = s_part[0] + s_part[1] + s_part[2] + s_part[3];
+    }
+    const int64_t nseg = lin_segs(eos - bos, p.seg_tok);
+    if (slot0 + nseg > p.items) return;  // overlapping requests: out of slots
+    const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (i >= p.elems) return;
+    const int64_t step = p.HV * p.elems;
+    f32x4 cur = zero4();
+    if (p.s0) cur = *(const f32x4 *)(p.s0 + (seq * p.HV + hv) * p.elems + i);
+    const int64_t last = nseg - 1;
+    float *base = p.seg + (slot0 * p.HV + hv) * p.elems + i;
+    const float *tot = p.tot + slot0 * p.HV + hv;
+    constexpr int U = 8;  // segments in flight
+    for (int64_t k0 = 0; k0 < nseg; k0 += U) {
+        f32x4 e[U];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u, sg = p.rev ? nseg - 1 - k : k;
+            e[u] = zero4();
+            f[u] = 1.f;
+            if (k < last) {
+                e[u] = *(const f32x4 *)(base + sg * step);
+                f[u] = __builtin_amdgcn_exp2f(tot[sg * p.HV]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u, sg = p.rev ? nseg - 1 - k : k;
+            if (k >= nseg) break;
+            *(f32x4 *)(base + sg * step) = cur;
+            cur = cur * f[u] + e[u];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient of the decays
+// dg_t is the sum of D(i,j) scale (q_i.k_j)(do_i.v_j) over the pairs i >= t > j
+// (the initial state an earlier row, the final state's gradient a later one),
+// so  dg_t - dg_{t+1} = rho_q[t] - rho_k[t]:  what row t takes from earlier rows
+// less what it gives to later ones.  Each segment is anchored at one border,
+// where the sum is the product of the state and the gradient that meet there,
+// so the running sums (64 bits) stay as short as a segment.
+__global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
+    const uint32_t b = blockIdx.x;
+    const int64_t id = b / (uint32_t)p.HV;
+    const int hv = (int)(b % (uint32_t)p.HV);
+    __shared__ double s_red[4];
+    __shared__ double s_carry;
+    const LinItem it = lin_item(p.cu, p.nseq, p.T, p.seg_tok, id);
+    if (it.seq < 0) {
+        if (p.part && threadIdx.x == 0) p.part[id * p.HV + hv] = 0.0;
+        return;
+    }
+    const int64_t t0 = it.bos + it.seg * p.seg_tok;
+    const int64_t t1 = t0 + p.seg_tok < it.eos ? t0 + p.seg_tok : it.eos;
+    const int64_t bi = p.cu ? 0 : it.seq, tb0 = p.cu ? t0 : t0 - it.bos, tb1 = tb0 + (t1 - t0);
+    // the anchor: at the segment's end (the state after it is the one entering
+    // the next segment), for the last segment at its start unless nothing
+    // comes in behind it
+    const bool last = t1 == it.eos, fwd = last && !p.end_zero;
+    const int64_t own = ((it.slot0 + it.seg) * p.HV + hv) * p.elems, step = p.HV * p.elems;
+    const float *S = nullptr, *R = nullptr;
+    int64_t through = -1;  // the row whose decay lies on the border
+    if (!last && id + 1 < p.items) {
+        S = p.s_in + own + step;
+        R = p.r_in + own;
+        through = tb1;
+    } else if (fwd && it.seg > 0) {
+        S = p.s_in + own;
+        R = p.r_in + own - step;
+        through = tb0;
+    } else if (fwd && p.h0) {  // dh0 has the first row's decay in it
+        S = p.h0 + (it.seq * p.HV + hv) * p.elems;
+        R = p.dh0 + (it.seq * p.HV + hv) * p.elems;
+    }
+    double x = 0.0;
+    if (S) {
+        float acc = 0.f;
+        for (int64_t i = threadIdx.x * 4; i < p.elems; i += 1024) {
+            const f32x4 u = *(const f32x4 *)(S + i), v = *(const f32x4 *)(R + i);
+            acc += (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
+        }
+        x = acc;
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+    }
+    if (lane_id() == 0) s_red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double c = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+        if (through >= 0 && p.g) c *= exp2(decay_log2(p.g[bi * p.g_bs + through * p.g_ts + hv]));
+        s_carry = c;
+    }
+    __syncthreads();
+    // the rows from the anchored border, 256 at a time
+    double sum = 0.0;
+    const int64_t BT = p.B * p.T;
+    for (int64_t k0 = 0; k0 < tb1 - tb0; k0 += 256) {
+        const int64_t k = k0 + threadIdx.x, t = fwd ? tb0 + k : tb1 - 1 - k;
+        const bool in = k < tb1 - tb0;
+        double d = 0.0;
+        if (in) {
+            const int64_t at = (int64_t)hv * BT + bi * p.T + t;
+            for (int i = 0; i < p.nq; ++i) d += (double)p.rho_q[at + (int64_t)i * p.HV * BT];
+            for (int i = 0; i < p.nk; ++i) d -= (double)p.rho_k[at + (int64_t)i * p.HV * BT];
+            if (fwd) d = -d;
+        }
+        const double incl = wave_inclusive_sum_f64(d);
+        const double tot = __shfl(incl, 63, 64);
+        if (lane_id() == 0) s_red[threadIdx.x >> 6] = tot;
+        __syncthreads();
+        double upto = s_carry + incl;
+        for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) upto += s_red[i];
+        const double v = fwd ? upto - d : upto;
+        if (in) {
+            if (p.dg) p.dg[(bi * p.T + t) * p.HV + hv] = (float)v;
+            sum += v;
+        }
+        __syncthreads();
+        if (threadIdx.x == 255) s_carry = upto;
+        __syncthreads();
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+    if (lane_id() == 0) s_red[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) p.part[id * p.HV + hv] = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+}
+
+// dg of a decay per head: the sum over every segment, in a fixed order
+__global__ void __launch_bounds__(256) gdp_lin_dg_head_k(const double *part, int64_t items, int HV, float *out) {
+    __shared__ double s_red[4];
+    const int hv = blockIdx.x;
+    double x = 0.0;
+    for (int64_t i = threadIdx.x; i < items; i += 256) x += part[i * HV + hv];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+    if (lane_id() == 0) s_red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) out[hv] = (float)((s_red[0] + s_red[1]) + (s_red[2] + s_red[3]));
+}
+
+// Gradients of shared key heads: the sum of r neighbouring heads' float rows,
+// rounded once.  One thread per 4 elements; tokens outside every request are
+// left alone (requests follow each other, so those lie before the first
+// offset or behind the last).
+template <typename T>
+__global__ void __launch_bounds__(256) gdp_lin_group_k(const float *x, T *y, int64_t units, int H, int r, int upr,
+                                                       const int32_t *cu, int64_t nseq) {
+    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (u >= units) return;
+    const int64_t row = u / upr;  // (token, key head)
+    if (cu) {
+        const int64_t t = row / H;
+        if (t < cu[0] || t >= cu[nseq]) return;
+    }
+    const float *p = x + (row * r * upr + u % upr) * 4;
+    f32x4 s = *(const f32x4 *)p;
+    for (int i = 1; i < r; ++i) s += *(const f32x4 *)(p + (int64_t)i * upr * 4);
+    typename Frag<T>::half o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(s[i]);
+    *(typename Frag<T>::half *)(y + u * 4) = o;
+}
+
+// ---------------------------------------------------------------- launches
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+static hipError_t launch_walk_t(const LinWalk &w, int64_t items, hipStream_t stream) {
+    const int64_t blocks = items * w.HV * (w.dc / DC);
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, NQ, OUT, DOT>), dim3((unsigned)blocks), dim3(LNT), 0, stream, w);
+    return hipGetLastError();
+}
+
+// Columns of c that one walk takes: the state of a walk is at most 128 x 128.
+int lin_slice(int da, int dc) {
+    const int most = da == 256 ? 64 : 128;
+    return dc < most ? dc : most;
+}
+
+template <typename T, int NS, int NQ, bool OUT, bool DOT>
+static hipError_t launch_walk_dims(const LinWalk &w, int64_t items, hipStream_t stream) {
+    switch (w.da * 1000 + lin_slice(w.da, w.dc)) {
+    case 64064: return launch_walk_t<T, 64, 64, NS, NQ, OUT, DOT>(w, items, stream);
+    case 64128: return launch_walk_t<T, 64, 128, NS, NQ, OUT, DOT>(w, items, stream);
+    case 128064: return launch_walk_t<T, 128, 64, NS, NQ, OUT, DOT>(w, items, stream);
+    case 128128: return launch_walk_t<T, 128, 128, NS, NQ, OUT, DOT>(w, items, stream);
+    case 256064: return launch_walk_t<T, 256, 64, NS, NQ, OUT, DOT>(w, items, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_lin_walk(const LinWalk &w, gdp_dtype dtype, LinKind kind, int64_t items, hipStream_t stream) {
+    if (items == 0) return hipSuccess;
+    if (dtype == GDP_F32) {
+        switch (kind) {
+        case LIN_SEG: return launch_walk_dims<float, 1, 1, false, false>(w, items, stream);
+        case LIN_OUT: return launch_walk_dims<float, 1, 1, true, false>(w, items, stream);
+        case LIN_DOT: return launch_walk_dims<float, 1, 1, true, true>(w, items, stream);
+        }
+    }
+    switch (kind) {
+    case LIN_SEG: return launch_walk_dims<bf16, 3, 1, false, false>(w, items, stream);
+    case LIN_OUT: return launch_walk_dims<bf16, 3, 1, true, false>(w, items, stream);
+    case LIN_DOT: return launch_walk_dims<bf16, 3, 3, true, true>(w, items, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
+    if (p.nseq == 0) return hipSuccess;
+    hipLaunchKernelGGL(gdp_lin_scan_k, dim3((unsigned)(p.nseq * p.HV), (unsigned)(p.elems / 1024)), dim3(256), 0,
+                       stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream) {
+    if (p.items > 0) {
+        hipLaunchKernelGGL(gdp_lin_dg_k, dim3((unsigned)(p.items * p.HV)), dim3(256), 0, stream, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (!dg_head) return hipSuccess;
+    hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items, p.HV, dg_head);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_group(const float *x, void *y, gdp_dtype dtype, int64_t tokens, int H, int r, int D,
+                            const int32_t *cu, int64_t nseq, hipStream_t stream) {
+    const int64_t units = tokens * H * (D / 4);
+    if (units == 0) return hipSuccess;
+    const dim3 grid((unsigned)((units + 255) / 256));
+    if (dtype == GDP_BF16)
+        hipLaunchKernelGGL(gdp_lin_group_k<bf16>, grid, dim3(256), 0, stream, x, (bf16 *)y, units, H, r, D / 4, cu,
+                           nseq);
+    else
+        hipLaunchKernelGGL(gdp_lin_group_k<float>, grid, dim3(256), 0, stream, x, (float *)y, units, H, r, D / 4,
+                           cu, nseq);
+    return hipGetLastError();
+}
+
+}  // namespace gdp

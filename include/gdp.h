@@ -34,6 +34,13 @@
  *                        state read from and written back to a state pool
  *                        (the fused recurrent update the prepare page names
  *                        as the decode consumer)
+ *   gdp_linattn_fwd      linear attention with a decay for each head (the
+ *                        recurrence without the delta correction), chunked
+ *   gdp_linattn_bwd      its gradients
+ *   gdp_linattn_decode   its recurrent form over a state pool
+ *   gdp_group_norm_fwd   the norm per head with an activation or a gate that
+ *                        follows either mixer, channels last
+ *   gdp_group_norm_bwd   its gradients
  *
  * Conventions shared by every entry point
  *   * All tensor pointers are device pointers owned by the caller.  No call
@@ -512,6 +519,205 @@ int32_t gdp_pipeline_plan(int64_t T, int32_t num_segments, int64_t *starts);
  */
 int64_t gdp_num_state_chunks(const int32_t *cu_seqlens_host, int64_t num_seqs,
                              int64_t B, int64_t T, int32_t M, int32_t chunk_size);
+
+/*
+ * Linear attention with a decay for each head:
+ *   S_t = exp(g_t) S_{t-1} + v_t k_t^T   (V x K),     o_t = scale S_t q_t
+ * over the sequences of gdp_chunk_args: B rows of T tokens, or (B == 1) the
+ * packed requests of cu_seqlens; H key heads, HV value heads (HV % H == 0),
+ * value head hv reading key head hv / (HV/H).  There is no L2 norm.
+ *   q, k   [B, T, H,  K]  dtype; element (b, t, h, i) at
+ *                         q + b*q_b_stride + t*q_t_stride + h*K + i (strides
+ *                         in elements, >= 0; rows 16-byte aligned), so slices
+ *                         of a wider projection can be passed as they are
+ *   v      [B, T, HV, V]  dtype, strided likewise
+ *   g      float32 natural-log decay of (b, t, hv) at g + b*g_b_stride +
+ *          t*g_t_stride + hv, or NULL.  -inf empties the state; below -110
+ *          a decay counts as -110 (its power is zero in float32 already).
+ *   g_head [HV] float32, a decay per head for every token, or NULL.  At most
+ *          one of g and g_head is given; neither: no decay.
+ *   h0     [nseq, HV, V, K] float32 state before each sequence, or NULL (0)
+ *   o      [B, T, HV, V] dtype, contiguous; tokens outside every request are
+ *          left as they were
+ *   ht     [nseq, HV, V, K] float32 state after each sequence, or NULL (h0,
+ *          or zero, for an empty one).  May be h0.
+ *   scale  <= 0 selects 1/sqrt(K).
+ * Inputs must be finite (an infinity or a NaN may reach every row of its
+ * 64-token chunk and the rows after it).
+ * Sizes: K in {64, 128}, V in {64, 128, 256}, both dtypes; HV <= 65535.
+ */
+typedef struct gdp_linattn_args {
+    int64_t B;
+    int64_t T;
+    int32_t H;
+    int32_t HV;
+    int32_t K;
+    int32_t V;
+    float scale;
+    gdp_dtype dtype;
+    const int32_t *cu_seqlens;
+    int64_t num_seqs;
+    const void *q;
+    int64_t q_b_stride;
+    int64_t q_t_stride;
+    const void *k;
+    int64_t k_b_stride;
+    int64_t k_t_stride;
+    const void *v;
+    int64_t v_b_stride;
+    int64_t v_t_stride;
+    const float *g;
+    int64_t g_b_stride;
+    int64_t g_t_stride;
+    const float *g_head;
+    const float *h0;
+    void *o;
+    float *ht;
+} gdp_linattn_args;
+
+/* Gradients of gdp_linattn_fwd.  dout [B, T, HV, V] dtype (strided like v) and
+ * dht (float32 [nseq, HV, V, K], or NULL: zero) are those of o and ht; every
+ * output is contiguous:
+ *   dq, dk   [B, T, H, K] dtype, summed over the value heads of a key head
+ *   dv       [B, T, HV, V] dtype
+ *   dg       [B, T, HV] float32, the gradient of g, or NULL
+ *   dg_head  [HV] float32, the gradient of g_head, or NULL
+ *   dh0      [nseq, HV, V, K] float32, the gradient of h0, or NULL
+ * Rows of tokens outside every request are left as they were. */
+typedef struct gdp_linattn_grads {
+    const void *dout;
+    int64_t do_b_stride;
+    int64_t do_t_stride;
+    const float *dht;
+    void *dq;
+    void *dk;
+    void *dv;
+    float *dg;
+    float *dg_head;
+    float *dh0;
+} gdp_linattn_grads;
+
+/* Device workspace in bytes that gdp_linattn_fwd (backward == 0) or
+ * gdp_linattn_bwd (backward != 0) needs for the sizes and pointers of a; 0:
+ * none.  -1 on bad arguments.  Only the sizes, num_seqs and whether cu_seqlens
+ * and h0 are NULL count, so it can be asked before the tensors exist. */
+int64_t gdp_linattn_workspace_bytes(const gdp_linattn_args *a, int32_t backward);
+
+/* o and ht.  Long sequences are cut into segments that run in parallel: each
+ * segment's own state first, then a scan over the segments, then the rows.
+ * workspace: gdp_linattn_workspace_bytes bytes, 256-byte aligned, caller-owned
+ * (its contents do not matter and are not kept). */
+gdp_status gdp_linattn_fwd(const gdp_linattn_args *a, void *workspace, int64_t workspace_bytes, void *stream);
+/* dq, dk, dv and whichever of dg, dg_head and dh0 are given, from q, k, v, g,
+ * h0 of a (o and ht are not read) and dout, dht. */
+gdp_status gdp_linattn_bwd(const gdp_linattn_args *a, const gdp_linattn_grads *d, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/*
+ * gdp_linattn_decode -- S new tokens (1 plus the draft length) of each of n
+ * requests through the same recurrence, the state of a request in its slot of
+ * a pool:
+ *   q, k   [n, S, H, K]  dtype;  v [n, S, HV, V] dtype (strides as above)
+ *   g      float32 [n, S, HV], strided, or NULL;  g_head [HV], or NULL
+ *   state  [pool, HV, V, K] float32, read and written in place
+ *   slots  int32 [n] device: the state slot of each request, or NULL (slot i
+ *          for request i).  A slot outside [0, pool) -- e.g. -1 for a padding
+ *          entry -- skips the request: no state is touched and its o rows are
+ *          zero.  Slots of one call must be distinct.
+ *   o      [n, S, HV, V] dtype, contiguous
+ *   scale  <= 0 selects 1/sqrt(K).
+ * Sizes as gdp_linattn_fwd, S <= 4096, n * V < 2^31.
+ */
+typedef struct gdp_linattn_decode_args {
+    int64_t n;
+    int64_t S;
+    int32_t H;
+    int32_t HV;
+    int32_t K;
+    int32_t V;
+    float scale;
+    gdp_dtype dtype;
+    int64_t pool;
+    const void *q;
+    int64_t q_n_stride;
+    int64_t q_t_stride;
+    const void *k;
+    int64_t k_n_stride;
+    int64_t k_t_stride;
+    const void *v;
+    int64_t v_n_stride;
+    int64_t v_t_stride;
+    const float *g;
+    int64_t g_n_stride;
+    int64_t g_t_stride;
+    const float *g_head;
+    float *state;
+    const int32_t *slots;
+    void *o;
+} gdp_linattn_decode_args;
+
+gdp_status gdp_linattn_decode(const gdp_linattn_decode_args *a, void *stream);
+
+/*
+ * Group norm with an activation, channels last: every token is a sample, and
+ * its C = groups * D channels are normalised in groups of D neighbours (the
+ * heads of a mixer's output [n, T, HV, V] with groups = HV, D = V).
+ *   xh = (x - mean) / sqrt(var + eps)  per group, var the mean of the squared
+ *        differences; centered == 0: x / sqrt(mean of x^2 + eps)
+ *   y  = (xh w + b) act(z)  with a gate z, else  act(xh w + b)
+ *   x      [n, T, C] dtype; element (i, t, c) at x + i*x_n_stride +
+ *          t*x_t_stride + c;  z likewise, or NULL
+ *   w, b   [C] float32, or NULL (1 and 0)
+ *   y      [n, T, C] dtype, contiguous.  May be x or z where that is
+ *          contiguous too.
+ * Statistics and sums are float32, the output is rounded once.
+ * Sizes: D <= 4096, n*T < 2^31.
+ */
+typedef enum gdp_activation {
+    GDP_ACT_NONE = 0,
+    GDP_ACT_SILU = 1,
+    GDP_ACT_SIGMOID = 2
+} gdp_activation;
+
+typedef struct gdp_group_norm_args {
+    int64_t n;
+    int64_t T;
+    int32_t groups;
+    int32_t D;
+    gdp_dtype dtype;
+    gdp_activation activation;
+    int32_t centered;
+    float eps;
+    const void *x;
+    int64_t x_n_stride;
+    int64_t x_t_stride;
+    const void *z;
+    int64_t z_n_stride;
+    int64_t z_t_stride;
+    const float *w;
+    const float *b;
+    void *y;
+} gdp_group_norm_args;
+
+/* Gradients: dy [n, T, C] dtype, strided; dx, dz (with a gate) [n, T, C]
+ * dtype, contiguous; dw, db [C] float32, each or both NULL (not wanted). */
+typedef struct gdp_group_norm_grads {
+    const void *dy;
+    int64_t dy_n_stride;
+    int64_t dy_t_stride;
+    void *dx;
+    void *dz;
+    float *dw;
+    float *db;
+} gdp_group_norm_grads;
+
+gdp_status gdp_group_norm_fwd(const gdp_group_norm_args *a, void *stream);
+/* Device workspace of gdp_group_norm_bwd for dw and db (0 where neither is
+ * wanted: pass any size); -1 on bad sizes. */
+int64_t gdp_group_norm_workspace_bytes(const gdp_group_norm_args *a);
+/* y of a is not used.  workspace: 256-byte aligned, caller-owned. */
+gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm_grads *d, void *workspace,
+                              int64_t workspace_bytes, void *stream);
 
 /* Message describing the last non-OK status of this thread ("" if none). */
 const char *gdp_last_error(void);
