@@ -78,7 +78,7 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
     s->s_tot = m.take<float>(heads);
     s->r = m.take<float>(heads * E);
     s->r_tot = m.take<float>(heads);
-    s->nq = s->nk = a.K / gdp::lin_slice(a.V, a.K);
+    s->nq = s->nk = a.K / gdp::lin_slice(a.K);
     s->rho_q = m.take<float>(s->nq * BTH);
     s->rho_k = m.take<float>(s->nk * BTH);
     s->part = m.take<double>(p.items * a.HV);
@@ -92,7 +92,8 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
 gdp_status check_dims(const char *name, int32_t H, int32_t HV, int32_t K, int32_t V, float scale, gdp_dtype dtype) {
     if (dtype != GDP_F32 && dtype != GDP_BF16) return fail(GDP_ERR_INVALID, "%s: unknown dtype %d", name, (int)dtype);
     if (H < 1 || HV < 1 || HV % H) return fail(GDP_ERR_INVALID, "%s: HV must be a positive multiple of H", name);
-    if (HV > 65535) return fail(GDP_ERR_UNSUPPORTED, "%s: HV > 65535", name);
+    if ((int64_t)HV * (K > V ? K : V) > (1 << 22))
+        return fail(GDP_ERR_UNSUPPORTED, "%s: rows of over 2^22 elements (HV=%d)", name, HV);
     if (!(K == 64 || K == 128) || !(V == 64 || V == 128 || V == 256))
         return fail(GDP_ERR_UNSUPPORTED, "%s: head dims K=%d, V=%d not built (K in {64, 128}, V in {64, 128, 256})", name,
                     K, V);
@@ -100,14 +101,18 @@ gdp_status check_dims(const char *name, int32_t H, int32_t HV, int32_t K, int32_
     return ok();
 }
 
-// Rows of a strided input: base and strides on 16 bytes, and a chunk of rows within 32-bit offsets.
-gdp_status check_rows(const char *name, const char *what, const void *p, int64_t bs, int64_t ts, gdp_dtype dtype) {
+// Rows of a strided input: base and strides on 16 bytes, no overlap, and a chunk of rows within 32-bit offsets.
+gdp_status check_rows(const char *name, const char *what, const void *p, int64_t bs, int64_t ts, int64_t T,
+                      int64_t width, gdp_dtype dtype) {
     const int64_t unit = 16 / (int64_t)dsize(dtype);
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
     if (bs < 0 || ts < 0) return fail(GDP_ERR_INVALID, "%s: strides of %s must be >= 0", name, what);
     if (!aligned16(p) || bs % unit || ts % unit)
         return fail(GDP_ERR_INVALID, "%s: rows of %s are not 16-byte aligned", name, what);
-    if (ts > (1 << 24)) return fail(GDP_ERR_UNSUPPORTED, "%s: token stride of %s over 2^24 elements", name, what);
+    if (T > 1 && ts < width)
+        return fail(GDP_ERR_INVALID, "%s: rows of %s overlap (stride %lld < width %lld)", name, what, (long long)ts,
+                    (long long)width);
+    if (ts > (1 << 23)) return fail(GDP_ERR_UNSUPPORTED, "%s: token stride of %s over 2^23 elements", name, what);
     return ok();
 }
 
@@ -137,9 +142,9 @@ gdp_status check_linattn(const char *name, const gdp_linattn_args *a, bool forwa
         return fail(GDP_ERR_INVALID, "%s: g, g_head or cu_seqlens is not 4-byte aligned", name);
     if (!aligned16(a->h0) || !aligned16(a->ht)) return fail(GDP_ERR_INVALID, "%s: h0 or ht is not 16-byte aligned", name);
     if (nseq == 0 || a->T == 0) return ok();
-    if ((st = check_rows(name, "q", a->q, a->q_b_stride, a->q_t_stride, a->dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "q", a->q, a->q_b_stride, a->q_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->T, (int64_t)a->HV * a->V, a->dtype)) != GDP_OK) return st;
     if (forward && (!a->o || !aligned16(a->o))) return fail(GDP_ERR_INVALID, "%s: o is NULL or not 16-byte aligned", name);
     return ok();
 }
@@ -151,6 +156,11 @@ gdp_status check_space(const char *name, const void *ws, int64_t bytes, int64_t 
     if (bytes < need)
         return fail(GDP_ERR_INVALID, "%s: workspace of %lld bytes, %lld needed", name, (long long)bytes, (long long)need);
     return ok();
+}
+
+// A tensor of a walk; the stride of a single token does not matter and is made that of a plain row.
+gdp::LinRows rows_of(const void *p, int64_t bs, int64_t ts, int64_t T, int64_t width, int div) {
+    return gdp::LinRows{p, bs, T > 1 ? ts : width, div};
 }
 
 // What every walk of a call shares.
@@ -205,9 +215,10 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
     hipStream_t s = (hipStream_t)stream;
 
     gdp::LinWalk w = walk_base(a, p);
-    w.a = {a.q, a.q_b_stride, a.q_t_stride, a.HV / a.H};
-    w.b = {a.k, a.k_b_stride, a.k_t_stride, a.HV / a.H};
-    w.c = {a.v, a.v_b_stride, a.v_t_stride, 1};
+    const int r = a.HV / a.H;
+    w.a = rows_of(a.q, a.q_b_stride, a.q_t_stride, a.T, (int64_t)a.H * a.K, r);
+    w.b = rows_of(a.k, a.k_b_stride, a.k_t_stride, a.T, (int64_t)a.H * a.K, r);
+    w.c = rows_of(a.v, a.v_b_stride, a.v_t_stride, a.T, (int64_t)a.HV * a.V, 1);
     w.da = a.K;
     w.dc = a.V;
     w.s0 = a.h0;
@@ -248,7 +259,8 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     if (!(a.scale > 0.f)) a.scale = 1.0f / std::sqrt((float)a.K);
     const Plan p = plan_of(a, true);
     if (p.nseq > 0 && a.T > 0) {
-        if ((st = check_rows(name, "dout", d->dout, d->do_b_stride, d->do_t_stride, a.dtype)) != GDP_OK) return st;
+        if ((st = check_rows(name, "dout", d->dout, d->do_b_stride, d->do_t_stride, a.T, (int64_t)a.HV * a.V,
+                             a.dtype)) != GDP_OK) return st;
         if (!d->dq || !d->dk || !d->dv || !aligned16(d->dq) || !aligned16(d->dk) || !aligned16(d->dv))
             return fail(GDP_ERR_INVALID, "%s: dq, dk or dv is NULL or not 16-byte aligned", name);
     }
@@ -268,8 +280,11 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     if (p.nseq == 0) return hip_status(gdp::launch_lin_dg(g, d->dg_head, s), name);
 
     const int r = a.HV / a.H;
-    const gdp::LinRows q{a.q, a.q_b_stride, a.q_t_stride, r}, k{a.k, a.k_b_stride, a.k_t_stride, r},
-        v{a.v, a.v_b_stride, a.v_t_stride, 1}, o{d->dout, d->do_b_stride, d->do_t_stride, 1};
+    const int64_t wk = (int64_t)a.H * a.K, wv = (int64_t)a.HV * a.V;
+    const gdp::LinRows q = rows_of(a.q, a.q_b_stride, a.q_t_stride, a.T, wk, r),
+                       k = rows_of(a.k, a.k_b_stride, a.k_t_stride, a.T, wk, r),
+                       v = rows_of(a.v, a.v_b_stride, a.v_t_stride, a.T, wv, 1),
+                       o = rows_of(d->dout, d->do_b_stride, d->do_t_stride, a.T, wv, 1);
     const gdp::LinWalk base = walk_base(a, p);
     const gdp::LinKind kind = want_g ? gdp::LIN_DOT : gdp::LIN_OUT;
     const bool shared = r > 1;
@@ -386,9 +401,9 @@ gdp_status gdp_linattn_decode(const gdp_linattn_decode_args *args, void *stream)
     if (((uintptr_t)a.g | (uintptr_t)a.g_head | (uintptr_t)a.slots) & 3)
         return fail(GDP_ERR_INVALID, "%s: g, g_head or slots is not 4-byte aligned", name);
     if (a.n == 0 || a.S == 0) return ok();
-    if ((st = check_rows(name, "q", a.q, a.q_n_stride, a.q_t_stride, a.dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "k", a.k, a.k_n_stride, a.k_t_stride, a.dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "v", a.v, a.v_n_stride, a.v_t_stride, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "q", a.q, a.q_n_stride, a.q_t_stride, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "k", a.k, a.k_n_stride, a.k_t_stride, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "v", a.v, a.v_n_stride, a.v_t_stride, a.S, (int64_t)a.HV * a.V, a.dtype)) != GDP_OK) return st;
     if ((!a.state && a.pool > 0) || !aligned16(a.state))
         return fail(GDP_ERR_INVALID, "%s: state is NULL or not 16-byte aligned", name);
     if (!a.o || !aligned16(a.o)) return fail(GDP_ERR_INVALID, "%s: o is NULL or not 16-byte aligned", name);

@@ -23,6 +23,7 @@ struct LinWalk {
     LinRows a, b, c, x;
     int da, dc;        // columns of a and b, of c (and x, y)
     int HV;
+    float sb, sy;      // factors of the products a_i.b_j (and c_j b_j^T), and of y
     int64_t B, T, nseq, seg_tok;
     const int32_t *cu;
     const float *g;    // log decay of (b, t, hv) at g + b*g_bs + t*g_ts + hv, or NULL
@@ -30,7 +31,6 @@ struct LinWalk {
     bool rev;          // backwards in time
     bool trans;        // states that are read hold element (c, a) at [a][c]
     bool y32;          // y is float
-    float sb, sy;      // factors of the products a_i.b_j (and c_j b_j^T), and of y
     void *y;           // [B, T, HV, dc]
     float *rho;        // [slices, HV, B*T]
     const float *s0;   // [nseq, HV, dc, da] or NULL: state before the first row of the walk
@@ -64,7 +64,7 @@ struct LinDg {
     double *part;      // [items, HV] or NULL: sums over each segment
 };
 
-int lin_slice(int da, int dc);
+int lin_slice(int dc);
 hipError_t launch_lin_walk(const LinWalk &w, gdp_dtype dtype, LinKind kind, int64_t items, hipStream_t stream);
 hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream);
 hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream);

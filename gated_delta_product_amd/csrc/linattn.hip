@@ -19,8 +19,8 @@
 //   P[i][j] = (a_i.b_j) 2^(G_i - G_j), j <= i      the masked in-chunk scores
 //   y_i     = 2^G_i S a_i + sum_j P[i][j] c_j
 //   S      <- 2^G_end S + sum_j 2^(G_end - G_j) c_j b_j^T
-// The four waves share the score tiles (through LDS) and then own a quarter
-// of the columns of c each: S^T stays in registers as result tiles of the
+// The waves (one to 16 columns of c) share the score tiles through LDS and
+// then own their columns: S^T stays in registers as result tiles of the
 // matrix core, whose lanes hold 4 consecutive rows a of a column c; the
 // columns of b are taken in the order 8g + i, 8g + 4 + i for the two tiles
 // of 32 columns, so those tiles are the operand of S a as they stand.
@@ -29,8 +29,6 @@
 #include "linattn.h"
 
 namespace gdp {
-
-constexpr int LNT = 256;  // threads of a walk: four waves
 
 // ---------------------------------------------------------------- LDS tiles
 // Rows of D elements without padding; the 16-byte unit u of row r sits at
@@ -46,38 +44,61 @@ template <typename T, int D>
 struct Tile {
     static constexpr int E = 16 / sizeof(T);  // elements of a unit
     static constexpr int UPR = D / E;
+    typedef typename Frag<T>::type frag;
+    typedef typename Frag<T>::half half;
     static __device__ __forceinline__ int at(int row, int col) {
         return row * D + (((col / E) ^ swz<UPR>(row)) * E) + col % E;
     }
-    // 8 elements [row][col .. col + 7], col a multiple of 8
-    static __device__ __forceinline__ typename Frag<T>::type row8(const T *t, int row, int col) {
-        if constexpr (sizeof(T) == 2) return *(const typename Frag<T>::type *)(t + at(row, col));
-        else return join<T>(*(const f32x4 *)(t + at(row, col)), *(const f32x4 *)(t + at(row, col + 4)));
+
+    // Operand rows: 8 elements [16 ib + m][32 kb + 8 g .. + 7] for lane 16 g + m.
+    // swz looks at the row's low 4 bits and 32 kb at the unit's bits above
+    // g's, so one offset per lane serves every ib (added) and kb (xor).
+    static __device__ __forceinline__ int row_base(int lane) { return at(lane & 15, 8 * (lane >> 4)); }
+    static __device__ __forceinline__ frag row8(const T *t, int base, int ib, int kb) {
+        const T *p = t + ((base ^ (32 * kb)) + 16 * ib * D);
+        if constexpr (sizeof(T) == 2) return *(const frag *)p;
+        else return join<T>(*(const f32x4 *)p, *(const f32x4 *)(t + ((base ^ (32 * kb) ^ 4) + 16 * ib * D)));
     }
-    static __device__ __forceinline__ typename Frag<T>::half row4(const T *t, int row, int col) {
-        return *(const typename Frag<T>::half *)(t + at(row, col));
-    }
-    // rows r0 .. r0 + 3 of one column per lane: lane m of 16 gets column
-    // col0 + STEP * (m / 4) + m % 4 (STEP 4: 16 neighbouring columns)
+
+    // Operand columns: rows 32 tb + 8 g + 0 .. 7 of one column per lane, the
+    // transposed read (a 16-lane group: source lane s points at row s / 4;
+    // output lane 4 i + j receives slot j of the sources 4 r + i).  The column
+    // of lane m is col0 + STEP * (m / 4) + m % 4: 16 neighbours (STEP 4), or
+    // with STEP 8 every other four of 32.  bf16: two offsets per lane (rows
+    // + 0 and + 4); 32-column groups come in by xor, rows and a step of 4
+    // columns (STEP 8) by addition.
+    struct Cols {
+        int o[2];
+    };
     template <int STEP>
-    static __device__ __forceinline__ typename Frag<T>::half col4(const T *t, int r0, int col0) {
-        const int s = lane_id() & 15;
+    static __device__ __forceinline__ Cols col_base(int lane, int col0) {
+        const int q = lane & 15, r = 8 * (lane >> 4) + (q >> 2);
+        return Cols{{at(r, col0 + STEP * (q & 3)), at(r + 4, col0 + STEP * (q & 3))}};
+    }
+    template <int STEP>
+    static __device__ __forceinline__ frag col8(const T *t, const Cols &c, int lane, int tb, int kb, int add) {
         if constexpr (sizeof(T) == 2) {
-            const T *p = t + at(r0 + (s >> 2), col0 + STEP * (s & 3));
-            return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                  (lds_i16x4 *)((__attribute__((address_space(3))) const char *)p)));
-        } else {
-            f32x4 r;
+            half h[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = t[at(r0 + i, col0 + STEP * (s >> 2) + (s & 3))];
-            return r;
+            for (int k = 0; k < 2; ++k) {
+                const T *p = t + ((c.o[k] ^ (32 * kb)) + 32 * tb * D + add);
+                h[k] = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (lds_i16x4 *)((__attribute__((address_space(3))) const char *)p)));
+            }
+            return join<T>(h[0], h[1]);
+        } else {
+            // o[0] holds the plain column
+            const int m = lane & 15, col = c.o[0] + 32 * kb + add + STEP * (m >> 2) + (m & 3), r = 32 * tb + 8 * (lane >> 4);
+            frag f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = t[at(r + i, col)];
+            return f;
         }
     }
-    // the fragment of 32 rows from r0 (8 rows of lane group g at r0 + 8g)
     template <int STEP>
-    static __device__ __forceinline__ typename Frag<T>::type col8(const T *t, int r0, int col0) {
-        const int r = r0 + 8 * (lane_id() >> 4);
-        return join<T>(col4<STEP>(t, r, col0), col4<STEP>(t, r + 4, col0));
+    static __device__ __forceinline__ Cols cols(int lane, int col0) {
+        if constexpr (sizeof(T) == 2) return col_base<STEP>(lane, col0);
+        else return Cols{{col0, 0}};
     }
 };
 
@@ -184,15 +205,23 @@ __device__ __forceinline__ LinItem lin_item(const int32_t *cu, int64_t nseq, int
 //      values: the part of the row that the decays scale.
 // NS:  bf16 parts of the decayed c in the state update (16 or 24 bits).
 // NQ:  parts of the state in S a.
+template <typename T> constexpr bool F32_Y = sizeof(T) == 4;
+
 template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
 struct Walk {
     static constexpr bool F32 = sizeof(T) == 4;
     static constexpr int CT = F32 ? 32 : 64;     // rows of a chunk
     static constexpr int NB = CT / 16;           // 16-row blocks
+    static constexpr int NP = NB * (NB + 1) / 2;  // score tiles at and below the diagonal
     static constexpr int TB = CT / 32;           // 32-row blocks
     static constexpr int KT = DA / 16;           // 16-row tiles of S^T
-    static constexpr int NW = DC / 64;           // 16-column tiles of a wave
-    static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / LNT, UC = CT * DC * (int)sizeof(T) / 16 / LNT;
+    static constexpr int WV = DC / 16;           // waves
+    static constexpr int NT = 64 * WV;
+    // waves a SIMD: two blocks to a compute unit where their LDS fits (and
+    // with 256 rows of S^T a wave needs the registers of two)
+    static constexpr int OCC = DA == 256 ? (WV == 8 ? 2 : 1) : WV / 2;
+    static constexpr int KG = OUT && OCC >= 4 ? 2 : 4;
+    static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
     typedef Tile<T, CT> TP;
@@ -206,29 +235,44 @@ struct Walk {
         T p[OUT ? CT * CT : 8];
         float gh[2][CT], gl[2][CT];  // G as two floats
         float eg[2][CT], wg[2][CT];  // 2^G_i and sb 2^(G_end - G_i)
-        float rho[DOT ? 4 * CT : 4];
+        float rho[DOT ? WV * CT : 4];
     };
 };
 
-template <typename T, int D, int UNITS>
-__device__ __forceinline__ void rows_to_regs(uint4 (&r)[UNITS], const T *base, int32_t ts, int n, bool rev) {
-    constexpr int E = 16 / sizeof(T), UPR = D / E;
-#pragma unroll
-    for (int it = 0; it < UNITS; ++it) {
-        const int u = threadIdx.x + LNT * it, row = u / UPR, col = u % UPR * E;
-        r[it] = make_uint4(0, 0, 0, 0);
-        if (row < n) r[it] = *(const uint4 *)(base + ((rev ? n - 1 - row : row) * ts + col));
+// A chunk's rows of one tensor into registers, 16 bytes a thread and step, and
+// from there into a tile.  Row r of the walk is row r of the buffer, or going
+// backwards row n - 1 - r; rows past n lie outside the buffer's range (there
+// below its start, as a large unsigned offset) and come as zeros.
+template <typename T, int D, int NT, int UNITS>
+struct Rows {
+    static constexpr int E = 16 / sizeof(T), UPR = D / E, STEP = NT / UPR;
+    uint4 r[UNITS];
+    uint32_t step;  // bytes between a thread's rows (negative going backwards)
+    uint32_t off;   // of its first row in a whole chunk
+    uint32_t ts;    // bytes of a row
+    __device__ __forceinline__ void init(int64_t ts_elems, bool rev, int rows) {
+        ts = (uint32_t)ts_elems * sizeof(T);
+        const int row = threadIdx.x / UPR;
+        off = (uint32_t)(rev ? rows - 1 - row : row) * ts + threadIdx.x % UPR * 16;
+        step = rev ? 0u - STEP * ts : STEP * ts;
     }
-}
-template <typename T, int D, int UNITS>
-__device__ __forceinline__ void regs_to_tile(T *t, const uint4 (&r)[UNITS]) {
-    constexpr int E = 16 / sizeof(T), UPR = D / E;
+    __device__ __forceinline__ void fetch(const T *base, int n, bool rev, int rows) {
+        const rsrc_t rs = make_rsrc(base, (uint32_t)(n - 1) * ts + D * sizeof(T));
+        const uint32_t o = off - (rev ? (uint32_t)(rows - n) * ts : 0u);
 #pragma unroll
-    for (int it = 0; it < UNITS; ++it) {
-        const int u = threadIdx.x + LNT * it;
-        *(uint4 *)(t + Tile<T, D>::at(u / UPR, u % UPR * E)) = r[it];
+        for (int i = 0; i < UNITS; ++i) r[i] = buf_load16(rs, o + i * step);
     }
-}
+    __device__ __forceinline__ void stage(T *t, int tid) const {
+        if constexpr (STEP % 16 == 0) {  // whole periods of the swizzle
+            T *p = t + Tile<T, D>::at(tid / UPR, tid % UPR * E);
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) *(uint4 *)(p + i * STEP * D) = r[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) *(uint4 *)(t + Tile<T, D>::at(tid / UPR + i * STEP, tid % UPR * E)) = r[i];
+        }
+    }
+};
 
 template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
 __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, int slice,
@@ -238,8 +282,9 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     typedef typename W::TA TA;
     typedef typename W::TC TC;
     typedef typename W::TP TP;
-    constexpr int CT = W::CT;
-    const int lane = lane_id(), wave = wave_id(), m = lane & 15, g4 = lane >> 4;
+    constexpr int CT = W::CT, NT = W::NT;
+    int lane = lane_id();
+    const int wave = wave_id();
 
     const LinItem it = lin_item(w.cu, w.nseq, w.T, w.seg_tok, id);
     if (it.seq < 0) return;
@@ -258,49 +303,31 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     const T *px = DOT ? (const T *)w.x.p + bi * w.x.bs + (int64_t)(hv / w.x.div) * w.dc + slice * DC : nullptr;
     const float *pg = w.g ? w.g + bi * w.g_bs + hv : nullptr;
 
-    // entering state: S^T tiles [kt][nw], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c = m
-    f32x4 s[W::KT][W::NW];
-    const int c0w = (wave * W::NW) * 16 + m;  // first column of this lane
-    {
-        const float *s0 = nullptr;
-        if (w.seg_in)
-            s0 = w.seg_in + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
-        else if (OUT && w.s0) s0 = w.s0 + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
-#pragma unroll
-        for (int kt = 0; kt < W::KT; ++kt)
-#pragma unroll
-            for (int nw = 0; nw < W::NW; ++nw) {
-                s[kt][nw] = zero4();
-                if (!s0) continue;
-                const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2), c = slice * DC + c0w + 16 * nw;
-                if (w.trans) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[kt][nw][i] = s0[(int64_t)(a + i) * w.dc + c];
-                } else {
-                    s[kt][nw] = *(const f32x4 *)(s0 + (int64_t)c * DA + a);
-                }
-            }
-    }
-
-    uint4 ra[OUT ? W::UA : 1], rb[W::UA], rc[W::UC], rx[DOT ? W::UC : 1];
+    Rows<T, DA, NT, W::UA> ra, rb;
+    Rows<T, DC, NT, W::UC> rc, rx;
+    if constexpr (OUT) ra.init(w.a.ts, w.rev, CT);
+    rb.init(w.b.ts, w.rev, CT);
+    rc.init(w.c.ts, w.rev, CT);
+    if constexpr (DOT) rx.init(w.x.ts, w.rev, CT);
+    const bool decayer = wave == W::WV - 1;  // the wave that forms the decays (it has fewer score tiles)
     float rg = 0.f;
-    // rows [c0, c0 + n) of the walk into registers (g: one row a lane of every wave)
+    // rows [c0, c0 + n) of the walk into registers (g: one row a lane)
     auto fetch = [&](int64_t c0, int n) {
         const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
-        if constexpr (OUT) rows_to_regs<T, DA>(ra, pa + first * w.a.ts, (int32_t)w.a.ts, n, w.rev);
-        rows_to_regs<T, DA>(rb, pb + first * w.b.ts, (int32_t)w.b.ts, n, w.rev);
-        rows_to_regs<T, DC>(rc, pc + first * w.c.ts, (int32_t)w.c.ts, n, w.rev);
-        if constexpr (DOT) rows_to_regs<T, DC>(rx, px + first * w.x.ts, (int32_t)w.x.ts, n, w.rev);
+        if constexpr (OUT) ra.fetch(pa + first * w.a.ts, n, w.rev, CT);
+        rb.fetch(pb + first * w.b.ts, n, w.rev, CT);
+        rc.fetch(pc + first * w.c.ts, n, w.rev, CT);
+        if constexpr (DOT) rx.fetch(px + first * w.x.ts, n, w.rev, CT);
         rg = 0.f;
-        if (pg && lane < n) {
+        if (pg && decayer && lane < n) {
             // backwards, a row is entered through the decay of the row after it
             const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
             if (t < eos_in) rg = pg[t * w.g_ts];
         }
     };
-    float tot = 0.f;  // log2 decay of the whole walk (wave 0), for the segment pass
+    float tot = 0.f;  // log2 decay of the whole walk (in the decayer), for the segment pass
     auto decays = [&](int n, int buf) {
-        if (wave != 0) return;
+        if (!decayer) return;
         const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(rg) : 0.0);
         const double Gend = __shfl(G, 63, 64);
         tot += (float)Gend;
@@ -312,88 +339,68 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             sm.wg[buf][lane] = w.sb * __builtin_amdgcn_exp2f((float)(Gend - G));
         }
     };
+    const int64_t nch = ceil_div64(len, CT);
+    if (nch > 0) fetch(0, len < CT ? (int)len : CT);
+
+    // entering state: S^T tiles [kt], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c
+    f32x4 s[W::KT];
+    const int cw = wave * 16;  // first column of this wave in the slice
+    {
+        const int m = lane & 15, g4 = lane >> 4, col = slice * DC + cw + m;
+        const float *s0 = nullptr;
+        if (w.seg_in) s0 = w.seg_in + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
+        else if (OUT && w.s0) s0 = w.s0 + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
+#pragma unroll
+        for (int kt = 0; kt < W::KT; ++kt) {
+            s[kt] = zero4();
+            if (!s0) continue;
+            const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2);
+            if (w.trans) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[kt][i] = s0[(a + i) * w.dc + col];
+            } else {
+                s[kt] = *(const f32x4 *)(s0 + col * DA + a);
+            }
+        }
+    }
     // tiles above the diagonal of P stay zero (a 32-row contraction of an even block reads one)
     if constexpr (OUT) {
-        for (int i = threadIdx.x; i < CT * CT; i += LNT) sm.p[i] = from_f32<T>(0.f);
+        for (int i = threadIdx.x; i < CT * CT; i += NT) sm.p[i] = from_f32<T>(0.f);
     }
+    if (nch > 0) decays(len < CT ? (int)len : CT, 0);
 
-    const int64_t nch = ceil_div64(len, CT);
-    if (nch > 0) {
-        const int n = len < CT ? (int)len : CT;
-        fetch(0, n);
-        decays(n, 0);
-    }
+    // The barriers order LDS only: the next chunk's rows stay in flight over
+    // them, and so do the stores of y.
     for (int64_t ch = 0; ch < nch; ++ch) {
         const int64_t c0 = ch * CT;
         const int n = len - c0 < CT ? (int)(len - c0) : CT;
         const int n1 = len - c0 - CT < CT ? (int)(len - c0 - CT) : CT;  // rows of the next chunk
         const int buf = (int)(ch & 1);
-        if constexpr (OUT) regs_to_tile<T, DA>(sm.a, ra);
-        regs_to_tile<T, DA>(sm.b, rb);
-        regs_to_tile<T, DC>(sm.c, rc);
-        if constexpr (DOT) regs_to_tile<T, DC>(sm.x, rx);
-        __syncthreads();
+        // LDS addresses are formed anew in each chunk: held over it they would
+        // not fit the registers
+        asm volatile("" : "+v"(lane));
+        const int m = lane & 15, g4 = lane >> 4, tid = wave * 64 + lane;
+        if constexpr (OUT) ra.stage(sm.a, tid);
+        rb.stage(sm.b, tid);
+        rc.stage(sm.c, tid);
+        if constexpr (DOT) rx.stage(sm.x, tid);
+        lds_barrier();
         if (ch + 1 < nch) fetch(c0 + CT, n1);
+        const int arow = TA::row_base(lane);
 
-        f32x4 y[W::NB][W::NW];
+        f32x4 y[W::NB];
         if constexpr (OUT) {
-            // S a: S^T tiles as the operand, rounded to NQ parts
+            // score tiles at and below the diagonal: P^T (rows j, columns i)
+            float rho_p[DOT ? (W::NP + W::WV - 1) / W::WV : 1];
 #pragma unroll
-            for (int ib = 0; ib < W::NB; ++ib)
-#pragma unroll
-                for (int nw = 0; nw < W::NW; ++nw) y[ib][nw] = zero4();
-#pragma unroll
-            for (int kb = 0; kb < DA / 32; ++kb) {
-                frag sp[W::NW][NQ];
-#pragma unroll
-                for (int nw = 0; nw < W::NW; ++nw) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = s[2 * kb + i / 4][nw][i % 4];
-                    split8<T, NQ>(v, sp[nw]);
-                }
-#pragma unroll
-                for (int ib = 0; ib < W::NB; ++ib) {
-                    const frag fa = TA::row8(sm.a, 16 * ib + m, 32 * kb + 8 * g4);
-#pragma unroll
-                    for (int nw = 0; nw < W::NW; ++nw)
-#pragma unroll
-                        for (int p = NQ - 1; p >= 0; --p) y[ib][nw] = mma(sp[nw][p], fa, y[ib][nw]);
-                }
-            }
-            float rho[W::NB];
-#pragma unroll
-            for (int ib = 0; ib < W::NB; ++ib) {
-                const float e = sm.eg[buf][16 * ib + m];
-                rho[ib] = 0.f;
-#pragma unroll
-                for (int nw = 0; nw < W::NW; ++nw) {
-                    y[ib][nw] *= e;
-                    if constexpr (DOT) {
-                        const auto xv = TC::row4(sm.x, 16 * ib + m, (wave * W::NW + nw) * 16 + 4 * g4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) rho[ib] += to_f32(xv[i]) * y[ib][nw][i];
-                    }
-                }
-            }
-            if constexpr (DOT) {
-#pragma unroll
-                for (int ib = 0; ib < W::NB; ++ib) {
-                    rho[ib] = xor32_sum(xor16_sum(rho[ib]));
-                    if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] = rho[ib];
-                }
-            }
-            // score tiles at and below the diagonal, four at a time: P^T (rows j, columns i)
-#pragma unroll
-            for (int k = 0; k < (W::NB * (W::NB + 1) / 2 + 3) / 4; ++k) {
-                const int t = 4 * k + wave;
-                if (t >= W::NB * (W::NB + 1) / 2) break;
+            for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
+                const int t = W::WV * k + wave;
+                if (t >= W::NP) break;
                 const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
                 f32x4 acc = zero4();
 #pragma unroll
                 for (int kb = 0; kb < DA / 32; ++kb)
-                    acc = mma(TA::row8(sm.b, 16 * jb + m, 32 * kb + 8 * g4),
-                              TA::row8(sm.a, 16 * ib + m, 32 * kb + 8 * g4), acc);
+                    acc = mma(TA::row8(sm.b, arow, jb, kb), TA::row8(sm.a, arow, ib, kb), acc);
                 const int i = 16 * ib + m, j0 = 16 * jb + 4 * g4;
                 const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
                 const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
@@ -406,82 +413,118 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 }
                 *(typename Frag<T>::half *)(sm.p + TP::at(i, j0)) = pv;
                 if constexpr (DOT) {
+                    const int crow = TC::row_base(lane);
                     f32x4 e = zero4();
 #pragma unroll
                     for (int kb = 0; kb < DC / 32; ++kb)
-                        e = mma(TC::row8(sm.c, 16 * jb + m, 32 * kb + 8 * g4),
-                                TC::row8(sm.x, 16 * ib + m, 32 * kb + 8 * g4), e);
+                        e = mma(TC::row8(sm.c, crow, jb, kb), TC::row8(sm.x, crow, ib, kb), e);
                     float q = 0.f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) q += j0 + r < i ? acc[r] * e[r] : 0.f;
+                    rho_p[k] = xor32_sum(xor16_sum(q));
+                }
+            }
+            // S a: S^T tiles as the operand, rounded to NQ parts
+#pragma unroll
+            for (int ib = 0; ib < W::NB; ++ib) y[ib] = zero4();
+#pragma unroll
+            for (int kb = 0; kb < DA / 32; ++kb) {
+                frag sp[NQ];
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = s[2 * kb + i / 4][i % 4];
+                split8<T, NQ>(v, sp);
+                frag fa[W::NB];
+#pragma unroll
+                for (int ib = 0; ib < W::NB; ++ib) fa[ib] = TA::row8(sm.a, arow, ib, kb);
+#pragma unroll
+                for (int p = NQ - 1; p >= 0; --p)
+#pragma unroll
+                    for (int ib = 0; ib < W::NB; ++ib) y[ib] = mma(sp[p], fa[ib], y[ib]);
+            }
+#pragma unroll
+            for (int ib = 0; ib < W::NB; ++ib) {
+                y[ib] *= sm.eg[buf][16 * ib + m];
+                if constexpr (DOT) {
+                    const auto xv = *(const typename Frag<T>::half *)(sm.x + TC::at(16 * ib + m, cw + 4 * g4));
+                    float q = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q += to_f32(xv[i]) * y[ib][i];
                     q = xor32_sum(xor16_sum(q));
-                    if (g4 == 0) sm.rho[wave * CT + i] += q;
+                    if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] = q;
+                }
+            }
+            if constexpr (DOT) {
+#pragma unroll
+                for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
+                    const int t = W::WV * k + wave;
+                    if (t >= W::NP) break;
+                    const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+                    if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] += rho_p[k];
                 }
             }
             lds_barrier();
         }
 
         // the rows c as operands, once for P c and (decayed) for the state
+        const float dec = sm.eg[buf][CT - 1];
+        const auto ccol = TC::template cols<4>(lane, cw);
+        const auto bcol = TA::template cols<8>(lane, 0);
+        const int prow = TP::row_base(lane);
 #pragma unroll
-        for (int kt = 0; kt < W::KT; ++kt)
-#pragma unroll
-            for (int nw = 0; nw < W::NW; ++nw) s[kt][nw] *= sm.eg[buf][CT - 1];
+        for (int kt = 0; kt < W::KT; ++kt) s[kt] *= dec;
 #pragma unroll
         for (int tb = 0; tb < W::TB; ++tb) {
-            frag fc[W::NW], fw[W::NW][NS];
+            const frag fc = TC::template col8<4>(sm.c, ccol, lane, tb, 0, 0);
+            frag fw[NS];
+            float v[8];
 #pragma unroll
-            for (int nw = 0; nw < W::NW; ++nw) {
-                fc[nw] = TC::template col8<4>(sm.c, 32 * tb, (wave * W::NW + nw) * 16);
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = to_f32(fc[nw][i]) * sm.wg[buf][32 * tb + 8 * g4 + i];
-                split8<T, NS>(v, fw[nw]);
-            }
+            for (int i = 0; i < 8; ++i) v[i] = to_f32(fc[i]) * sm.wg[buf][32 * tb + 8 * g4 + i];
+            split8<T, NS>(v, fw);
             if constexpr (OUT) {
 #pragma unroll
-                for (int ib = 2 * tb; ib < W::NB; ++ib) {
-                    const frag fp = TP::row8(sm.p, 16 * ib + m, 32 * tb + 8 * g4);
-#pragma unroll
-                    for (int nw = 0; nw < W::NW; ++nw) y[ib][nw] = mma(fc[nw], fp, y[ib][nw]);
-                }
+                for (int ib = 2 * tb; ib < W::NB; ++ib)
+                    y[ib] = mma(fc, TP::row8(sm.p, prow, ib, tb), y[ib]);
             }
+            // KG tiles at a time, so that a tile's parts are not back to back
 #pragma unroll
-            for (int kt = 0; kt < W::KT; ++kt) {
-                const frag fb = TA::template col8<8>(sm.b, 32 * tb, 32 * (kt / 2) + 4 * (kt % 2));
+            for (int k0 = 0; k0 < W::KT; k0 += W::KG) {
+                frag fb[W::KG];
 #pragma unroll
-                for (int nw = 0; nw < W::NW; ++nw)
+                for (int k = 0; k < W::KG; ++k)
+                    fb[k] = TA::template col8<8>(sm.b, bcol, lane, tb, (k0 + k) / 2, 4 * (k % 2));
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) s[kt][nw] = mma(fb, fw[nw][p], s[kt][nw]);
+                for (int p = NS - 1; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < W::KG; ++k) s[k0 + k] = mma(fb[k], fw[p], s[k0 + k]);
             }
         }
         if (ch + 1 < nch) decays(n1, buf ^ 1);
         if constexpr (OUT) {
+            // rows of y as a buffer that ends with the chunk, like the inputs' (stores past it are dropped)
+            const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
+            const int64_t e = ((bi * w.T + first) * w.HV + hv) * (int64_t)w.dc + slice * DC + cw;
+            const uint32_t es = w.y32 ? 4 : sizeof(T), ys = (uint32_t)w.HV * w.dc * es;
+            const rsrc_t rs = make_rsrc((const char *)w.y + e * es, (uint32_t)(n - 1) * ys + 16 * es);
+            const uint32_t off = (uint32_t)(w.rev ? n - 1 - m : m) * ys + 4 * g4 * es, step = w.rev ? 0u - 16 * ys : 16 * ys;
 #pragma unroll
             for (int ib = 0; ib < W::NB; ++ib) {
-                const int row = 16 * ib + m;
-                if (row >= n) continue;
-                const int64_t t = w.rev ? tb0 + len - 1 - c0 - row : tb0 + c0 + row;
-                const int64_t e = ((bi * w.T + t) * w.HV + hv) * (int64_t)w.dc + slice * DC + (wave * W::NW) * 16 + 4 * g4;
-#pragma unroll
-                for (int nw = 0; nw < W::NW; ++nw) {
-                    const f32x4 v = y[ib][nw] * w.sy;
-                    if (w.y32) {
-                        *(f32x4 *)((float *)w.y + e + 16 * nw) = v;
-                    } else {
-                        typename Frag<T>::half o;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(v[i]);
-                        *(typename Frag<T>::half *)((T *)w.y + e + 16 * nw) = o;
-                    }
+                const f32x4 v = y[ib] * w.sy;
+                if (F32_Y<T> || w.y32) {
+                    buf_store16(rs, off + ib * step, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                                __float_as_uint(v[2]), __float_as_uint(v[3])));
+                } else {
+                    const bf16x4 o = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+                    buf_store8(rs, off + ib * step, __builtin_bit_cast(uint2, o));
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
         if constexpr (DOT) {
             if (wave == 0 && lane < n) {
                 float q = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q += sm.rho[i * CT + lane];
+                for (int i = 0; i < W::WV; ++i) q += sm.rho[i * CT + lane];
                 const int64_t t = w.rev ? tb0 + len - 1 - c0 - lane : tb0 + c0 + lane;
                 w.rho[((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + t] = q * w.sy;
             }
@@ -493,24 +536,22 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     float f = 1.f;
     if constexpr (!OUT) {
         so = w.seg_out + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
-        if (threadIdx.x == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = tot;
+        if (decayer && lane == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = tot;
     } else if (at_end && w.s_out) {
         so = w.s_out + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
         if (w.rev && pg && it.eos > it.bos)  // through the first row's decay too
             f = __builtin_amdgcn_exp2f((float)decay_log2(pg[(w.cu ? it.bos : 0) * w.g_ts]));
     }
     if (!so) return;
+    const int col = slice * DC + cw + (lane & 15), g4 = lane >> 4;
 #pragma unroll
     for (int kt = 0; kt < W::KT; ++kt)
-#pragma unroll
-        for (int nw = 0; nw < W::NW; ++nw) {
-            const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2), c = slice * DC + c0w + 16 * nw;
-            *(f32x4 *)(so + (int64_t)c * DA + a) = s[kt][nw] * f;
-        }
+        *(f32x4 *)(so + col * DA + 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2)) = s[kt] * f;
 }
 
 template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
-__global__ void __launch_bounds__(LNT, DA == 256 && OUT ? 1 : 2) gdp_lin_walk_k(LinWalk w) {
+__global__ void __launch_bounds__((Walk<T, DA, DC, NS, NQ, OUT, DOT>::NT), (Walk<T, DA, DC, NS, NQ, OUT, DOT>::OCC))
+gdp_lin_walk_k(LinWalk w) {
     __shared__ __align__(16) typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds sm;
     const int slices = w.dc / DC;
     const uint32_t b = blockIdx.x, per = (uint32_t)w.HV * slices;
@@ -712,24 +753,23 @@ template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
 static hipError_t launch_walk_t(const LinWalk &w, int64_t items, hipStream_t stream) {
     const int64_t blocks = items * w.HV * (w.dc / DC);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, NQ, OUT, DOT>), dim3((unsigned)blocks), dim3(LNT), 0, stream, w);
+    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, NQ, OUT, DOT>), dim3((unsigned)blocks),
+                       dim3(Walk<T, DA, DC, NS, NQ, OUT, DOT>::NT), 0, stream, w);
     return hipGetLastError();
 }
 
-// Columns of c that one walk takes: the state of a walk is at most 128 x 128.
-int lin_slice(int da, int dc) {
-    const int most = da == 256 ? 64 : 128;
-    return dc < most ? dc : most;
-}
+// Columns of c that one walk takes.
+int lin_slice(int dc) { return dc < 128 ? dc : 128; }
 
 template <typename T, int NS, int NQ, bool OUT, bool DOT>
 static hipError_t launch_walk_dims(const LinWalk &w, int64_t items, hipStream_t stream) {
-    switch (w.da * 1000 + lin_slice(w.da, w.dc)) {
+    switch (w.da * 1000 + lin_slice(w.dc)) {
     case 64064: return launch_walk_t<T, 64, 64, NS, NQ, OUT, DOT>(w, items, stream);
     case 64128: return launch_walk_t<T, 64, 128, NS, NQ, OUT, DOT>(w, items, stream);
     case 128064: return launch_walk_t<T, 128, 64, NS, NQ, OUT, DOT>(w, items, stream);
     case 128128: return launch_walk_t<T, 128, 128, NS, NQ, OUT, DOT>(w, items, stream);
     case 256064: return launch_walk_t<T, 256, 64, NS, NQ, OUT, DOT>(w, items, stream);
+    case 256128: return launch_walk_t<T, 256, 128, NS, NQ, OUT, DOT>(w, items, stream);
     default: return hipErrorInvalidValue;
     }
 }

@@ -528,8 +528,9 @@ int64_t gdp_num_state_chunks(const int32_t *cu_seqlens_host, int64_t num_seqs,
  * value head hv reading key head hv / (HV/H).  There is no L2 norm.
  *   q, k   [B, T, H,  K]  dtype; element (b, t, h, i) at
  *                         q + b*q_b_stride + t*q_t_stride + h*K + i (strides
- *                         in elements, >= 0; rows 16-byte aligned), so slices
- *                         of a wider projection can be passed as they are
+ *                         in elements, >= 0; rows 16-byte aligned, not
+ *                         overlapping, at most 2^23 apart), so slices of a
+ *                         wider projection can be passed as they are
  *   v      [B, T, HV, V]  dtype, strided likewise
  *   g      float32 natural-log decay of (b, t, hv) at g + b*g_b_stride +
  *          t*g_t_stride + hv, or NULL.  -inf empties the state; below -110
@@ -544,7 +545,8 @@ int64_t gdp_num_state_chunks(const int32_t *cu_seqlens_host, int64_t num_seqs,
  *   scale  <= 0 selects 1/sqrt(K).
  * Inputs must be finite (an infinity or a NaN may reach every row of its
  * 64-token chunk and the rows after it).
- * Sizes: K in {64, 128}, V in {64, 128, 256}, both dtypes; HV <= 65535.
+ * Sizes: K in {64, 128}, V in {64, 128, 256}, both dtypes; HV max(K, V) at
+ * most 2^22.
  */
 typedef struct gdp_linattn_args {
     int64_t B;
