@@ -34,24 +34,33 @@ struct Plan {
     bool segments;
 };
 
-// Walks (one per item, value head and column slice) a launch should have to
-// fill the card: two to each of 256 compute units.
+// Walks a launch should have: two to each of 256 compute units, all resident
+// at once.  A launch of the gradients has three walks to an item.
 constexpr int64_t kFill = 512;
 
 Plan plan_of(const gdp_linattn_args &a, bool backward) {
     Plan p;
     p.nseq = a.cu_seqlens ? a.num_seqs : a.B;
-    const int64_t rows = a.B * a.T, HV = a.HV;
+    p.seg_tok = a.T > 0 ? a.T : 1;
+    p.segments = false;
+    p.items = p.nseq;
+    // segments there may be, and sequences' (on average half full) last ones among them
+    const int64_t fill = (backward ? kFill / 3 : kFill) / a.HV;
+    if (p.nseq == 0 || a.T <= 64) return p;
     int64_t seg = a.T;
-    if (a.T > 64 && p.nseq > 0 && p.nseq * HV < kFill) {
-        seg = 1024;
-        while (seg > 64 && cdiv(rows, seg) * HV < kFill) seg /= 2;
+    if (a.cu_seqlens) {
+        const int64_t n = fill - p.nseq / 2;
+        if (p.nseq < fill) seg = cdiv(a.T, n > 1 ? n : 1);
+    } else if (fill >= 2 * a.B) {
+        seg = cdiv(a.T, fill / a.B);
     }
     // backward: the running sums of dg are as long as a segment
-    if (backward && p.nseq > 0 && seg > 1024) seg = 1024;
-    p.segments = seg < a.T;
-    p.seg_tok = p.segments ? seg : (a.T > 0 ? a.T : 1);
-    p.items = !p.segments ? p.nseq : a.cu_seqlens ? cdiv(a.T, seg) + p.nseq : a.B * cdiv(a.T, seg);
+    if (backward && seg > 2048) seg = 2048;
+    seg = (seg + 63) / 64 * 64;
+    if (seg >= a.T) return p;
+    p.segments = true;
+    p.seg_tok = seg;
+    p.items = a.cu_seqlens ? cdiv(a.T, seg) + p.nseq : a.B * cdiv(a.T, seg);
     return p;
 }
 
@@ -78,7 +87,7 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
     s->s_tot = m.take<float>(heads);
     s->r = m.take<float>(heads * E);
     s->r_tot = m.take<float>(heads);
-    s->nq = s->nk = a.K / gdp::lin_slice(a.K);
+    s->nq = s->nk = a.K / gdp::lin_grads_slice(a.K, a.V);
     s->rho_q = m.take<float>(s->nq * BTH);
     s->rho_k = m.take<float>(s->nk * BTH);
     s->part = m.take<double>(p.items * a.HV);
@@ -171,6 +180,7 @@ gdp::LinWalk walk_base(const gdp_linattn_args &a, const Plan &p) {
     w.T = a.T;
     w.nseq = p.nseq;
     w.seg_tok = p.seg_tok;
+    w.items = p.items;
     w.cu = a.cu_seqlens;
     w.g = a.g ? a.g : a.g_head;
     w.g_bs = a.g ? a.g_b_stride : 0;
@@ -223,21 +233,20 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
     w.dc = a.V;
     w.s0 = a.h0;
     if (p.segments) {
-        gdp::LinWalk e = w;
-        e.seg_out = ws.seg;
-        e.seg_tot = ws.tot;
-        if ((st = hip_status(gdp::launch_lin_walk(e, a.dtype, gdp::LIN_SEG, p.items, s), name)) != GDP_OK) return st;
+        gdp::LinWalks e{{w, {}, {}}, 1};
+        e.w[0].seg_out = ws.seg;
+        e.w[0].seg_tot = ws.tot;
+        if ((st = hip_status(gdp::launch_lin_walks(e, a.dtype, false, s), name)) != GDP_OK) return st;
         gdp::LinScan c = scan_base(a, p);
-        c.s0 = a.h0;
-        c.seg = ws.seg;
-        c.tot = ws.tot;
+        c.n = 1;
+        c.s[0] = {false, a.h0, ws.seg, ws.tot};
         if ((st = hip_status(gdp::launch_lin_scan(c, s), name)) != GDP_OK) return st;
         w.seg_in = ws.seg;
     }
     w.sy = a.scale;
     w.y = a.o;
     w.s_out = a.ht;
-    return hip_status(gdp::launch_lin_walk(w, a.dtype, gdp::LIN_OUT, p.items, s), name);
+    return hip_status(gdp::launch_lin_walks({{w, {}, {}}, 1}, a.dtype, true, s), name);
 }
 
 gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads *d, void *workspace,
@@ -286,53 +295,47 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
                        v = rows_of(a.v, a.v_b_stride, a.v_t_stride, a.T, wv, 1),
                        o = rows_of(d->dout, d->do_b_stride, d->do_t_stride, a.T, wv, 1);
     const gdp::LinWalk base = walk_base(a, p);
-    const gdp::LinKind kind = want_g ? gdp::LIN_DOT : gdp::LIN_OUT;
     const bool shared = r > 1;
     // the states S entering every segment, and their gradients entering it from behind
     if (p.segments) {
-        gdp::LinWalk w = base;
-        w.da = a.K;
-        w.dc = a.V;
-        w.b = k;
-        w.c = v;
-        w.seg_out = ws.s;
-        w.seg_tot = ws.s_tot;
-        if ((st = hip_status(gdp::launch_lin_walk(w, a.dtype, gdp::LIN_SEG, p.items, s), name)) != GDP_OK) return st;
-        w.b = q;
-        w.c = o;
-        w.sb = a.scale;
-        w.rev = true;
-        w.seg_out = ws.r;
-        w.seg_tot = ws.r_tot;
-        if ((st = hip_status(gdp::launch_lin_walk(w, a.dtype, gdp::LIN_SEG, p.items, s), name)) != GDP_OK) return st;
+        gdp::LinWalk f = base;
+        f.da = a.K;
+        f.dc = a.V;
+        f.b = k;
+        f.c = v;
+        f.seg_out = ws.s;
+        f.seg_tot = ws.s_tot;
+        gdp::LinWalk b = f;
+        b.b = q;
+        b.c = o;
+        b.sb = a.scale;
+        b.rev = true;
+        b.seg_out = ws.r;
+        b.seg_tot = ws.r_tot;
+        if ((st = hip_status(gdp::launch_lin_walks({{f, b, {}}, 2}, a.dtype, false, s), name)) != GDP_OK)
+            return st;
         gdp::LinScan c = scan_base(a, p);
-        c.s0 = a.h0;
-        c.seg = ws.s;
-        c.tot = ws.s_tot;
-        if ((st = hip_status(gdp::launch_lin_scan(c, s), name)) != GDP_OK) return st;
-        c.s0 = d->dht;
-        c.seg = ws.r;
-        c.tot = ws.r_tot;
-        c.rev = true;
+        c.n = 2;
+        c.s[0] = {false, a.h0, ws.s, ws.s_tot};
+        c.s[1] = {true, d->dht, ws.r, ws.r_tot};
         if ((st = hip_status(gdp::launch_lin_scan(c, s), name)) != GDP_OK) return st;
     }
-    // dq: (do, v, k) forwards from S^T
-    gdp::LinWalk w = base;
-    w.a = o;
-    w.b = v;
-    w.c = k;
-    w.x = q;
-    w.da = a.V;
-    w.dc = a.K;
-    w.trans = true;
-    w.s0 = a.h0;
-    w.seg_in = p.segments ? ws.s : nullptr;
-    w.sy = a.scale;
-    w.y = shared ? (void *)ws.dq : d->dq;
-    w.y32 = shared;
-    w.rho = ws.rho_q;
-    if ((st = hip_status(gdp::launch_lin_walk(w, a.dtype, kind, p.items, s), name)) != GDP_OK) return st;
-    // dk: (v, do, q) backwards from the gradient's transpose
+    // dq: (do, v, k) forwards from S^T; dk: (v, do, q) backwards from the gradient's transpose
+    gdp::LinWalk f = base;
+    f.a = o;
+    f.b = v;
+    f.c = k;
+    f.x = q;
+    f.da = a.V;
+    f.dc = a.K;
+    f.trans = true;
+    f.s0 = a.h0;
+    f.seg_in = p.segments ? ws.s : nullptr;
+    f.sy = a.scale;
+    f.y = shared ? (void *)ws.dq : d->dq;
+    f.y32 = shared;
+    f.rho = ws.rho_q;
+    gdp::LinWalk w = f;
     w.a = v;
     w.b = o;
     w.c = q;
@@ -344,29 +347,25 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     w.sy = 1.0f;
     w.y = shared ? (void *)ws.dk : d->dk;
     w.rho = ws.rho_k;
-    if ((st = hip_status(gdp::launch_lin_walk(w, a.dtype, kind, p.items, s), name)) != GDP_OK) return st;
     // dv: (k, q, do) backwards
-    w.a = k;
-    w.b = q;
-    w.c = o;
-    w.x = gdp::LinRows{};
-    w.da = a.K;
-    w.dc = a.V;
-    w.trans = false;
-    w.y = d->dv;
-    w.y32 = false;
-    w.rho = nullptr;
+    gdp::LinWalk x = w;
+    x.a = k;
+    x.b = q;
+    x.c = o;
+    x.x = gdp::LinRows{};
+    x.da = a.K;
+    x.dc = a.V;
+    x.trans = false;
+    x.y = d->dv;
+    x.y32 = false;
+    x.rho = nullptr;
     // <h0, dh0> anchors dg where one segment has a state before it and a gradient behind it
-    w.s_out = d->dh0 ? d->dh0 : want_g && d->dht && a.h0 ? ws.dh0 : nullptr;
-    if ((st = hip_status(gdp::launch_lin_walk(w, a.dtype, gdp::LIN_OUT, p.items, s), name)) != GDP_OK) return st;
-    if (shared && a.T > 0) {
-        const int64_t tokens = a.B * a.T;
-        if ((st = hip_status(gdp::launch_lin_group(ws.dq, d->dq, a.dtype, tokens, a.H, r, a.K, a.cu_seqlens, p.nseq, s),
-                             name)) != GDP_OK)
-            return st;
-        if ((st = hip_status(gdp::launch_lin_group(ws.dk, d->dk, a.dtype, tokens, a.H, r, a.K, a.cu_seqlens, p.nseq, s),
-                             name)) != GDP_OK)
-            return st;
+    x.s_out = d->dh0 ? d->dh0 : want_g && d->dht && a.h0 ? ws.dh0 : nullptr;
+    if ((st = hip_status(gdp::launch_lin_grads({{f, w, x}, 3}, a.dtype, want_g, s), name)) != GDP_OK) return st;
+    if (shared) {
+        const gdp::LinGroup c{{ws.dq, ws.dk}, {d->dq, d->dk}, a.B * a.T * a.H * (a.K / 4), p.nseq, a.H, r, a.K / 4,
+                              a.cu_seqlens};
+        if ((st = hip_status(gdp::launch_lin_group(c, a.dtype, s), name)) != GDP_OK) return st;
     }
     if (!want_g) return ok();
     g.nq = ws.nq;

@@ -15,8 +15,6 @@ struct LinRows {
     int div = 1;
 };
 
-enum LinKind { LIN_SEG, LIN_OUT, LIN_DOT };
-
 // One walk (linattn.hip): y_i = sum D(i,j) (a_i.b_j) c_j over every sequence,
 // cut into segments of seg_tok rows.
 struct LinWalk {
@@ -24,7 +22,7 @@ struct LinWalk {
     int da, dc;        // columns of a and b, of c (and x, y)
     int HV;
     float sb, sy;      // factors of the products a_i.b_j (and c_j b_j^T), and of y
-    int64_t B, T, nseq, seg_tok;
+    int64_t B, T, nseq, seg_tok, items;
     const int32_t *cu;
     const float *g;    // log decay of (b, t, hv) at g + b*g_bs + t*g_ts + hv, or NULL
     int64_t g_bs, g_ts;
@@ -40,14 +38,22 @@ struct LinWalk {
     float *seg_tot;
 };
 
+// The walks of a launch: one or two of one shape, or the gradients' three.
+struct LinWalks {
+    LinWalk w[3];
+    int n;
+};
+
 struct LinScan {
     const int32_t *cu;
     int64_t T, nseq, seg_tok, elems, items;
-    int HV;
-    bool rev;
-    const float *s0;
-    float *seg;
-    const float *tot;
+    int HV, n;         // states that are scanned
+    struct {
+        bool rev;
+        const float *s0;
+        float *seg;
+        const float *tot;
+    } s[2];
 };
 
 struct LinDg {
@@ -64,14 +70,24 @@ struct LinDg {
     double *part;      // [items, HV] or NULL: sums over each segment
 };
 
-int lin_slice(int dc);
-hipError_t launch_lin_walk(const LinWalk &w, gdp_dtype dtype, LinKind kind, int64_t items, hipStream_t stream);
+// y[i] [B*T, H, D] = sums over r neighbouring heads of x[i] [B*T, H*r, D]
+// (units: 4 elements of y); with cu only the tokens of its requests
+struct LinGroup {
+    const float *x[2];
+    void *y[2];
+    int64_t units, nseq;
+    int H, r, upr;     // upr: units of a head
+    const int32_t *cu;
+};
+
+// out: the rows y (else each segment's state only)
+hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, hipStream_t stream);
+// w[0] dq, w[1] dk, w[2] dv; dot: rho of dq and dk too
+int lin_grads_slice(int K, int V);
+hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream);
 hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream);
 hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream);
-// y [B*T, H, D] = sums over r neighbouring heads of x [B*T, H*r, D]; with cu only the tokens of its requests
-hipError_t launch_lin_group(const float *x, void *y, gdp_dtype dtype, int64_t tokens, int H, int r, int D,
-                            const int32_t *cu, int64_t nseq, hipStream_t stream);
-
+hipError_t launch_lin_group(const LinGroup &p, gdp_dtype dtype, hipStream_t stream);
 hipError_t launch_lin_decode(const gdp_linattn_decode_args &a, hipStream_t stream);
 
 }  // namespace gdp

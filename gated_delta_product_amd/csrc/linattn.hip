@@ -35,10 +35,14 @@ namespace gdp {
 // u ^ swz(r).  16 rows at one unit (operand rows) then fall on 16 units
 // (8 with 8 units a row, two rows to a span of all banks), and 4 rows at 4
 // neighbouring units (the transposed reads) on all banks once.
+// The low bits run 0, 2, 3, 1 over the blocks of 4 rows: a 16-byte read takes
+// lanes 0-3 with 20-23, 4-7 with 16-19 and so on at once, and those then sit
+// on different units too.
 template <int UPR>
 __device__ __forceinline__ int swz(int row) {
-    if constexpr (UPR == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
-    else return ((row & 3) << 2) | ((row >> 2) & 3);
+    const int low = (0x78 >> (2 * ((row >> 2) & 3))) & 3;
+    if constexpr (UPR == 8) return (((row >> 1) & 1) << 2) | low;
+    else return ((row & 3) << 2) | low;
 }
 template <typename T, int D>
 struct Tile {
@@ -549,14 +553,39 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         *(f32x4 *)(so + col * DA + 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2)) = s[kt] * f;
 }
 
+// The block's item, value head and column slice.
 template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
-__global__ void __launch_bounds__((Walk<T, DA, DC, NS, NQ, OUT, DOT>::NT), (Walk<T, DA, DC, NS, NQ, OUT, DOT>::OCC))
-gdp_lin_walk_k(LinWalk w) {
-    __shared__ __align__(16) typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds sm;
-    const int slices = w.dc / DC;
-    const uint32_t b = blockIdx.x, per = (uint32_t)w.HV * slices;
+__device__ __forceinline__ void lin_block(const LinWalk &w, void *lds) {
+    const uint32_t b = blockIdx.x, slices = w.dc / DC, per = (uint32_t)w.HV * slices;
     const uint32_t id = b / per, r = b - id * per;
-    lin_walk<T, DA, DC, NS, NQ, OUT, DOT>(w, id, (int)(r / slices), (int)(r % slices), sm);
+    if (id >= w.items) return;
+    lin_walk<T, DA, DC, NS, NQ, OUT, DOT>(w, id, (int)(r / slices), (int)(r % slices),
+                                          *(typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds *)lds);
+}
+
+template <typename T, int DA, int DC, int NS, bool OUT>
+__global__ void __launch_bounds__((Walk<T, DA, DC, NS, 1, OUT, false>::NT), (Walk<T, DA, DC, NS, 1, OUT, false>::OCC))
+gdp_lin_walk_k(LinWalks p) {
+    typedef Walk<T, DA, DC, NS, 1, OUT, false> W;
+    __shared__ __align__(16) char lds[sizeof(typename W::Lds)];
+    lin_block<T, DA, DC, NS, 1, OUT, false>(p.w[blockIdx.y], lds);
+}
+
+// The three walks of the gradients in one launch: dq and dk (DA = V, slices of
+// K columns) and dv (DA = K, slices of V columns), all in slices of SL.
+template <typename T, int K, int V, int SL, int NS, int NQ, bool DOT>
+struct Grads {
+    typedef Walk<T, V, SL, NS, NQ, true, DOT> QK;
+    typedef Walk<T, K, SL, NS, 1, true, false> D;
+    static constexpr int OCC = QK::OCC < D::OCC ? QK::OCC : D::OCC;
+    static constexpr int BYTES = sizeof(typename QK::Lds) > sizeof(typename D::Lds) ? sizeof(typename QK::Lds)
+                                                                                   : sizeof(typename D::Lds);
+};
+template <typename T, int K, int V, int SL, int NS, int NQ, bool DOT>
+__global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, DOT>::OCC)) gdp_lin_grads_k(LinWalks p) {
+    __shared__ __align__(16) char lds[Grads<T, K, V, SL, NS, NQ, DOT>::BYTES];
+    if (blockIdx.y < 2) lin_block<T, V, SL, NS, NQ, true, DOT>(p.w[blockIdx.y], lds);
+    else lin_block<T, K, SL, NS, 1, true, false>(p.w[2], lds);
 }
 
 // ---------------------------------------------------------------- the scan over segments
@@ -587,19 +616,21 @@ __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
     if (slot0 + nseg > p.items) return;  // overlapping requests: out of slots
     const int64_t i = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
     if (i >= p.elems) return;
+    const auto &sc = p.s[blockIdx.z];
+    const bool rev = sc.rev;
     const int64_t step = p.HV * p.elems;
     f32x4 cur = zero4();
-    if (p.s0) cur = *(const f32x4 *)(p.s0 + (seq * p.HV + hv) * p.elems + i);
+    if (sc.s0) cur = *(const f32x4 *)(sc.s0 + (seq * p.HV + hv) * p.elems + i);
     const int64_t last = nseg - 1;
-    float *base = p.seg + (slot0 * p.HV + hv) * p.elems + i;
-    const float *tot = p.tot + slot0 * p.HV + hv;
+    float *base = sc.seg + (slot0 * p.HV + hv) * p.elems + i;
+    const float *tot = sc.tot + slot0 * p.HV + hv;
     constexpr int U = 8;  // segments in flight
     for (int64_t k0 = 0; k0 < nseg; k0 += U) {
         f32x4 e[U];
         float f[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u, sg = p.rev ? nseg - 1 - k : k;
+            const int64_t k = k0 + u, sg = rev ? nseg - 1 - k : k;
             e[u] = zero4();
             f[u] = 1.f;
             if (k < last) {
@@ -609,7 +640,7 @@ __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u, sg = p.rev ? nseg - 1 - k : k;
+            const int64_t k = k0 + u, sg = rev ? nseg - 1 - k : k;
             if (k >= nseg) break;
             *(f32x4 *)(base + sg * step) = cur;
             cur = cur * f[u] + e[u];
@@ -730,70 +761,78 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_head_k(const double *part, int
 // left alone (requests follow each other, so those lie before the first
 // offset or behind the last).
 template <typename T>
-__global__ void __launch_bounds__(256) gdp_lin_group_k(const float *x, T *y, int64_t units, int H, int r, int upr,
-                                                       const int32_t *cu, int64_t nseq) {
+__global__ void __launch_bounds__(256) gdp_lin_group_k(LinGroup p) {
     const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (u >= units) return;
-    const int64_t row = u / upr;  // (token, key head)
-    if (cu) {
-        const int64_t t = row / H;
-        if (t < cu[0] || t >= cu[nseq]) return;
+    if (u >= p.units) return;
+    const int64_t row = u / p.upr;  // (token, key head)
+    if (p.cu) {
+        const int64_t t = row / p.H;
+        if (t < p.cu[0] || t >= p.cu[p.nseq]) return;
     }
-    const float *p = x + (row * r * upr + u % upr) * 4;
-    f32x4 s = *(const f32x4 *)p;
-    for (int i = 1; i < r; ++i) s += *(const f32x4 *)(p + (int64_t)i * upr * 4);
+    const float *x = p.x[blockIdx.y] + (row * p.r * p.upr + u % p.upr) * 4;
+    f32x4 s = *(const f32x4 *)x;
+    for (int i = 1; i < p.r; ++i) s += *(const f32x4 *)(x + (int64_t)i * p.upr * 4);
     typename Frag<T>::half o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = from_f32<T>(s[i]);
-    *(typename Frag<T>::half *)(y + u * 4) = o;
+    *(typename Frag<T>::half *)((T *)p.y[blockIdx.y] + u * 4) = o;
 }
 
 // ---------------------------------------------------------------- launches
-template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
-static hipError_t launch_walk_t(const LinWalk &w, int64_t items, hipStream_t stream) {
-    const int64_t blocks = items * w.HV * (w.dc / DC);
+template <typename T, int DA, int DC, int NS, bool OUT>
+static hipError_t launch_walk_t(const LinWalks &w, hipStream_t stream) {
+    const int64_t blocks = w.w[0].items * w.w[0].HV * (w.w[0].dc / DC);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, NQ, OUT, DOT>), dim3((unsigned)blocks),
-                       dim3(Walk<T, DA, DC, NS, NQ, OUT, DOT>::NT), 0, stream, w);
+    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, OUT>), dim3((unsigned)blocks, w.n), dim3(4 * DC), 0, stream, w);
     return hipGetLastError();
 }
 
-// Columns of c that one walk takes.
-int lin_slice(int dc) { return dc < 128 ? dc : 128; }
+template <typename T, int NS, bool OUT>
+static hipError_t launch_walk_dims(const LinWalks &w, hipStream_t stream) {
+    const int da = w.w[0].da, dc = w.w[0].dc;
+    if (da == 64) return dc == 64 ? launch_walk_t<T, 64, 64, NS, OUT>(w, stream) : launch_walk_t<T, 64, 128, NS, OUT>(w, stream);
+    return dc == 64 ? launch_walk_t<T, 128, 64, NS, OUT>(w, stream) : launch_walk_t<T, 128, 128, NS, OUT>(w, stream);
+}
 
-template <typename T, int NS, int NQ, bool OUT, bool DOT>
-static hipError_t launch_walk_dims(const LinWalk &w, int64_t items, hipStream_t stream) {
-    switch (w.da * 1000 + lin_slice(w.dc)) {
-    case 64064: return launch_walk_t<T, 64, 64, NS, NQ, OUT, DOT>(w, items, stream);
-    case 64128: return launch_walk_t<T, 64, 128, NS, NQ, OUT, DOT>(w, items, stream);
-    case 128064: return launch_walk_t<T, 128, 64, NS, NQ, OUT, DOT>(w, items, stream);
-    case 128128: return launch_walk_t<T, 128, 128, NS, NQ, OUT, DOT>(w, items, stream);
-    case 256064: return launch_walk_t<T, 256, 64, NS, NQ, OUT, DOT>(w, items, stream);
-    case 256128: return launch_walk_t<T, 256, 128, NS, NQ, OUT, DOT>(w, items, stream);
+hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, hipStream_t stream) {
+    if (w.w[0].items == 0) return hipSuccess;
+    if (dtype == GDP_F32) return out ? launch_walk_dims<float, 1, true>(w, stream) : launch_walk_dims<float, 1, false>(w, stream);
+    return out ? launch_walk_dims<bf16, 3, true>(w, stream) : launch_walk_dims<bf16, 3, false>(w, stream);
+}
+
+// Columns of c that one walk of the gradients takes: as many waves in each of the three.
+int lin_grads_slice(int K, int V) { return K == 64 || V == 64 ? 64 : 128; }
+
+template <typename T, int K, int V, int NS, int NQ, bool DOT>
+static hipError_t launch_grads_t(const LinWalks &w, hipStream_t stream) {
+    constexpr int SL = K == 64 || V == 64 ? 64 : 128;
+    const int64_t most = w.w[0].items * w.w[0].HV * ((K > V ? K : V) / SL);
+    if (most > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gdp_lin_grads_k<T, K, V, SL, NS, NQ, DOT>), dim3((unsigned)most, 3), dim3(4 * SL), 0, stream, w);
+    return hipGetLastError();
+}
+template <typename T, int NS, int NQ, bool DOT>
+static hipError_t launch_grads_dims(const LinWalks &w, hipStream_t stream) {
+    switch (w.w[2].da * 1000 + w.w[2].dc) {
+    case 64064: return launch_grads_t<T, 64, 64, NS, NQ, DOT>(w, stream);
+    case 64128: return launch_grads_t<T, 64, 128, NS, NQ, DOT>(w, stream);
+    case 64256: return launch_grads_t<T, 64, 256, NS, NQ, DOT>(w, stream);
+    case 128064: return launch_grads_t<T, 128, 64, NS, NQ, DOT>(w, stream);
+    case 128128: return launch_grads_t<T, 128, 128, NS, NQ, DOT>(w, stream);
+    case 128256: return launch_grads_t<T, 128, 256, NS, NQ, DOT>(w, stream);
     default: return hipErrorInvalidValue;
     }
 }
-
-hipError_t launch_lin_walk(const LinWalk &w, gdp_dtype dtype, LinKind kind, int64_t items, hipStream_t stream) {
-    if (items == 0) return hipSuccess;
-    if (dtype == GDP_F32) {
-        switch (kind) {
-        case LIN_SEG: return launch_walk_dims<float, 1, 1, false, false>(w, items, stream);
-        case LIN_OUT: return launch_walk_dims<float, 1, 1, true, false>(w, items, stream);
-        case LIN_DOT: return launch_walk_dims<float, 1, 1, true, true>(w, items, stream);
-        }
-    }
-    switch (kind) {
-    case LIN_SEG: return launch_walk_dims<bf16, 3, 1, false, false>(w, items, stream);
-    case LIN_OUT: return launch_walk_dims<bf16, 3, 1, true, false>(w, items, stream);
-    case LIN_DOT: return launch_walk_dims<bf16, 3, 3, true, true>(w, items, stream);
-    }
-    return hipErrorInvalidValue;
+hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream) {
+    if (w.w[0].items == 0) return hipSuccess;
+    if (dtype == GDP_F32)
+        return dot ? launch_grads_dims<float, 1, 1, true>(w, stream) : launch_grads_dims<float, 1, 1, false>(w, stream);
+    return dot ? launch_grads_dims<bf16, 3, 3, true>(w, stream) : launch_grads_dims<bf16, 3, 1, false>(w, stream);
 }
 
 hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
     if (p.nseq == 0) return hipSuccess;
-    hipLaunchKernelGGL(gdp_lin_scan_k, dim3((unsigned)(p.nseq * p.HV), (unsigned)(p.elems / 1024)), dim3(256), 0,
+    hipLaunchKernelGGL(gdp_lin_scan_k, dim3((unsigned)(p.nseq * p.HV), (unsigned)(p.elems / 1024), p.n), dim3(256), 0,
                        stream, p);
     return hipGetLastError();
 }
@@ -809,17 +848,11 @@ hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_lin_group(const float *x, void *y, gdp_dtype dtype, int64_t tokens, int H, int r, int D,
-                            const int32_t *cu, int64_t nseq, hipStream_t stream) {
-    const int64_t units = tokens * H * (D / 4);
-    if (units == 0) return hipSuccess;
-    const dim3 grid((unsigned)((units + 255) / 256));
-    if (dtype == GDP_BF16)
-        hipLaunchKernelGGL(gdp_lin_group_k<bf16>, grid, dim3(256), 0, stream, x, (bf16 *)y, units, H, r, D / 4, cu,
-                           nseq);
-    else
-        hipLaunchKernelGGL(gdp_lin_group_k<float>, grid, dim3(256), 0, stream, x, (float *)y, units, H, r, D / 4,
-                           cu, nseq);
+hipError_t launch_lin_group(const LinGroup &p, gdp_dtype dtype, hipStream_t stream) {
+    if (p.units == 0) return hipSuccess;
+    const dim3 grid((unsigned)((p.units + 255) / 256), 2);
+    if (dtype == GDP_BF16) hipLaunchKernelGGL(gdp_lin_group_k<bf16>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(gdp_lin_group_k<float>, grid, dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
