@@ -224,7 +224,9 @@ struct Walk {
     // waves a SIMD: two blocks to a compute unit where their LDS fits (and
     // with 256 rows of S^T a wave needs the registers of two)
     static constexpr int OCC = DA == 256 ? (WV == 8 ? 2 : 1) : WV / 2;
-    static constexpr int KG = OUT && OCC >= 4 ? 2 : 4;
+    // tiles whose operands are loaded together: fewer where registers are
+    // short (a spill's reload would wait for every row in flight)
+    static constexpr int KG = OUT && OCC >= 4 ? 2 : 4, IG = OCC >= 4 ? 2 : NB;
     static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
@@ -251,20 +253,14 @@ template <typename T, int D, int NT, int UNITS>
 struct Rows {
     static constexpr int E = 16 / sizeof(T), UPR = D / E, STEP = NT / UPR;
     uint4 r[UNITS];
-    uint32_t step;  // bytes between a thread's rows (negative going backwards)
-    uint32_t off;   // of its first row in a whole chunk
-    uint32_t ts;    // bytes of a row
-    __device__ __forceinline__ void init(int64_t ts_elems, bool rev, int rows) {
-        ts = (uint32_t)ts_elems * sizeof(T);
-        const int row = threadIdx.x / UPR;
-        off = (uint32_t)(rev ? rows - 1 - row : row) * ts + threadIdx.x % UPR * 16;
-        step = rev ? 0u - STEP * ts : STEP * ts;
-    }
-    __device__ __forceinline__ void fetch(const T *base, int n, bool rev, int rows) {
+    __device__ __forceinline__ void fetch(const T *base, int64_t ts_elems, int n, bool rev, int tid) {
+        const uint32_t ts = (uint32_t)ts_elems * sizeof(T);  // bytes of a row
         const rsrc_t rs = make_rsrc(base, (uint32_t)(n - 1) * ts + D * sizeof(T));
-        const uint32_t o = off - (rev ? (uint32_t)(rows - n) * ts : 0u);
+        const int row = tid / UPR;
+        const uint32_t off = (uint32_t)(rev ? n - 1 - row : row) * ts + tid % UPR * 16;
+        const uint32_t step = rev ? 0u - STEP * ts : STEP * ts;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) r[i] = buf_load16(rs, o + i * step);
+        for (int i = 0; i < UNITS; ++i) r[i] = buf_load16(rs, off + i * step);
     }
     __device__ __forceinline__ void stage(T *t, int tid) const {
         if constexpr (STEP % 16 == 0) {  // whole periods of the swizzle
@@ -309,25 +305,23 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
     Rows<T, DA, NT, W::UA> ra, rb;
     Rows<T, DC, NT, W::UC> rc, rx;
-    if constexpr (OUT) ra.init(w.a.ts, w.rev, CT);
-    rb.init(w.b.ts, w.rev, CT);
-    rc.init(w.c.ts, w.rev, CT);
-    if constexpr (DOT) rx.init(w.x.ts, w.rev, CT);
     const bool decayer = wave == W::WV - 1;  // the wave that forms the decays (it has fewer score tiles)
     float rg = 0.f;
-    // rows [c0, c0 + n) of the walk into registers (g: one row a lane)
+    // rows [c0, c0 + n) of the walk into registers (g: one row a lane, asked for
+    // first, so that the wait for it leaves the rows in flight)
     auto fetch = [&](int64_t c0, int n) {
         const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
-        if constexpr (OUT) ra.fetch(pa + first * w.a.ts, n, w.rev, CT);
-        rb.fetch(pb + first * w.b.ts, n, w.rev, CT);
-        rc.fetch(pc + first * w.c.ts, n, w.rev, CT);
-        if constexpr (DOT) rx.fetch(px + first * w.x.ts, n, w.rev, CT);
+        const int tid = wave * 64 + lane;
         rg = 0.f;
-        if (pg && decayer && lane < n) {
+        if (pg && decayer) {
             // backwards, a row is entered through the decay of the row after it
             const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
-            if (t < eos_in) rg = pg[t * w.g_ts];
+            if (lane < n && t < eos_in) rg = pg[t * w.g_ts];
         }
+        if constexpr (OUT) ra.fetch(pa + first * w.a.ts, w.a.ts, n, w.rev, tid);
+        rb.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
+        rc.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
+        if constexpr (DOT) rx.fetch(px + first * w.x.ts, w.x.ts, n, w.rev, tid);
     };
     float tot = 0.f;  // log2 decay of the whole walk (in the decayer), for the segment pass
     auto decays = [&](int n, int buf) {
@@ -354,17 +348,19 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         const float *s0 = nullptr;
         if (w.seg_in) s0 = w.seg_in + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
         else if (OUT && w.s0) s0 = w.s0 + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
+        if (!s0) {
 #pragma unroll
-        for (int kt = 0; kt < W::KT; ++kt) {
-            s[kt] = zero4();
-            if (!s0) continue;
-            const int a = 32 * (kt / 2) + 8 * g4 + 4 * (kt % 2);
-            if (w.trans) {
+            for (int kt = 0; kt < W::KT; ++kt) s[kt] = zero4();
+        } else if (w.trans) {
+            const float *q = s0 + 8 * g4 * w.dc + col;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[kt][i] = s0[(a + i) * w.dc + col];
-            } else {
-                s[kt] = *(const f32x4 *)(s0 + col * DA + a);
-            }
+            for (int kt = 0; kt < W::KT; ++kt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[kt][i] = q[(32 * (kt / 2) + 4 * (kt % 2) + i) * w.dc];
+        } else {
+            const float *q = s0 + col * DA + 8 * g4;
+#pragma unroll
+            for (int kt = 0; kt < W::KT; ++kt) s[kt] = *(const f32x4 *)(q + 32 * (kt / 2) + 4 * (kt % 2));
         }
     }
     // tiles above the diagonal of P stay zero (a 32-row contraction of an even block reads one)
@@ -438,13 +434,16 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = s[2 * kb + i / 4][i % 4];
                 split8<T, NQ>(v, sp);
-                frag fa[W::NB];
 #pragma unroll
-                for (int ib = 0; ib < W::NB; ++ib) fa[ib] = TA::row8(sm.a, arow, ib, kb);
+                for (int i0 = 0; i0 < W::NB; i0 += W::IG) {
+                    frag fa[W::IG];
 #pragma unroll
-                for (int p = NQ - 1; p >= 0; --p)
+                    for (int i = 0; i < W::IG; ++i) fa[i] = TA::row8(sm.a, arow, i0 + i, kb);
 #pragma unroll
-                    for (int ib = 0; ib < W::NB; ++ib) y[ib] = mma(sp[p], fa[ib], y[ib]);
+                    for (int p = NQ - 1; p >= 0; --p)
+#pragma unroll
+                        for (int i = 0; i < W::IG; ++i) y[i0 + i] = mma(sp[p], fa[i], y[i0 + i]);
+                }
             }
 #pragma unroll
             for (int ib = 0; ib < W::NB; ++ib) {
@@ -511,13 +510,18 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             const uint32_t es = w.y32 ? 4 : sizeof(T), ys = (uint32_t)w.HV * w.dc * es;
             const rsrc_t rs = make_rsrc((const char *)w.y + e * es, (uint32_t)(n - 1) * ys + 16 * es);
             const uint32_t off = (uint32_t)(w.rev ? n - 1 - m : m) * ys + 4 * g4 * es, step = w.rev ? 0u - 16 * ys : 16 * ys;
+            const float sy = w.sy;
+            if (F32_Y<T> || w.y32) {
 #pragma unroll
-            for (int ib = 0; ib < W::NB; ++ib) {
-                const f32x4 v = y[ib] * w.sy;
-                if (F32_Y<T> || w.y32) {
+                for (int ib = 0; ib < W::NB; ++ib) {
+                    const f32x4 v = y[ib] * sy;
                     buf_store16(rs, off + ib * step, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
                                                                 __float_as_uint(v[2]), __float_as_uint(v[3])));
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int ib = 0; ib < W::NB; ++ib) {
+                    const f32x4 v = y[ib] * sy;
                     const bf16x4 o = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                     buf_store8(rs, off + ib * step, __builtin_bit_cast(uint2, o));
                 }
