@@ -620,65 +620,92 @@ def decode_update(q, k, v, beta, g, state, M, slots=None, scale=None, o=None):
 
 
 # ------------------------------------------------------------------ linear attention
+#
+# These calls are made once a layer and token in decoding, where the host sets
+# the pace: pointers go over as plain integers and every attribute of a tensor
+# is asked for once.
 
-def _rows(t, name, shape, dtype, dev):
+def _call(dev, fn, *args):
+    """fn(*args, stream) on the tensors' device and its current stream."""
+    i = dev.index
+    if torch._C._cuda_getDevice() == i:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status != GDP_OK:
+        raise GdpError(status, lib().gdp_last_error().decode())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, name, shape, dtype):
     """Checks a [n, T, heads, D] tensor whose rows [heads, D] are contiguous; its batch and token strides."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.dtype != dtype:
         raise ValueError("q, k, v and %s must share a dtype" % name)
-    if t.device != dev:
-        raise ValueError("tensors on different devices")
-    if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+    s = t.stride()
+    if (s[3] != 1 and shape[3] > 1) or (s[2] != shape[3] and shape[2] > 1):
         raise ValueError("the heads of %s must be contiguous" % name)
-    return t.stride(0), t.stride(1)
+    return s[0], s[1]
 
 
-def _lin_common(q, k, v, g, scale, extra=()):
-    """Dimensions, strides and decay fields shared by the linear-attention calls."""
-    dev = _need_cuda(q, k, v, g, *extra)
+def _decay(g, n, T, HV):
+    """(g, batch stride, token stride, g_head) of a decay per token [n, T, HV], per head [HV], or None."""
+    if g is None:
+        return None, 0, 0, None
+    if g.dtype != torch.float32:
+        raise ValueError("g must be float32")
+    if g.dim() == 1:
+        if g.shape[0] != HV or not g.is_contiguous():
+            raise ValueError("a decay per head must be a contiguous [HV]")
+        return None, 0, 0, g.data_ptr()
+    s = g.stride()
+    if g.shape != (n, T, HV) or (HV > 1 and s[2] != 1):
+        raise ValueError("g must be [n, T, HV] with a contiguous last dimension, or [HV]")
+    return g.data_ptr(), s[0], s[1], None
+
+
+def _qkv(q, k, v):
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be 4-D")
-    n, T, H, K = q.shape
-    HV, V = v.shape[2], v.shape[3]
-    f = dict(H=H, HV=HV, K=K, V=V, scale=float(scale) if scale is not None else 0.0, dtype=_dtype_code(q.dtype))
-    strides = [_rows(t, nm, s, q.dtype, dev) for t, nm, s in
-               ((q, "q", (n, T, H, K)), (k, "k", (n, T, H, K)), (v, "v", (n, T, HV, V)))]
-    gs = (0, 0)
-    if g is not None:
-        if g.dtype != torch.float32:
-            raise ValueError("g must be float32")
-        if g.dim() == 1:
-            if tuple(g.shape) != (HV,) or not g.is_contiguous():
-                raise ValueError("a decay per head must be a contiguous [HV]")
-            f["g_head"] = g.data_ptr()
-        else:
-            if tuple(g.shape) != (n, T, HV) or (HV > 1 and g.stride(2) != 1):
-                raise ValueError("g must be [n, T, HV] with a contiguous last dimension, or [HV]")
-            gs = (g.stride(0), g.stride(1))
-            f["g"] = g.data_ptr()
-    return dev, n, T, f, strides, gs
+    shape = q.shape
+    n, T, H, K = shape
+    HV, V = v.shape[2:]
+    dt = q.dtype
+    return (n, T, H, HV, K, V, _dtype_code(dt), _rows(q, "q", shape, dt), _rows(k, "k", shape, dt),
+            _rows(v, "v", (n, T, HV, V), dt))
 
 
-def _state(t, name, shape, dev):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous()
-                          or t.device != dev):
+def _state(t, name, shape):
+    if t is not None and (t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous()):
         raise ValueError("%s must be a contiguous float32 %s" % (name, list(shape)))
 
 
-def _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, extra=()):
-    dev, B, T, f, (qs, ks, vs), gs = _lin_common(q, k, v, g, scale, (cu_seqlens, initial_state) + tuple(extra))
+def _output(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s" % (name, dtype, list(shape)))
+    return t
+
+
+def _lin_args(q, k, v, g, scale, cu_seqlens, initial_state):
+    B, T, H, HV, K, V, code, qs, ks, vs = _qkv(q, k, v)
     nseq = B
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
         _contig(cu_seqlens, "cu_seqlens")
         nseq = cu_seqlens.numel() - 1
-    _state(initial_state, "initial_state", (nseq, f["HV"], f["V"], f["K"]), dev)
-    a = LinattnArgs(B=B, T=T, cu_seqlens=_ptr(cu_seqlens), num_seqs=nseq, q=_ptr(q), q_b_stride=qs[0],
-                    q_t_stride=qs[1], k=_ptr(k), k_b_stride=ks[0], k_t_stride=ks[1], v=_ptr(v), v_b_stride=vs[0],
-                    v_t_stride=vs[1], g_b_stride=gs[0], g_t_stride=gs[1], h0=_ptr(initial_state), **f)
-    return dev, nseq, a
+    _state(initial_state, "initial_state", (nseq, HV, V, K))
+    gp, gb, gt, gh = _decay(g, B, T, HV)
+    return nseq, LinattnArgs(B, T, H, HV, K, V, 0.0 if scale is None else scale, code, _at(cu_seqlens), nseq,
+                             q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                             gp, gb, gt, gh, _at(initial_state))
 
 
 def _workspace(need, dev):
@@ -698,17 +725,18 @@ def linattn_fwd(q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=None
     None; initial_state [nseq, HV, V, K] float32 or None.  ``o`` may hold a
     preallocated contiguous output.  Returns (o [B, T, HV, V], ht
     [nseq, HV, V, K] float32 or None)."""
-    dev, nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, (o,))
-    shape = (a.B, a.T, a.HV, a.V)
-    if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
-    elif tuple(o.shape) != shape or o.dtype != q.dtype or not o.is_contiguous():
-        raise ValueError("o must be a contiguous %s %s" % (q.dtype, list(shape)))
-    ht = torch.empty((nseq, a.HV, a.V, a.K), dtype=torch.float32, device=dev) if output_final_state else None
-    a.o, a.ht = _ptr(o), _ptr(ht)
-    with torch.cuda.device(dev):
-        ws = _workspace(lib().gdp_linattn_workspace_bytes(ctypes.byref(a), 0), dev)
-        _check(lib().gdp_linattn_fwd(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    dev = _need_cuda(q, k, v, g, cu_seqlens, initial_state, o)
+    nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state)
+    o = _output(o, "o", (a.B, a.T, a.HV, a.V), q.dtype, dev)
+    a.o = o.data_ptr()
+    ht = None
+    if output_final_state:
+        ht = torch.empty((nseq, a.HV, a.V, a.K), dtype=torch.float32, device=dev)
+        a.ht = ht.data_ptr()
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_linattn_workspace_bytes(pa, 0)
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_linattn_fwd, pa, _at(ws), need)
     return o, ht
 
 
@@ -719,9 +747,10 @@ def linattn_bwd(do, q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=
     head, dv [B, T, HV, V], dg shaped as g (None without g), dh0
     [nseq, HV, V, K] float32 (None without initial_state).  Rows of tokens
     outside every request hold zeros."""
-    dev, nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state, (do, dht))
-    dos = _rows(do, "do", v.shape, q.dtype, dev)
-    _state(dht, "dht", (nseq, a.HV, a.V, a.K), dev)
+    dev = _need_cuda(q, k, v, g, cu_seqlens, initial_state, do, dht)
+    nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state)
+    ds = _rows(do, "do", v.shape, q.dtype)
+    _state(dht, "dht", (nseq, a.HV, a.V, a.K))
     new = torch.empty if cu_seqlens is None else torch.zeros
     dq = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
     dk = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
@@ -731,13 +760,12 @@ def linattn_bwd(do, q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=
     if g is not None:
         dg = (torch.empty if per_head else new)(g.shape, dtype=torch.float32, device=dev)
     dh0 = None if initial_state is None else torch.empty_like(initial_state)
-    d = LinattnGrads(dout=_ptr(do), do_b_stride=dos[0], do_t_stride=dos[1], dht=_ptr(dht), dq=_ptr(dq), dk=_ptr(dk),
-                     dv=_ptr(dv), dg=None if per_head else _ptr(dg), dg_head=_ptr(dg) if per_head else None,
-                     dh0=_ptr(dh0))
-    with torch.cuda.device(dev):
-        ws = _workspace(lib().gdp_linattn_workspace_bytes(ctypes.byref(a), 1), dev)
-        _check(lib().gdp_linattn_bwd(ctypes.byref(a), ctypes.byref(d), _ptr(ws), 0 if ws is None else ws.numel(),
-                                     _stream(dev)))
+    d = LinattnGrads(do.data_ptr(), ds[0], ds[1], _at(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                     None if per_head else _at(dg), _at(dg) if per_head else None, _at(dh0))
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_linattn_workspace_bytes(pa, 1)
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_linattn_bwd, pa, ctypes.byref(d), _at(ws), need)
     return dq, dk, dv, dg, dh0
 
 
@@ -747,21 +775,18 @@ def linattn_decode(q, k, v, state, g=None, slots=None, scale=None, o=None):
     float32 [n, S, HV], [HV] or None; state [pool, HV, V, K] float32, updated
     in place; slots int32 [n] (outside [0, pool): skipped, its o rows zero) or
     None.  Returns o [n, S, HV, V]."""
-    dev, n, S, f, (qs, ks, vs), gs = _lin_common(q, k, v, g, scale, (state, slots, o))
-    if state.dim() != 4:
-        raise ValueError("state must be [pool, HV, V, K]")
-    _state(state, "state", (state.shape[0], f["HV"], f["V"], f["K"]), dev)
-    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (n,) or not slots.is_contiguous()):
+    dev = _need_cuda(q, k, v, g, state, slots, o)
+    n, S, H, HV, K, V, code, qs, ks, vs = _qkv(q, k, v)
+    pool = state.shape[0] if state.dim() else 0
+    _state(state, "state", (pool, HV, V, K))
+    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous()):
         raise ValueError("slots must be a contiguous int32 [n]")
-    if o is None:
-        o = torch.empty((n, S, f["HV"], f["V"]), dtype=q.dtype, device=dev)
-    elif tuple(o.shape) != tuple(v.shape) or o.dtype != q.dtype or not o.is_contiguous():
-        raise ValueError("o must be a contiguous %s %s" % (q.dtype, list(v.shape)))
-    a = LinattnDecodeArgs(n=n, S=S, pool=state.shape[0], q=_ptr(q), q_n_stride=qs[0], q_t_stride=qs[1], k=_ptr(k),
-                          k_n_stride=ks[0], k_t_stride=ks[1], v=_ptr(v), v_n_stride=vs[0], v_t_stride=vs[1],
-                          g_n_stride=gs[0], g_t_stride=gs[1], state=_ptr(state), slots=_ptr(slots), o=_ptr(o), **f)
-    with torch.cuda.device(dev):
-        _check(lib().gdp_linattn_decode(ctypes.byref(a), _stream(dev)))
+    o = _output(o, "o", (n, S, HV, V), q.dtype, dev)
+    gp, gb, gt, gh = _decay(g, n, S, HV)
+    a = LinattnDecodeArgs(n, S, H, HV, K, V, 0.0 if scale is None else scale, code, pool, q.data_ptr(), qs[0], qs[1],
+                          k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], gp, gb, gt, gh, state.data_ptr(),
+                          _at(slots), o.data_ptr())
+    _call(dev, lib().gdp_linattn_decode, ctypes.byref(a))
     return o
 
 
@@ -770,14 +795,15 @@ def linattn_decode(q, k, v, state, g=None, slots=None, scale=None, o=None):
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
 
 
-def _token_rows(t, name, like=None):
+def _token_rows(t, name):
     """[..., C] with a contiguous last dimension as (n, T, n stride, t stride): leading dimensions beyond two
     have to fold into the first."""
-    if t.dim() < 1 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 1 or (strides[-1] != 1 and shape[-1] > 1):
         raise ValueError("the last dimension of %s must be contiguous" % name)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError("%s must match x: %s %s" % (name, like.dtype, list(like.shape)))
-    lead, strides = list(t.shape[:-1]), list(t.stride()[:-1])
+    if len(shape) == 2:
+        return 1, shape[0], 0, strides[0]
+    lead, strides = list(shape[:-1]), list(strides[:-1])
     while len(lead) < 2:
         lead.insert(0, 1)
         strides.insert(0, 0)
@@ -788,24 +814,26 @@ def _token_rows(t, name, like=None):
     return lead[0], lead[1], strides[0], strides[1]
 
 
-def _norm_args(x, groups, weight, bias, gate, activation, centered, eps, extra=()):
-    dev = _need_cuda(x, weight, bias, gate, *extra)
-    if activation not in ACTIVATIONS:
+def _like(t, name, x):
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError("%s must match x: %s %s" % (name, x.dtype, list(x.shape)))
+    return _token_rows(t, name)[2:]
+
+
+def _norm_args(x, groups, weight, bias, gate, activation, centered, eps):
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s" % sorted(k for k in ACTIVATIONS if k))
-    C = x.shape[-1]
-    if groups < 1 or C % groups or C < 1:
-        raise ValueError("the %d channels do not split into %d groups" % (C, groups))
     n, T, ns, ts = _token_rows(x, "x")
+    C = x.shape[-1]
+    if groups < 1 or C < 1 or C % groups:
+        raise ValueError("the %d channels do not split into %d groups" % (C, groups))
     for t, nm in ((weight, "weight"), (bias, "bias")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (C,) or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (C,) or not t.is_contiguous()):
             raise ValueError("%s must be a contiguous float32 [C]" % nm)
-    a = GroupNormArgs(n=n, T=T, groups=groups, D=C // groups, dtype=_dtype_code(x.dtype),
-                      activation=ACTIVATIONS[activation], centered=1 if centered else 0, eps=float(eps), x=_ptr(x),
-                      x_n_stride=ns, x_t_stride=ts, w=_ptr(weight), b=_ptr(bias))
-    if gate is not None:
-        zn, zT, a.z_n_stride, a.z_t_stride = _token_rows(gate, "gate", x)
-        a.z = _ptr(gate)
-    return dev, a
+    zs = (0, 0) if gate is None else _like(gate, "gate", x)
+    return GroupNormArgs(n, T, groups, C // groups, _dtype_code(x.dtype), act, 1 if centered else 0, eps,
+                         x.data_ptr(), ns, ts, _at(gate), zs[0], zs[1], _at(weight), _at(bias))
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="silu", centered=True, eps=1e-5, out=None):
@@ -814,14 +842,11 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="sil
     float32 or None), then times activation(gate), or without a gate through the activation ("silu", "sigmoid",
     "none").  gate is shaped as x; both may be slices of wider rows.  Returns y, contiguous (``out`` if given; it
     may be x or gate)."""
-    dev, a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps, (out,))
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
-        raise ValueError("out must be a contiguous %s %s" % (x.dtype, list(x.shape)))
-    a.y = _ptr(out)
-    with torch.cuda.device(dev):
-        _check(lib().gdp_group_norm_fwd(ctypes.byref(a), _stream(dev)))
+    dev = _need_cuda(x, weight, bias, gate, out)
+    a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps)
+    out = _output(out, "out", x.shape, x.dtype, dev)
+    a.y = out.data_ptr()
+    _call(dev, lib().gdp_group_norm_fwd, ctypes.byref(a))
     return out
 
 
@@ -829,17 +854,16 @@ def group_norm_bwd(dy, x, groups, weight=None, bias=None, gate=None, activation=
     """gdp_group_norm_bwd: the gradients of group_norm_fwd for that of y (dy, shaped as x).  Returns (dx, dz,
     dweight, dbias): dx and dz as x (dz None without a gate), dweight and dbias [C] float32 (None where there is
     none)."""
-    dev, a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps, (dy,))
-    _, _, dns, dts = _token_rows(dy, "dy", x)
+    dev = _need_cuda(x, weight, bias, gate, dy)
+    a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps)
+    ds = _like(dy, "dy", x)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dz = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
     dw = None if weight is None else torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
-    d = GroupNormGrads(dy=_ptr(dy), dy_n_stride=dns, dy_t_stride=dts, dx=_ptr(dx), dz=_ptr(dz), dw=_ptr(dw),
-                       db=_ptr(db))
-    with torch.cuda.device(dev):
-        need = lib().gdp_group_norm_workspace_bytes(ctypes.byref(a)) if dw is not None or db is not None else 0
-        ws = _workspace(need, dev)
-        _check(lib().gdp_group_norm_bwd(ctypes.byref(a), ctypes.byref(d), _ptr(ws), 0 if ws is None else ws.numel(),
-                                        _stream(dev)))
+    d = GroupNormGrads(dy.data_ptr(), ds[0], ds[1], dx.data_ptr(), _at(dz), _at(dw), _at(db))
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_group_norm_workspace_bytes(pa) if dw is not None or db is not None else 0
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_group_norm_bwd, pa, ctypes.byref(d), _at(ws), need)
     return dx, dz, dw, db

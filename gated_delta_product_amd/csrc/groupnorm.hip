@@ -28,14 +28,29 @@ template <> struct Unit<float, 4> { typedef uint4 type; };
 template <> struct Unit<bf16, 1> { typedef bf16 type; };
 template <> struct Unit<float, 1> { typedef float type; };
 
-template <typename T, int E>
-__device__ __forceinline__ void get(const T *p, float *f) {
+// The units of a lane, as they lie in memory; lanes past the group hold zeros.
+template <typename T, int E, int LPG, int NU>
+struct Raw {
     typedef typename Unit<T, E>::type U;
-    const U u = *(const U *)p;
-    const T *e = (const T *)&u;
+    U u[NU];
+    __device__ __forceinline__ void load(const T *p, int l, int D) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = to_f32(e[i]);
-}
+        for (int k = 0; k < NU; ++k) {
+            const int d = (l + k * LPG) * E;
+            u[k] = U{};
+            if (d < D) u[k] = *(const U *)(p + d);
+        }
+    }
+    __device__ __forceinline__ void floats(float *f) const {
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const U v = u[k];
+            const T *e = (const T *)&v;
+#pragma unroll
+            for (int i = 0; i < E; ++i) f[k * E + i] = to_f32(e[i]);
+        }
+    }
+};
 template <typename T, int E>
 __device__ __forceinline__ void put(T *p, const float *f) {
     typedef typename Unit<T, E>::type U;
@@ -107,20 +122,21 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_k(GroupNorm p) {
             b[k * E + i] = p.b && d < p.D ? p.b[col + d + i] : 0.f;
         }
     }
+    // the next row's loads are in flight while a row is worked on (wide groups
+    // have no registers for it)
+    constexpr bool AHEAD = N <= 16;
+    Raw<T, E, LPG, NU> rx, rz;
+    auto load = [&](int64_t row) {
+        rx.load((const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col, l, p.D);
+        if constexpr (GATE) rz.load((const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col, l, p.D);
+    };
+    if constexpr (AHEAD) load(r0);
     for (int64_t row = r0; row < p.rows; row += p.split) {
-        const T *x = (const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col;
-        const T *z = GATE ? (const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col : nullptr;
+        if constexpr (!AHEAD) load(row);
         float v[N], zv[GATE ? N : 1];
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int d = (l + k * LPG) * E;
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[k * E + i] = 0.f;
-            if (d < p.D) {
-                get<T, E>(x + d, v + k * E);
-                if constexpr (GATE) get<T, E>(z + d, zv + k * E);
-            }
-        }
+        rx.floats(v);
+        if constexpr (GATE) rz.floats(zv);
+        if (AHEAD && row + p.split < p.rows) load(row + p.split);
         normalise<N, LPG>(v, in, p.D, p.eps, p.centered);
         T *y = (T *)p.y + row * ((int64_t)p.groups * p.D) + col;
 #pragma unroll
@@ -162,25 +178,21 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
             dw[k * E + i] = db[k * E + i] = 0.f;
         }
     }
+    constexpr bool AHEAD = N <= 16;
+    Raw<T, E, LPG, NU> rx, rz, ry;
+    auto load = [&](int64_t row) {
+        rx.load((const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col, l, p.D);
+        ry.load((const T *)p.dy + row_at((uint32_t)row, p.T, p.dy_ns, p.dy_ts) + col, l, p.D);
+        if constexpr (GATE) rz.load((const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col, l, p.D);
+    };
+    if constexpr (AHEAD) load(r0);
     for (int64_t row = r0; row < p.rows; row += p.split) {
-        const T *x = (const T *)p.x + row_at((uint32_t)row, p.T, p.x_ns, p.x_ts) + col;
-        const T *dy = (const T *)p.dy + row_at((uint32_t)row, p.T, p.dy_ns, p.dy_ts) + col;
-        const T *z = GATE ? (const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col : nullptr;
+        if constexpr (!AHEAD) load(row);
         float v[N], dv[N], zv[GATE ? N : 1];
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int d = (l + k * LPG) * E;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                v[k * E + i] = dv[k * E + i] = 0.f;
-                if constexpr (GATE) zv[k * E + i] = 0.f;
-            }
-            if (d < p.D) {
-                get<T, E>(x + d, v + k * E);
-                get<T, E>(dy + d, dv + k * E);
-                if constexpr (GATE) get<T, E>(z + d, zv + k * E);
-            }
-        }
+        rx.floats(v);
+        ry.floats(dv);
+        if constexpr (GATE) rz.floats(zv);
+        if (AHEAD && row + p.split < p.rows) load(row + p.split);
         const float rstd = normalise<N, LPG>(v, in, p.D, p.eps, p.centered);
         const int64_t at = row * C + col;
         float s1 = 0.f, s2 = 0.f;
@@ -235,22 +247,31 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
 }
 
 // dw and db: the partial sums of every split, in a fixed order.  64 channels
-// a block, its four waves a quarter of the splits each.
-__global__ void __launch_bounds__(GNT) gdp_group_norm_sum_k(const float *part, int64_t split, int64_t C, float *dw,
-                                                            float *db) {
-    __shared__ double s[4][64];
+// a block, its 16 waves every 16th split each, 8 of them in flight.
+constexpr int GSW = 16;
+__global__ void __launch_bounds__(64 * GSW) gdp_group_norm_sum_k(const float *part, int64_t split, int64_t C, float *dw,
+                                                                 float *db) {
+    __shared__ double s[GSW][64];
     const int64_t c = (int64_t)blockIdx.x * 64 + lane_id();
     const int which = blockIdx.y;
     float *out = which ? db : dw;
     if (!out) return;
+    const float *q = part + which * C + c;
     double x = 0.0;
     if (c < C)
-        for (int64_t i = wave_id(); i < split; i += 4) x += part[(i * 2 + which) * C + c];
+        for (int64_t i = wave_id(); i < split; i += 8 * GSW) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = i + j * GSW < split ? q[(i + j * GSW) * 2 * C] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x += f[j];
+        }
     s[wave_id()][lane_id()] = x;
     __syncthreads();
     if (wave_id() == 0 && c < C) {
-        const int l = lane_id();
-        out[c] = (float)((s[0][l] + s[1][l]) + (s[2][l] + s[3][l]));
+        double t = 0.0;
+        for (int w = 0; w < GSW; ++w) t += s[w][lane_id()];
+        out[c] = (float)t;
     }
 }
 
@@ -317,12 +338,12 @@ hipError_t launch_shape(const GroupNorm &p, const Shape &s, hipStream_t stream) 
 // Row sets that run side by side: threads of one set walk rows r0, r0 + split, ...
 int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
     // forward: about 4 rows a thread once the card is full (2048 threads a CU);
-    // backward: as many threads as the card holds and no more, each split
-    // costing 8 bytes a channel of partial sums
+    // backward: at least 4 rows a thread and no more threads than the card
+    // holds, each split costing 8 bytes a channel of partial sums
     const int64_t per_row = (int64_t)groups * D / 8 > 0 ? (int64_t)groups * D / 8 : 1;
-    const int64_t fill = (bwd ? 131072 : 524288) / per_row + 1;
+    const int64_t fill = (bwd ? 262144 : 524288) / per_row + 1;
     const int64_t quarter = (rows + 3) / 4;
-    int64_t s = bwd ? fill : (quarter > fill ? quarter : fill);
+    const int64_t s = bwd ? (quarter < fill ? quarter : fill) : (quarter > fill ? quarter : fill);
     return s < rows ? s : rows;
 }
 
@@ -333,7 +354,7 @@ hipError_t launch_group_norm(const GroupNorm &p, gdp_dtype dtype, hipStream_t st
     else e = s.vec ? launch_shape<float, 4>(p, s, stream) : launch_shape<float, 1>(p, s, stream);
     if (e != hipSuccess || !(p.dw || p.db)) return e;
     const int64_t C = (int64_t)p.groups * p.D;
-    hipLaunchKernelGGL(gdp_group_norm_sum_k, dim3((unsigned)((C + 63) / 64), 2), dim3(GNT), 0, stream, p.part, p.split,
+    hipLaunchKernelGGL(gdp_group_norm_sum_k, dim3((unsigned)((C + 63) / 64), 2), dim3(64 * GSW), 0, stream, p.part, p.split,
                        C, p.dw, p.db);
     return hipGetLastError();
 }
