@@ -46,7 +46,8 @@ Plan plan_of(const gdp_linattn_args &a, bool backward) {
     p.items = p.nseq;
     // segments there may be, and sequences' (on average half full) last ones among them
     const int64_t fill = (backward ? kFill / 3 : kFill) / a.HV;
-    if (p.nseq == 0 || a.T <= 64) return p;
+    // eight chunks one after the other take as long as the two launches more
+    if (p.nseq == 0 || a.T <= 512) return p;
     int64_t seg = a.T;
     if (a.cu_seqlens) {
         const int64_t n = fill - p.nseq / 2;

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
 }
 
 // dw and db: the partial sums of every split, in a fixed order.  64 channels
-// a block, its 16 waves every 16th split each, 8 of them in flight.
+// a block, its 16 waves every 16th split each, 16 of them in flight.
 constexpr int GSW = 16;
 __global__ void __launch_bounds__(64 * GSW) gdp_group_norm_sum_k(const float *part, int64_t split, int64_t C, float *dw,
                                                                  float *db) {
@@ -259,12 +259,12 @@ __global__ void __launch_bounds__(64 * GSW) gdp_group_norm_sum_k(const float *pa
     const float *q = part + which * C + c;
     double x = 0.0;
     if (c < C)
-        for (int64_t i = wave_id(); i < split; i += 8 * GSW) {
-            float f[8];
+        for (int64_t i = wave_id(); i < split; i += 16 * GSW) {
+            float f[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = i + j * GSW < split ? q[(i + j * GSW) * 2 * C] : 0.f;
+            for (int j = 0; j < 16; ++j) f[j] = i + j * GSW < split ? q[(i + j * GSW) * 2 * C] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x += f[j];
+            for (int j = 0; j < 16; ++j) x += f[j];
         }
     s[wave_id()][lane_id()] = x;
     __syncthreads();
@@ -337,13 +337,13 @@ hipError_t launch_shape(const GroupNorm &p, const Shape &s, hipStream_t stream) 
 
 // Row sets that run side by side: threads of one set walk rows r0, r0 + split, ...
 int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
-    // forward: about 4 rows a thread once the card is full (2048 threads a CU);
-    // backward: at least 4 rows a thread and no more threads than the card
-    // holds, each split costing 8 bytes a channel of partial sums
+    // about 16 rows a thread forwards and 8 backwards once the card is full
+    // (32768 x 2048: 4 / 8 / 16 / 32 rows forwards 107 / 95 / 90 / 91 us);
+    // backwards at least 4, and each split costs 8 bytes a channel of partial sums
     const int64_t per_row = (int64_t)groups * D / 8 > 0 ? (int64_t)groups * D / 8 : 1;
-    const int64_t fill = (bwd ? 262144 : 524288) / per_row + 1;
-    const int64_t quarter = (rows + 3) / 4;
-    const int64_t s = bwd ? (quarter < fill ? quarter : fill) : (quarter > fill ? quarter : fill);
+    const int64_t fill = (bwd ? 131072 : 262144) / per_row + 1;
+    const int64_t few = (rows + (bwd ? 3 : 15)) / (bwd ? 4 : 16);
+    const int64_t s = bwd ? (few < fill ? few : fill) : (few > fill ? few : fill);
     return s < rows ? s : rows;
 }
 

@@ -106,7 +106,7 @@ struct Tile {
     }
 };
 
-// N values x[0..7] as NS parts of the storage type whose sum carries 8 NS
+// Values x[0..7] as NS parts of the storage type whose sum carries 8 NS
 // bits (bf16); for float storage one part is the value.
 template <typename T, int NS>
 __device__ __forceinline__ void split8(const float *x, typename Frag<T>::type *part) {
@@ -226,7 +226,7 @@ struct Walk {
     static constexpr int OCC = DA == 256 ? (WV == 8 ? 2 : 1) : WV / 2;
     // tiles whose operands are loaded together: fewer where registers are
     // short (a spill's reload would wait for every row in flight)
-    static constexpr int KG = OUT && OCC >= 4 ? 2 : 4, IG = OCC >= 4 ? 2 : NB;
+    static constexpr int KG = DOT && OCC >= 4 ? 2 : 4, IG = DOT && OCC >= 4 ? 2 : NB;
     static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
@@ -241,7 +241,8 @@ struct Walk {
         T p[OUT ? CT * CT : 8];
         float gh[2][CT], gl[2][CT];  // G as two floats
         float eg[2][CT], wg[2][CT];  // 2^G_i and sb 2^(G_end - G_i)
-        float rho[DOT ? WV * CT : 4];
+        float rho[DOT ? WV * CT : 4];  // rows' shares: of the columns of a wave,
+        float rho_p[DOT ? 16 * NP : 4];  // and of a score tile
     };
 };
 
@@ -261,6 +262,19 @@ struct Rows {
         const uint32_t step = rev ? 0u - STEP * ts : STEP * ts;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) r[i] = buf_load16(rs, off + i * step);
+    }
+    // The same rows straight into a tile (no registers): lane 16-byte slots of
+    // LDS lie in a row, so each lane asks for the unit that belongs in its slot.
+    static __device__ __forceinline__ void dma(T *t, const T *base, int64_t ts_elems, int n, bool rev, int wave, int lane) {
+        const uint32_t ts = (uint32_t)ts_elems * sizeof(T);
+        const rsrc_t rs = make_rsrc(base, (uint32_t)(n - 1) * ts + D * sizeof(T));
+        const uint32_t lds = lds_addr(t) + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i) {
+            const int slot = NT * i + wave * 64 + lane, row = slot / UPR;
+            const uint32_t unit = (uint32_t)(slot % UPR) ^ swz<UPR>(row);
+            dma16(rs, (uint32_t)(rev ? n - 1 - row : row) * ts + unit * 16, lds + NT * 16 * i);
+        }
     }
     __device__ __forceinline__ void stage(T *t, int tid) const {
         if constexpr (STEP % 16 == 0) {  // whole periods of the swizzle
@@ -303,8 +317,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     const T *px = DOT ? (const T *)w.x.p + bi * w.x.bs + (int64_t)(hv / w.x.div) * w.dc + slice * DC : nullptr;
     const float *pg = w.g ? w.g + bi * w.g_bs + hv : nullptr;
 
-    Rows<T, DA, NT, W::UA> ra, rb;
-    Rows<T, DC, NT, W::UC> rc, rx;
+    typedef Rows<T, DA, NT, W::UA> RA;
+    typedef Rows<T, DC, NT, W::UC> RC;
+    RA rb;
+    RC rc;
     const bool decayer = wave == W::WV - 1;  // the wave that forms the decays (it has fewer score tiles)
     float rg = 0.f;
     // rows [c0, c0 + n) of the walk into registers (g: one row a lane, asked for
@@ -318,10 +334,15 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
             if (lane < n && t < eos_in) rg = pg[t * w.g_ts];
         }
-        if constexpr (OUT) ra.fetch(pa + first * w.a.ts, w.a.ts, n, w.rev, tid);
         rb.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
         rc.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
-        if constexpr (DOT) rx.fetch(px + first * w.x.ts, w.x.ts, n, w.rev, tid);
+    };
+    // a and x are done with halfway through a chunk: the next rows then go into
+    // their tiles directly (b and c, needed to its end, wait in registers)
+    auto fetch_ax = [&](int64_t c0, int n) {
+        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
+        RA::dma(sm.a, pa + first * w.a.ts, w.a.ts, n, w.rev, wave, lane);
+        if constexpr (DOT) RC::dma(sm.x, px + first * w.x.ts, w.x.ts, n, w.rev, wave, lane);
     };
     float tot = 0.f;  // log2 decay of the whole walk (in the decayer), for the segment pass
     auto decays = [&](int n, int buf) {
@@ -338,7 +359,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         }
     };
     const int64_t nch = ceil_div64(len, CT);
-    if (nch > 0) fetch(0, len < CT ? (int)len : CT);
+    if (nch > 0) {
+        fetch(0, len < CT ? (int)len : CT);
+        if constexpr (OUT) fetch_ax(0, len < CT ? (int)len : CT);
+    }
 
     // entering state: S^T tiles [kt], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c
     f32x4 s[W::KT];
@@ -380,10 +404,9 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         // not fit the registers
         asm volatile("" : "+v"(lane));
         const int m = lane & 15, g4 = lane >> 4, tid = wave * 64 + lane;
-        if constexpr (OUT) ra.stage(sm.a, tid);
         rb.stage(sm.b, tid);
         rc.stage(sm.c, tid);
-        if constexpr (DOT) rx.stage(sm.x, tid);
+        if constexpr (OUT) wait_vmcnt<0>();  // a and x
         lds_barrier();
         if (ch + 1 < nch) fetch(c0 + CT, n1);
         const int arow = TA::row_base(lane);
@@ -391,37 +414,37 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         f32x4 y[W::NB];
         if constexpr (OUT) {
             // score tiles at and below the diagonal: P^T (rows j, columns i)
-            float rho_p[DOT ? (W::NP + W::WV - 1) / W::WV : 1];
 #pragma unroll
             for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
                 const int t = W::WV * k + wave;
                 if (t >= W::NP) break;
                 const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
-                f32x4 acc = zero4();
+                f32x4 acc[2] = {zero4(), zero4()}, e = zero4();
 #pragma unroll
                 for (int kb = 0; kb < DA / 32; ++kb)
-                    acc = mma(TA::row8(sm.b, arow, jb, kb), TA::row8(sm.a, arow, ib, kb), acc);
+                    acc[kb & 1] = mma(TA::row8(sm.b, arow, jb, kb), TA::row8(sm.a, arow, ib, kb), acc[kb & 1]);
+                if constexpr (DOT) {
+                    const int crow = TC::row_base(lane);
+#pragma unroll
+                    for (int kb = 0; kb < DC / 32; ++kb)
+                        e = mma(TC::row8(sm.c, crow, jb, kb), TC::row8(sm.x, crow, ib, kb), e);
+                }
                 const int i = 16 * ib + m, j0 = 16 * jb + 4 * g4;
                 const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
                 const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
                 typename Frag<T>::half pv;
+                float q = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r]));
-                    acc[r] = j0 + r <= i ? acc[r] * (d * w.sb) : 0.f;
-                    pv[r] = from_f32<T>(acc[r]);
+                    const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r])) * w.sb;
+                    const float sc = j0 + r <= i ? (acc[0][r] + acc[1][r]) * d : 0.f;
+                    pv[r] = from_f32<T>(sc);
+                    if constexpr (DOT) q += j0 + r < i ? sc * e[r] : 0.f;
                 }
                 *(typename Frag<T>::half *)(sm.p + TP::at(i, j0)) = pv;
                 if constexpr (DOT) {
-                    const int crow = TC::row_base(lane);
-                    f32x4 e = zero4();
-#pragma unroll
-                    for (int kb = 0; kb < DC / 32; ++kb)
-                        e = mma(TC::row8(sm.c, crow, jb, kb), TC::row8(sm.x, crow, ib, kb), e);
-                    float q = 0.f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) q += j0 + r < i ? acc[r] * e[r] : 0.f;
-                    rho_p[k] = xor32_sum(xor16_sum(q));
+                    q = xor32_sum(xor16_sum(q));
+                    if (g4 == 0) sm.rho_p[16 * t + m] = q;
                 }
             }
             // S a: S^T tiles as the operand, rounded to NQ parts
@@ -429,10 +452,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             for (int ib = 0; ib < W::NB; ++ib) y[ib] = zero4();
 #pragma unroll
             for (int kb = 0; kb < DA / 32; ++kb) {
-                frag sp[NQ];
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = s[2 * kb + i / 4][i % 4];
+                frag sp[NQ];
                 split8<T, NQ>(v, sp);
 #pragma unroll
                 for (int i0 = 0; i0 < W::NB; i0 += W::IG) {
@@ -457,16 +480,8 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                     if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] = q;
                 }
             }
-            if constexpr (DOT) {
-#pragma unroll
-                for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
-                    const int t = W::WV * k + wave;
-                    if (t >= W::NP) break;
-                    const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
-                    if (g4 == 0) sm.rho[wave * CT + 16 * ib + m] += rho_p[k];
-                }
-            }
             lds_barrier();
+            if (ch + 1 < nch) fetch_ax(c0 + CT, n1);
         }
 
         // the rows c as operands, once for P c and (decayed) for the state
@@ -533,6 +548,8 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 float q = 0.f;
 #pragma unroll
                 for (int i = 0; i < W::WV; ++i) q += sm.rho[i * CT + lane];
+                const int ib = lane / 16;
+                for (int jb = 0; jb <= ib; ++jb) q += sm.rho_p[16 * (ib * (ib + 1) / 2 + jb) + lane % 16];
                 const int64_t t = w.rev ? tb0 + len - 1 - c0 - lane : tb0 + c0 + lane;
                 w.rho[((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + t] = q * w.sy;
             }
