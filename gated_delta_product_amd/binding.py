@@ -751,14 +751,11 @@ def linattn_bwd(do, q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=
     nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state)
     ds = _rows(do, "do", v.shape, q.dtype)
     _state(dht, "dht", (nseq, a.HV, a.V, a.K))
-    new = torch.empty if cu_seqlens is None else torch.zeros
-    dq = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
-    dk = new((a.B, a.T, a.H, a.K), dtype=q.dtype, device=dev)
-    dv = new((a.B, a.T, a.HV, a.V), dtype=q.dtype, device=dev)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dk = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
     per_head = g is not None and g.dim() == 1
-    dg = None
-    if g is not None:
-        dg = (torch.empty if per_head else new)(g.shape, dtype=torch.float32, device=dev)
+    dg = None if g is None else torch.empty(g.shape, dtype=torch.float32, device=dev)
     dh0 = None if initial_state is None else torch.empty_like(initial_state)
     d = LinattnGrads(do.data_ptr(), ds[0], ds[1], _at(dht), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                      None if per_head else _at(dg), _at(dg) if per_head else None, _at(dh0))

@@ -34,9 +34,15 @@ struct Plan {
     bool segments;
 };
 
-// Walks a launch should have: two to each of 256 compute units, all resident
-// at once.  A launch of the gradients has three walks to an item.
-constexpr int64_t kFill = 512;
+// Segments of all sequences together that fill the card: as many walks as its
+// 256 compute units hold at once (by registers and LDS two blocks of eight
+// waves or three of four to a unit; one where a walk keeps 256 rows of S^T).
+int64_t segments_to_fill(const gdp_linattn_args &a, bool backward) {
+    const int sl = backward ? gdp::lin_grads_slice(a.K, a.V) : (a.V < 128 ? a.V : 128);
+    const int da = backward ? a.V : a.K;
+    const int64_t walks = da == 256 ? 256 : sl == 64 ? 768 : 512;
+    return walks / ((int64_t)a.HV * (backward ? 2 * a.K / sl : a.V / sl));  // backward: dq and dk first
+}
 
 Plan plan_of(const gdp_linattn_args &a, bool backward) {
     Plan p;
@@ -44,13 +50,16 @@ Plan plan_of(const gdp_linattn_args &a, bool backward) {
     p.seg_tok = a.T > 0 ? a.T : 1;
     p.segments = false;
     p.items = p.nseq;
-    // segments there may be, and sequences' (on average half full) last ones among them
-    const int64_t fill = (backward ? kFill / 3 : kFill) / a.HV;
     // eight chunks one after the other take as long as the two launches more
     if (p.nseq == 0 || a.T <= 512) return p;
+    const int64_t fill = segments_to_fill(a, backward);
     int64_t seg = a.T;
     if (a.cu_seqlens) {
-        const int64_t n = fill - p.nseq / 2;
+        // ragged requests: last segments are half full on average, and the long
+        // walks of the gradients are cut finer, so that none ends alone (8
+        // requests of 821 to 3562 tokens, 16 heads: once / twice / three / four
+        // times the card 451 / 441 / 466 / 493 us)
+        const int64_t n = (backward ? 2 : 1) * fill - p.nseq / 2;
         if (p.nseq < fill) seg = cdiv(a.T, n > 1 ? n : 1);
     } else if (fill >= 2 * a.B) {
         seg = cdiv(a.T, fill / a.B);
@@ -58,6 +67,7 @@ Plan plan_of(const gdp_linattn_args &a, bool backward) {
     // backward: the running sums of dg are as long as a segment
     if (backward && seg > 2048) seg = 2048;
     seg = (seg + 63) / 64 * 64;
+    if (seg < 128) seg = 128;  // a state costs as much traffic as 128 rows
     if (seg >= a.T) return p;
     p.segments = true;
     p.seg_tok = seg;
@@ -151,7 +161,7 @@ gdp_status check_linattn(const char *name, const gdp_linattn_args *a, bool forwa
     if (((uintptr_t)a->g | (uintptr_t)a->g_head | (uintptr_t)a->cu_seqlens) & 3)
         return fail(GDP_ERR_INVALID, "%s: g, g_head or cu_seqlens is not 4-byte aligned", name);
     if (!aligned16(a->h0) || !aligned16(a->ht)) return fail(GDP_ERR_INVALID, "%s: h0 or ht is not 16-byte aligned", name);
-    if (nseq == 0 || a->T == 0) return ok();
+    if (a->T == 0 || (forward ? nseq : a->B) == 0) return ok();
     if ((st = check_rows(name, "q", a->q, a->q_b_stride, a->q_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
     if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
     if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->T, (int64_t)a->HV * a->V, a->dtype)) != GDP_OK) return st;
@@ -237,7 +247,7 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
         gdp::LinWalks e{{w, {}, {}}, 1};
         e.w[0].seg_out = ws.seg;
         e.w[0].seg_tot = ws.tot;
-        if ((st = hip_status(gdp::launch_lin_walks(e, a.dtype, false, s), name)) != GDP_OK) return st;
+        if ((st = hip_status(gdp::launch_lin_walks(e, a.dtype, false, a.ht != nullptr, s), name)) != GDP_OK) return st;
         gdp::LinScan c = scan_base(a, p);
         c.n = 1;
         c.s[0] = {false, a.h0, ws.seg, ws.tot};
@@ -247,7 +257,7 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
     w.sy = a.scale;
     w.y = a.o;
     w.s_out = a.ht;
-    return hip_status(gdp::launch_lin_walks({{w, {}, {}}, 1}, a.dtype, true, s), name);
+    return hip_status(gdp::launch_lin_walks({{w, {}, {}}, 1}, a.dtype, true, a.ht != nullptr, s), name);
 }
 
 gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads *d, void *workspace,
@@ -268,7 +278,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
         return fail(GDP_ERR_INVALID, "%s: dh0 may not be dht or h0", name);
     if (!(a.scale > 0.f)) a.scale = 1.0f / std::sqrt((float)a.K);
     const Plan p = plan_of(a, true);
-    if (p.nseq > 0 && a.T > 0) {
+    if (a.B > 0 && a.T > 0) {
         if ((st = check_rows(name, "dout", d->dout, d->do_b_stride, d->do_t_stride, a.T, (int64_t)a.HV * a.V,
                              a.dtype)) != GDP_OK) return st;
         if (!d->dq || !d->dk || !d->dv || !aligned16(d->dq) || !aligned16(d->dk) || !aligned16(d->dv))
@@ -287,10 +297,10 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     g.elems = (int64_t)a.K * a.V;
     g.items = p.items;  // 0 without sequences: dg_head is zero then
     g.HV = a.HV;
-    if (p.nseq == 0) return hip_status(gdp::launch_lin_dg(g, d->dg_head, s), name);
 
     const int r = a.HV / a.H;
     const int64_t wk = (int64_t)a.H * a.K, wv = (int64_t)a.HV * a.V;
+    if (p.nseq == 0 && a.T == 0) return hip_status(gdp::launch_lin_dg(g, d->dg_head, s), name);
     const gdp::LinRows q = rows_of(a.q, a.q_b_stride, a.q_t_stride, a.T, wk, r),
                        k = rows_of(a.k, a.k_b_stride, a.k_t_stride, a.T, wk, r),
                        v = rows_of(a.v, a.v_b_stride, a.v_t_stride, a.T, wv, 1),
@@ -313,7 +323,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
         b.rev = true;
         b.seg_out = ws.r;
         b.seg_tot = ws.r_tot;
-        if ((st = hip_status(gdp::launch_lin_walks({{f, b, {}}, 2}, a.dtype, false, s), name)) != GDP_OK)
+        if ((st = hip_status(gdp::launch_lin_walks({{f, b, {}}, 2}, a.dtype, false, want_g || d->dh0, s), name)) != GDP_OK)
             return st;
         gdp::LinScan c = scan_base(a, p);
         c.n = 2;
@@ -363,6 +373,12 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     // <h0, dh0> anchors dg where one segment has a state before it and a gradient behind it
     x.s_out = d->dh0 ? d->dh0 : want_g && d->dht && a.h0 ? ws.dh0 : nullptr;
     if ((st = hip_status(gdp::launch_lin_grads({{f, w, x}, 3}, a.dtype, want_g, s), name)) != GDP_OK) return st;
+    if (a.cu_seqlens && a.T > 0) {
+        const int64_t es = (int64_t)dsize(a.dtype);
+        const gdp::LinOutside c{{d->dq, d->dk, d->dv, d->dg}, {wk * es / 4, wk * es / 4, wv * es / 4, a.HV}, a.T, p.nseq,
+                                a.cu_seqlens};
+        if ((st = hip_status(gdp::launch_lin_outside(c, s), name)) != GDP_OK) return st;
+    }
     if (shared) {
         const gdp::LinGroup c{{ws.dq, ws.dk}, {d->dq, d->dk}, a.B * a.T * a.H * (a.K / 4), p.nseq, a.H, r, a.K / 4,
                               a.cu_seqlens};

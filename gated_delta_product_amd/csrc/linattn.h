@@ -80,8 +80,17 @@ struct LinGroup {
     const int32_t *cu;
 };
 
-// out: the rows y (else each segment's state only)
-hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, hipStream_t stream);
+// Zeros in the rows outside every request: y[i] [T, words[i]] of 4 bytes (or NULL).
+struct LinOutside {
+    void *y[4];
+    int64_t words[4];
+    int64_t T, nseq;
+    const int32_t *cu;
+};
+hipError_t launch_lin_outside(const LinOutside &p, hipStream_t stream);
+
+// out: the rows y (else each segment's state only); exact: states to 24 bits
+hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, bool exact, hipStream_t stream);
 // w[0] dq, w[1] dk, w[2] dv; dot: rho of dq and dk too
 int lin_grads_slice(int K, int V);
 hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream);

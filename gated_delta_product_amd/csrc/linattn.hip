@@ -344,24 +344,32 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         RA::dma(sm.a, pa + first * w.a.ts, w.a.ts, n, w.rev, wave, lane);
         if constexpr (DOT) RC::dma(sm.x, px + first * w.x.ts, w.x.ts, n, w.rev, wave, lane);
     };
-    float tot = 0.f;  // log2 decay of the whole walk (in the decayer), for the segment pass
+    // The segment pass takes its chunks from the last to the first (each row's
+    // weight then reaches to the segment's end and the sum is never scaled):
+    // the rows walk that follows starts on the rows that were read last, which
+    // the last level of cache still holds.
+    double tot = 0.0;  // log2 decay of the chunks taken (in the decayer)
     auto decays = [&](int n, int buf) {
         if (!decayer) return;
         const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(rg) : 0.0);
         const double Gend = __shfl(G, 63, 64);
-        tot += (float)Gend;
         if (lane < CT) {
-            const float hi = (float)G;
-            sm.gh[buf][lane] = hi;
-            sm.gl[buf][lane] = (float)(G - (double)hi);
-            sm.eg[buf][lane] = __builtin_amdgcn_exp2f((float)G);
-            sm.wg[buf][lane] = w.sb * __builtin_amdgcn_exp2f((float)(Gend - G));
+            if constexpr (OUT) {
+                const float hi = (float)G;
+                sm.gh[buf][lane] = hi;
+                sm.gl[buf][lane] = (float)(G - (double)hi);
+                sm.eg[buf][lane] = __builtin_amdgcn_exp2f((float)G);
+            }
+            sm.wg[buf][lane] = w.sb * __builtin_amdgcn_exp2f((float)(OUT ? Gend - G : Gend - G + tot));
         }
+        tot += Gend;
     };
     const int64_t nch = ceil_div64(len, CT);
+    const int64_t cfirst = OUT || nch == 0 ? 0 : (nch - 1) * CT, cstep = OUT ? CT : -CT;
+    const int nfirst = len - cfirst < CT ? (int)(len - cfirst) : CT;
     if (nch > 0) {
-        fetch(0, len < CT ? (int)len : CT);
-        if constexpr (OUT) fetch_ax(0, len < CT ? (int)len : CT);
+        fetch(cfirst, nfirst);
+        if constexpr (OUT) fetch_ax(0, nfirst);
     }
 
     // entering state: S^T tiles [kt], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c
@@ -391,14 +399,14 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     if constexpr (OUT) {
         for (int i = threadIdx.x; i < CT * CT; i += NT) sm.p[i] = from_f32<T>(0.f);
     }
-    if (nch > 0) decays(len < CT ? (int)len : CT, 0);
+    if (nch > 0) decays(nfirst, 0);
 
     // The barriers order LDS only: the next chunk's rows stay in flight over
     // them, and so do the stores of y.
     for (int64_t ch = 0; ch < nch; ++ch) {
-        const int64_t c0 = ch * CT;
+        const int64_t c0 = cfirst + ch * cstep, c1 = c0 + cstep;  // this chunk's first row and the next one's
         const int n = len - c0 < CT ? (int)(len - c0) : CT;
-        const int n1 = len - c0 - CT < CT ? (int)(len - c0 - CT) : CT;  // rows of the next chunk
+        const int n1 = len - c1 < CT ? (int)(len - c1) : CT;
         const int buf = (int)(ch & 1);
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
@@ -408,7 +416,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         rc.stage(sm.c, tid);
         if constexpr (OUT) wait_vmcnt<0>();  // a and x
         lds_barrier();
-        if (ch + 1 < nch) fetch(c0 + CT, n1);
+        if (ch + 1 < nch) fetch(c1, n1);
         const int arow = TA::row_base(lane);
 
         f32x4 y[W::NB];
@@ -481,16 +489,18 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 }
             }
             lds_barrier();
-            if (ch + 1 < nch) fetch_ax(c0 + CT, n1);
+            if (ch + 1 < nch) fetch_ax(c1, n1);
         }
 
         // the rows c as operands, once for P c and (decayed) for the state
-        const float dec = sm.eg[buf][CT - 1];
         const auto ccol = TC::template cols<4>(lane, cw);
         const auto bcol = TA::template cols<8>(lane, 0);
         const int prow = TP::row_base(lane);
+        if constexpr (OUT) {
+            const float dec = sm.eg[buf][CT - 1];
 #pragma unroll
-        for (int kt = 0; kt < W::KT; ++kt) s[kt] *= dec;
+            for (int kt = 0; kt < W::KT; ++kt) s[kt] *= dec;
+        }
 #pragma unroll
         for (int tb = 0; tb < W::TB; ++tb) {
             const frag fc = TC::template col8<4>(sm.c, ccol, lane, tb, 0, 0);
@@ -561,7 +571,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     float f = 1.f;
     if constexpr (!OUT) {
         so = w.seg_out + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
-        if (decayer && lane == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = tot;
+        if (decayer && lane == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = (float)tot;
     } else if (at_end && w.s_out) {
         so = w.s_out + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
         if (w.rev && pg && it.eos > it.bos)  // through the first row's decay too
@@ -594,19 +604,20 @@ gdp_lin_walk_k(LinWalks p) {
 
 // The three walks of the gradients in one launch: dq and dk (DA = V, slices of
 // K columns) and dv (DA = K, slices of V columns), all in slices of SL.
-template <typename T, int K, int V, int SL, int NS, int NQ, bool DOT>
+// ND: parts of dv's state, which also leaves as dh0.
+template <typename T, int K, int V, int SL, int NS, int NQ, int ND, bool DOT>
 struct Grads {
     typedef Walk<T, V, SL, NS, NQ, true, DOT> QK;
-    typedef Walk<T, K, SL, NS, 1, true, false> D;
+    typedef Walk<T, K, SL, ND, 1, true, false> D;
     static constexpr int OCC = QK::OCC < D::OCC ? QK::OCC : D::OCC;
     static constexpr int BYTES = sizeof(typename QK::Lds) > sizeof(typename D::Lds) ? sizeof(typename QK::Lds)
                                                                                    : sizeof(typename D::Lds);
 };
-template <typename T, int K, int V, int SL, int NS, int NQ, bool DOT>
-__global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, DOT>::OCC)) gdp_lin_grads_k(LinWalks p) {
-    __shared__ __align__(16) char lds[Grads<T, K, V, SL, NS, NQ, DOT>::BYTES];
+template <typename T, int K, int V, int SL, int NS, int NQ, int ND, bool DOT>
+__global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, ND, DOT>::OCC)) gdp_lin_grads_k(LinWalks p) {
+    __shared__ __align__(16) char lds[Grads<T, K, V, SL, NS, NQ, ND, DOT>::BYTES];
     if (blockIdx.y < 2) lin_block<T, V, SL, NS, NQ, true, DOT>(p.w[blockIdx.y], lds);
-    else lin_block<T, K, SL, NS, 1, true, false>(p.w[2], lds);
+    else lin_block<T, K, SL, ND, 1, true, false>(p.w[2], lds);
 }
 
 // ---------------------------------------------------------------- the scan over segments
@@ -676,11 +687,12 @@ __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
 // less what it gives to later ones.  Each segment is anchored at one border,
 // where the sum is the product of the state and the gradient that meet there,
 // so the running sums (64 bits) stay as short as a segment.
-__global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
+constexpr int DGT = 512;
+__global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
     const uint32_t b = blockIdx.x;
     const int64_t id = b / (uint32_t)p.HV;
     const int hv = (int)(b % (uint32_t)p.HV);
-    __shared__ double s_red[4];
+    __shared__ double s_red[DGT / 64];
     __shared__ double s_carry;
     const LinItem it = lin_item(p.cu, p.nseq, p.T, p.seg_tok, id);
     if (it.seq < 0) {
@@ -711,10 +723,22 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
     }
     double x = 0.0;
     if (S) {
+        // 4 elements a thread and step, four steps' loads in flight (elems: 4096 to 32768)
         float acc = 0.f;
-        for (int64_t i = threadIdx.x * 4; i < p.elems; i += 1024) {
-            const f32x4 u = *(const f32x4 *)(S + i), v = *(const f32x4 *)(R + i);
-            acc += (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]);
+        for (int64_t i0 = (int64_t)threadIdx.x * 4; i0 < p.elems; i0 += 16 * DGT) {
+            f32x4 u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i0 + k * 4 * DGT;
+                u[k] = v[k] = zero4();
+                if (i < p.elems) {
+                    u[k] = *(const f32x4 *)(S + i);
+                    v[k] = *(const f32x4 *)(R + i);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc += (u[k][0] * v[k][0] + u[k][1] * v[k][1]) + (u[k][2] * v[k][2] + u[k][3] * v[k][3]);
         }
         x = acc;
 #pragma unroll
@@ -723,15 +747,17 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
     if (lane_id() == 0) s_red[threadIdx.x >> 6] = x;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double c = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-        if (through >= 0 && p.g) c *= exp2(decay_log2(p.g[bi * p.g_bs + through * p.g_ts + hv]));
+        double c = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < DGT / 64; ++i) c += s_red[i];
+        if (through >= 0 && p.g) c *= (double)__builtin_amdgcn_exp2f((float)decay_log2(p.g[bi * p.g_bs + through * p.g_ts + hv]));
         s_carry = c;
     }
     __syncthreads();
-    // the rows from the anchored border, 256 at a time
+    // the rows from the anchored border, DGT at a time
     double sum = 0.0;
     const int64_t BT = p.B * p.T;
-    for (int64_t k0 = 0; k0 < tb1 - tb0; k0 += 256) {
+    for (int64_t k0 = 0; k0 < tb1 - tb0; k0 += DGT) {
         const int64_t k = k0 + threadIdx.x, t = fwd ? tb0 + k : tb1 - 1 - k;
         const bool in = k < tb1 - tb0;
         double d = 0.0;
@@ -746,6 +772,7 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
         if (lane_id() == 0) s_red[threadIdx.x >> 6] = tot;
         __syncthreads();
         double upto = s_carry + incl;
+#pragma unroll 1
         for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) upto += s_red[i];
         const double v = fwd ? upto - d : upto;
         if (in) {
@@ -753,7 +780,7 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
             sum += v;
         }
         __syncthreads();
-        if (threadIdx.x == 255) s_carry = upto;
+        if (threadIdx.x == DGT - 1) s_carry = upto;
         __syncthreads();
     }
     if (!p.part) return;
@@ -761,7 +788,11 @@ __global__ void __launch_bounds__(256) gdp_lin_dg_k(LinDg p) {
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
     if (lane_id() == 0) s_red[threadIdx.x >> 6] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) p.part[id * p.HV + hv] = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int i = 0; i < DGT / 64; ++i) t += s_red[i];
+        p.part[id * p.HV + hv] = t;
+    }
 }
 
 // dg of a decay per head: the sum over every segment, in a fixed order
@@ -799,6 +830,27 @@ __global__ void __launch_bounds__(256) gdp_lin_group_k(LinGroup p) {
     *(typename Frag<T>::half *)((T *)p.y[blockIdx.y] + u * 4) = o;
 }
 
+// Gradients of tokens outside every request: zero.  A block looks after 64
+// tokens and mostly finds them inside.
+__global__ void __launch_bounds__(256) gdp_lin_outside_k(LinOutside p) {
+    const int64_t t0 = (int64_t)blockIdx.x * 64, t1 = t0 + 64 < p.T ? t0 + 64 : p.T;
+    // requests follow each other from the first offset to the last
+    int64_t lo = 0, hi = 0;
+    if (p.nseq > 0) {
+        lo = p.cu[0] < 0 ? 0 : p.cu[0];
+        hi = p.cu[p.nseq];
+    }
+    if (t0 >= lo && t1 <= hi) return;
+    for (int64_t t = t0; t < t1; ++t) {
+        if (t >= lo && t < hi) continue;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t *y = (uint32_t *)p.y[i];
+            if (!y) continue;
+            for (int64_t w = threadIdx.x; w < p.words[i]; w += 256) y[t * p.words[i] + w] = 0;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- launches
 template <typename T, int DA, int DC, int NS, bool OUT>
 static hipError_t launch_walk_t(const LinWalks &w, hipStream_t stream) {
@@ -815,40 +867,49 @@ static hipError_t launch_walk_dims(const LinWalks &w, hipStream_t stream) {
     return dc == 64 ? launch_walk_t<T, 128, 64, NS, OUT>(w, stream) : launch_walk_t<T, 128, 128, NS, OUT>(w, stream);
 }
 
-hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, hipStream_t stream) {
+hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, bool exact, hipStream_t stream) {
     if (w.w[0].items == 0) return hipSuccess;
     if (dtype == GDP_F32) return out ? launch_walk_dims<float, 1, true>(w, stream) : launch_walk_dims<float, 1, false>(w, stream);
-    return out ? launch_walk_dims<bf16, 3, true>(w, stream) : launch_walk_dims<bf16, 3, false>(w, stream);
+    if (exact) return out ? launch_walk_dims<bf16, 3, true>(w, stream) : launch_walk_dims<bf16, 3, false>(w, stream);
+    return out ? launch_walk_dims<bf16, 2, true>(w, stream) : launch_walk_dims<bf16, 2, false>(w, stream);
 }
 
 // Columns of c that one walk of the gradients takes: as many waves in each of the three.
 int lin_grads_slice(int K, int V) { return K == 64 || V == 64 ? 64 : 128; }
 
-template <typename T, int K, int V, int NS, int NQ, bool DOT>
+template <typename T, int K, int V, int NS, int NQ, int ND, bool DOT>
 static hipError_t launch_grads_t(const LinWalks &w, hipStream_t stream) {
     constexpr int SL = K == 64 || V == 64 ? 64 : 128;
     const int64_t most = w.w[0].items * w.w[0].HV * ((K > V ? K : V) / SL);
     if (most > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gdp_lin_grads_k<T, K, V, SL, NS, NQ, DOT>), dim3((unsigned)most, 3), dim3(4 * SL), 0, stream, w);
+    hipLaunchKernelGGL((gdp_lin_grads_k<T, K, V, SL, NS, NQ, ND, DOT>), dim3((unsigned)most, 3), dim3(4 * SL), 0, stream, w);
     return hipGetLastError();
 }
-template <typename T, int NS, int NQ, bool DOT>
+template <typename T, int NS, int NQ, int ND, bool DOT>
 static hipError_t launch_grads_dims(const LinWalks &w, hipStream_t stream) {
     switch (w.w[2].da * 1000 + w.w[2].dc) {
-    case 64064: return launch_grads_t<T, 64, 64, NS, NQ, DOT>(w, stream);
-    case 64128: return launch_grads_t<T, 64, 128, NS, NQ, DOT>(w, stream);
-    case 64256: return launch_grads_t<T, 64, 256, NS, NQ, DOT>(w, stream);
-    case 128064: return launch_grads_t<T, 128, 64, NS, NQ, DOT>(w, stream);
-    case 128128: return launch_grads_t<T, 128, 128, NS, NQ, DOT>(w, stream);
-    case 128256: return launch_grads_t<T, 128, 256, NS, NQ, DOT>(w, stream);
+    case 64064: return launch_grads_t<T, 64, 64, NS, NQ, ND, DOT>(w, stream);
+    case 64128: return launch_grads_t<T, 64, 128, NS, NQ, ND, DOT>(w, stream);
+    case 64256: return launch_grads_t<T, 64, 256, NS, NQ, ND, DOT>(w, stream);
+    case 128064: return launch_grads_t<T, 128, 64, NS, NQ, ND, DOT>(w, stream);
+    case 128128: return launch_grads_t<T, 128, 128, NS, NQ, ND, DOT>(w, stream);
+    case 128256: return launch_grads_t<T, 128, 256, NS, NQ, ND, DOT>(w, stream);
     default: return hipErrorInvalidValue;
     }
 }
+// Parts of bf16 in the state's products.  What leaves in float32 (ht, dh0, and
+// dg through rho) takes three, 24 bits: with two, dg was 1e-5 off and ht 2e-6
+// (relative to 64 bits; with three 1e-6 and 2e-7, as float32 sums are).  States
+// that only reach bf16 rows take two, and one as the operand of S a: that
+// rounding, the scores' and the result's are of one size (2.3e-3 for 1.7e-3
+// of the result's alone).
 hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream) {
     if (w.w[0].items == 0) return hipSuccess;
     if (dtype == GDP_F32)
-        return dot ? launch_grads_dims<float, 1, 1, true>(w, stream) : launch_grads_dims<float, 1, 1, false>(w, stream);
-    return dot ? launch_grads_dims<bf16, 3, 3, true>(w, stream) : launch_grads_dims<bf16, 3, 1, false>(w, stream);
+        return dot ? launch_grads_dims<float, 1, 1, 1, true>(w, stream) : launch_grads_dims<float, 1, 1, 1, false>(w, stream);
+    if (w.w[2].s_out)
+        return dot ? launch_grads_dims<bf16, 3, 3, 3, true>(w, stream) : launch_grads_dims<bf16, 2, 1, 3, false>(w, stream);
+    return dot ? launch_grads_dims<bf16, 3, 3, 2, true>(w, stream) : launch_grads_dims<bf16, 2, 1, 2, false>(w, stream);
 }
 
 hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
@@ -860,12 +921,17 @@ hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
 
 hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream) {
     if (p.items > 0) {
-        hipLaunchKernelGGL(gdp_lin_dg_k, dim3((unsigned)(p.items * p.HV)), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL(gdp_lin_dg_k, dim3((unsigned)(p.items * p.HV)), dim3(DGT), 0, stream, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!dg_head) return hipSuccess;
     hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items, p.HV, dg_head);
+    return hipGetLastError();
+}
+
+hipError_t launch_lin_outside(const LinOutside &p, hipStream_t stream) {
+    hipLaunchKernelGGL(gdp_lin_outside_k, dim3((unsigned)((p.T + 63) / 64)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

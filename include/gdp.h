@@ -585,7 +585,7 @@ typedef struct gdp_linattn_args {
  *   dg       [B, T, HV] float32, the gradient of g, or NULL
  *   dg_head  [HV] float32, the gradient of g_head, or NULL
  *   dh0      [nseq, HV, V, K] float32, the gradient of h0, or NULL
- * Rows of tokens outside every request are left as they were. */
+ * The gradients of tokens outside every request are zero. */
 typedef struct gdp_linattn_grads {
     const void *dout;
     int64_t do_b_stride;
