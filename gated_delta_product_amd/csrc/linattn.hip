@@ -319,23 +319,29 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
     typedef Rows<T, DA, NT, W::UA> RA;
     typedef Rows<T, DC, NT, W::UC> RC;
-    RA rb;
-    RC rc;
+    // a chunk's rows of b and c and its log decays on their way; the segment
+    // pass, which has the registers, keeps two chunks' under way
+    struct Set {
+        RA b;
+        RC c;
+        float g;
+    };
+    constexpr int AHEAD = OUT ? 1 : 2;
+    Set set[AHEAD];
     const bool decayer = wave == W::WV - 1;  // the wave that forms the decays (it has fewer score tiles)
-    float rg = 0.f;
     // rows [c0, c0 + n) of the walk into registers (g: one row a lane, asked for
     // first, so that the wait for it leaves the rows in flight)
-    auto fetch = [&](int64_t c0, int n) {
+    auto fetch = [&](int64_t c0, int n, Set &r) {
         const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
         const int tid = wave * 64 + lane;
-        rg = 0.f;
+        r.g = 0.f;
         if (pg && decayer) {
             // backwards, a row is entered through the decay of the row after it
             const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
-            if (lane < n && t < eos_in) rg = pg[t * w.g_ts];
+            if (lane < n && t < eos_in) r.g = pg[t * w.g_ts];
         }
-        rb.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
-        rc.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
+        r.b.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
+        r.c.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
     };
     // a and x are done with halfway through a chunk: the next rows then go into
     // their tiles directly (b and c, needed to its end, wait in registers)
@@ -349,9 +355,9 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     // the rows walk that follows starts on the rows that were read last, which
     // the last level of cache still holds.
     double tot = 0.0;  // log2 decay of the chunks taken (in the decayer)
-    auto decays = [&](int n, int buf) {
+    auto decays = [&](int n, int buf, float g) {
         if (!decayer) return;
-        const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(rg) : 0.0);
+        const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(g) : 0.0);
         const double Gend = __shfl(G, 63, 64);
         if (lane < CT) {
             if constexpr (OUT) {
@@ -366,10 +372,11 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     };
     const int64_t nch = ceil_div64(len, CT);
     const int64_t cfirst = OUT || nch == 0 ? 0 : (nch - 1) * CT, cstep = OUT ? CT : -CT;
-    const int nfirst = len - cfirst < CT ? (int)(len - cfirst) : CT;
+    auto rows_of = [&](int64_t c0) { return len - c0 < CT ? (int)(len - c0) : CT; };
     if (nch > 0) {
-        fetch(cfirst, nfirst);
-        if constexpr (OUT) fetch_ax(0, nfirst);
+        fetch(cfirst, rows_of(cfirst), set[0]);
+        if (AHEAD == 2 && nch > 1) fetch(cfirst + cstep, rows_of(cfirst + cstep), set[AHEAD - 1]);
+        if constexpr (OUT) fetch_ax(0, rows_of(0));
     }
 
     // entering state: S^T tiles [kt], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c
@@ -399,24 +406,23 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     if constexpr (OUT) {
         for (int i = threadIdx.x; i < CT * CT; i += NT) sm.p[i] = from_f32<T>(0.f);
     }
-    if (nch > 0) decays(nfirst, 0);
+    if (nch > 0) decays(rows_of(cfirst), 0, set[0].g);
 
     // The barriers order LDS only: the next chunk's rows stay in flight over
     // them, and so do the stores of y.
-    for (int64_t ch = 0; ch < nch; ++ch) {
+    auto chunk = [&](int64_t ch, Set &cur, const Set &next) __attribute__((always_inline)) {
         const int64_t c0 = cfirst + ch * cstep, c1 = c0 + cstep;  // this chunk's first row and the next one's
-        const int n = len - c0 < CT ? (int)(len - c0) : CT;
-        const int n1 = len - c1 < CT ? (int)(len - c1) : CT;
+        const int n = rows_of(c0), n1 = rows_of(c1);
         const int buf = (int)(ch & 1);
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
         asm volatile("" : "+v"(lane));
         const int m = lane & 15, g4 = lane >> 4, tid = wave * 64 + lane;
-        rb.stage(sm.b, tid);
-        rc.stage(sm.c, tid);
+        cur.b.stage(sm.b, tid);
+        cur.c.stage(sm.c, tid);
         if constexpr (OUT) wait_vmcnt<0>();  // a and x
         lds_barrier();
-        if (ch + 1 < nch) fetch(c1, n1);
+        if (ch + AHEAD < nch) fetch(c0 + AHEAD * cstep, rows_of(c0 + AHEAD * cstep), cur);
         const int arow = TA::row_base(lane);
 
         f32x4 y[W::NB];
@@ -527,7 +533,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                     for (int k = 0; k < W::KG; ++k) s[k0 + k] = mma(fb[k], fw[p], s[k0 + k]);
             }
         }
-        if (ch + 1 < nch) decays(n1, buf ^ 1);
+        if (ch + 1 < nch) decays(n1, buf ^ 1, next.g);
         if constexpr (OUT) {
             // rows of y as a buffer that ends with the chunk, like the inputs' (stores past it are dropped)
             const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
@@ -564,6 +570,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 w.rho[((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + t] = q * w.sy;
             }
         }
+    };
+    for (int64_t ch = 0; ch < nch; ch += AHEAD) {
+        chunk(ch, set[0], set[AHEAD - 1]);
+        if (AHEAD == 2 && ch + 1 < nch) chunk(ch + 1, set[AHEAD - 1], set[0]);
     }
 
     // the state after the walk: the segment's own (segment pass), or the sequence's
