@@ -141,6 +141,13 @@ __device__ __forceinline__ double wave_inclusive_sum_f64(double x) {
     return x;
 }
 
+__device__ __forceinline__ double lane63_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // A log decay in log2 units.  Anything below -160 empties the state as far
 // as a float can tell (2^-160 is zero), and is held there so that the
 // cumulative sums stay finite (g = -inf is a reset).
@@ -220,6 +227,7 @@ struct Walk {
     static constexpr int TB = CT / 32;           // 32-row blocks
     static constexpr int KT = DA / 16;           // 16-row tiles of S^T
     static constexpr int WV = DC / 16;           // waves
+    static constexpr int GD = 4;                 // chunks whose decays are formed together, by a wave each
     static constexpr int NT = 64 * WV;
     // waves a SIMD: two blocks to a compute unit where their LDS fits (and
     // with 256 rows of S^T a wave needs the registers of two)
@@ -239,8 +247,9 @@ struct Walk {
         T a[OUT ? CT * DA : 8];
         T x[DOT ? CT * DC : 8];
         T p[OUT ? CT * CT : 8];
-        float gh[2][CT], gl[2][CT];  // G as two floats
-        float eg[2][CT], wg[2][CT];  // 2^G_i and sb 2^(G_end - G_i)
+        // decays of GD chunks: G as two floats, 2^G_i, sb 2^(G_end - G_i), G_end
+        float gh[OUT ? GD : 1][CT], gl[OUT ? GD : 1][CT], eg[OUT ? GD : 1][CT], wg[GD][CT];
+        double gend[GD];
         float rho[DOT ? WV * CT : 4];  // rows' shares: of the columns of a wave,
         float rho_p[DOT ? 16 * NP : 4];  // and of a score tile
     };
@@ -319,27 +328,17 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
     typedef Rows<T, DA, NT, W::UA> RA;
     typedef Rows<T, DC, NT, W::UC> RC;
-    // a chunk's rows of b and c and its log decays on their way; the segment
-    // pass, which has the registers, keeps two chunks' under way
+    // a chunk's rows of b and c on their way; the segment pass, which has the registers, keeps two chunks' under way
     struct Set {
         RA b;
         RC c;
-        float g;
     };
     constexpr int AHEAD = OUT ? 1 : 2;
     Set set[AHEAD];
-    const bool decayer = wave == W::WV - 1;  // the wave that forms the decays (it has fewer score tiles)
-    // rows [c0, c0 + n) of the walk into registers (g: one row a lane, asked for
-    // first, so that the wait for it leaves the rows in flight)
+    // rows [c0, c0 + n) of the walk into registers
     auto fetch = [&](int64_t c0, int n, Set &r) {
         const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
         const int tid = wave * 64 + lane;
-        r.g = 0.f;
-        if (pg && decayer) {
-            // backwards, a row is entered through the decay of the row after it
-            const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
-            if (lane < n && t < eos_in) r.g = pg[t * w.g_ts];
-        }
         r.b.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
         r.c.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
     };
@@ -354,25 +353,41 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     // weight then reaches to the segment's end and the sum is never scaled):
     // the rows walk that follows starts on the rows that were read last, which
     // the last level of cache still holds.
-    double tot = 0.0;  // log2 decay of the chunks taken (in the decayer)
-    auto decays = [&](int n, int buf, float g) {
-        if (!decayer) return;
-        const double G = wave_inclusive_sum_f64(lane < n && pg ? decay_log2(g) : 0.0);
-        const double Gend = __shfl(G, 63, 64);
-        if (lane < CT) {
-            if constexpr (OUT) {
-                const float hi = (float)G;
-                sm.gh[buf][lane] = hi;
-                sm.gl[buf][lane] = (float)(G - (double)hi);
-                sm.eg[buf][lane] = __builtin_amdgcn_exp2f((float)G);
-            }
-            sm.wg[buf][lane] = w.sb * __builtin_amdgcn_exp2f((float)(OUT ? Gend - G : Gend - G + tot));
-        }
-        tot += Gend;
-    };
     const int64_t nch = ceil_div64(len, CT);
     const int64_t cfirst = OUT || nch == 0 ? 0 : (nch - 1) * CT, cstep = OUT ? CT : -CT;
     auto rows_of = [&](int64_t c0) { return len - c0 < CT ? (int)(len - c0) : CT; };
+
+    // The decays of GD chunks at once, one chunk to each of the last GD waves;
+    // their log decays (one row a lane) are asked for a group ahead.
+    float rg = 0.f;
+    auto fetch_g = [&](int64_t group) {
+        const int64_t k = group * W::GD + wave - (W::WV - W::GD);
+        rg = 0.f;
+        if (!pg || wave < W::WV - W::GD || k >= nch) return;
+        const int64_t c0 = cfirst + k * cstep;
+        const int n = rows_of(c0);
+        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
+        // backwards, a row is entered through the decay of the row after it
+        const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
+        if (lane < n && t < eos_in) rg = pg[t * w.g_ts];
+    };
+    auto decays = [&]() {  // rows past the chunk's end have none, nor have chunks past the walk's
+        const int k = wave - (W::WV - W::GD);
+        if (k < 0) return;
+        const double G = wave_inclusive_sum_f64(decay_log2(rg)), Gend = lane63_f64(G);
+        if (lane < CT) {
+            if constexpr (OUT) {
+                const float hi = (float)G;
+                sm.gh[k][lane] = hi;
+                sm.gl[k][lane] = (float)(G - (double)hi);
+                sm.eg[k][lane] = __builtin_amdgcn_exp2f((float)G);
+            }
+            sm.wg[k][lane] = w.sb * __builtin_amdgcn_exp2f((float)(Gend - G));
+        }
+        if (lane == 0) sm.gend[k] = Gend;
+    };
+    double tot = 0.0;  // segment pass: log2 decay of the chunks taken
+    fetch_g(0);
     if (nch > 0) {
         fetch(cfirst, rows_of(cfirst), set[0]);
         if (AHEAD == 2 && nch > 1) fetch(cfirst + cstep, rows_of(cfirst + cstep), set[AHEAD - 1]);
@@ -406,22 +421,22 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     if constexpr (OUT) {
         for (int i = threadIdx.x; i < CT * CT; i += NT) sm.p[i] = from_f32<T>(0.f);
     }
-    if (nch > 0) decays(rows_of(cfirst), 0, set[0].g);
 
     // The barriers order LDS only: the next chunk's rows stay in flight over
     // them, and so do the stores of y.
-    auto chunk = [&](int64_t ch, Set &cur, const Set &next) __attribute__((always_inline)) {
-        const int64_t c0 = cfirst + ch * cstep, c1 = c0 + cstep;  // this chunk's first row and the next one's
-        const int n = rows_of(c0), n1 = rows_of(c1);
-        const int buf = (int)(ch & 1);
+    auto chunk = [&](int64_t ch, Set &cur) __attribute__((always_inline)) {
+        const int64_t c0 = cfirst + ch * cstep;  // the chunk's first row
+        const int n = rows_of(c0), buf = (int)(ch % W::GD);
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
         asm volatile("" : "+v"(lane));
         const int m = lane & 15, g4 = lane >> 4, tid = wave * 64 + lane;
         cur.b.stage(sm.b, tid);
         cur.c.stage(sm.c, tid);
+        if (buf == 0) decays();
         if constexpr (OUT) wait_vmcnt<0>();  // a and x
         lds_barrier();
+        if (buf == 0) fetch_g(ch / W::GD + 1);
         if (ch + AHEAD < nch) fetch(c0 + AHEAD * cstep, rows_of(c0 + AHEAD * cstep), cur);
         const int arow = TA::row_base(lane);
 
@@ -495,7 +510,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 }
             }
             lds_barrier();
-            if (ch + 1 < nch) fetch_ax(c1, n1);
+            if (ch + 1 < nch) fetch_ax(c0 + CT, rows_of(c0 + CT));
         }
 
         // the rows c as operands, once for P c and (decayed) for the state
@@ -507,13 +522,15 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
             for (int kt = 0; kt < W::KT; ++kt) s[kt] *= dec;
         }
+        const float later = OUT ? 1.f : __builtin_amdgcn_exp2f((float)tot);  // the chunks taken before come after it
+        if constexpr (!OUT) tot += sm.gend[buf];
 #pragma unroll
         for (int tb = 0; tb < W::TB; ++tb) {
             const frag fc = TC::template col8<4>(sm.c, ccol, lane, tb, 0, 0);
             frag fw[NS];
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = to_f32(fc[i]) * sm.wg[buf][32 * tb + 8 * g4 + i];
+            for (int i = 0; i < 8; ++i) v[i] = to_f32(fc[i]) * (sm.wg[buf][32 * tb + 8 * g4 + i] * later);
             split8<T, NS>(v, fw);
             if constexpr (OUT) {
 #pragma unroll
@@ -533,7 +550,6 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                     for (int k = 0; k < W::KG; ++k) s[k0 + k] = mma(fb[k], fw[p], s[k0 + k]);
             }
         }
-        if (ch + 1 < nch) decays(n1, buf ^ 1, next.g);
         if constexpr (OUT) {
             // rows of y as a buffer that ends with the chunk, like the inputs' (stores past it are dropped)
             const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
@@ -572,8 +588,8 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         }
     };
     for (int64_t ch = 0; ch < nch; ch += AHEAD) {
-        chunk(ch, set[0], set[AHEAD - 1]);
-        if (AHEAD == 2 && ch + 1 < nch) chunk(ch + 1, set[AHEAD - 1], set[0]);
+        chunk(ch, set[0]);
+        if (AHEAD == 2 && ch + 1 < nch) chunk(ch + 1, set[AHEAD - 1]);
     }
 
     // the state after the walk: the segment's own (segment pass), or the sequence's
@@ -581,7 +597,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     float f = 1.f;
     if constexpr (!OUT) {
         so = w.seg_out + ((it.slot0 + it.seg) * w.HV + hv) * (int64_t)w.dc * DA;
-        if (decayer && lane == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = (float)tot;
+        if (threadIdx.x == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = (float)tot;
     } else if (at_end && w.s_out) {
         so = w.s_out + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
         if (w.rev && pg && it.eos > it.bos)  // through the first row's decay too
