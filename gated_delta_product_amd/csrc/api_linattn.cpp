@@ -320,7 +320,6 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
         b.b = q;
         b.c = o;
         b.sb = a.scale;
-        b.rev = true;
         b.seg_out = ws.r;
         b.seg_tot = ws.r_tot;
         if ((st = hip_status(gdp::launch_lin_walks({{f, b, {}}, 2}, a.dtype, false, want_g || d->dh0, s), name)) != GDP_OK)
@@ -351,7 +350,6 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     w.b = o;
     w.c = q;
     w.x = k;
-    w.rev = true;
     w.s0 = d->dht;
     w.seg_in = p.segments ? ws.r : nullptr;
     w.sb = a.scale;

@@ -26,7 +26,6 @@ struct LinWalk {
     const int32_t *cu;
     const float *g;    // log decay of (b, t, hv) at g + b*g_bs + t*g_ts + hv, or NULL
     int64_t g_bs, g_ts;
-    bool rev;          // backwards in time
     bool trans;        // states that are read hold element (c, a) at [a][c]
     bool y32;          // y is float
     void *y;           // [B, T, HV, dc]
@@ -38,7 +37,8 @@ struct LinWalk {
     float *seg_tot;
 };
 
-// The walks of a launch: one or two of one shape, or the gradients' three.
+// The walks of a launch: one forwards, with a second one of its shape backwards
+// (segment passes), or the gradients' three (dq's forwards, the others back).
 struct LinWalks {
     LinWalk w[3];
     int n;

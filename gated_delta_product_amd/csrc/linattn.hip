@@ -263,26 +263,28 @@ template <typename T, int D, int NT, int UNITS>
 struct Rows {
     static constexpr int E = 16 / sizeof(T), UPR = D / E, STEP = NT / UPR;
     uint4 r[UNITS];
-    __device__ __forceinline__ void fetch(const T *base, int64_t ts_elems, int n, bool rev, int tid) {
-        const uint32_t ts = (uint32_t)ts_elems * sizeof(T);  // bytes of a row
+    template <bool REV>
+    __device__ __forceinline__ void fetch(const T *base, uint32_t ts_elems, int n, int tid) {
+        const uint32_t ts = ts_elems * sizeof(T);  // bytes of a row
         const rsrc_t rs = make_rsrc(base, (uint32_t)(n - 1) * ts + D * sizeof(T));
         const int row = tid / UPR;
-        const uint32_t off = (uint32_t)(rev ? n - 1 - row : row) * ts + tid % UPR * 16;
-        const uint32_t step = rev ? 0u - STEP * ts : STEP * ts;
+        const uint32_t off = (uint32_t)(REV ? n - 1 - row : row) * ts + tid % UPR * 16;
+        const uint32_t step = REV ? 0u - STEP * ts : STEP * ts;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) r[i] = buf_load16(rs, off + i * step);
     }
     // The same rows straight into a tile (no registers): lane 16-byte slots of
     // LDS lie in a row, so each lane asks for the unit that belongs in its slot.
-    static __device__ __forceinline__ void dma(T *t, const T *base, int64_t ts_elems, int n, bool rev, int wave, int lane) {
-        const uint32_t ts = (uint32_t)ts_elems * sizeof(T);
+    template <bool REV>
+    static __device__ __forceinline__ void dma(T *t, const T *base, uint32_t ts_elems, int n, int wave, int lane) {
+        const uint32_t ts = ts_elems * sizeof(T);
         const rsrc_t rs = make_rsrc(base, (uint32_t)(n - 1) * ts + D * sizeof(T));
         const uint32_t lds = lds_addr(t) + wave * 1024;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i) {
             const int slot = NT * i + wave * 64 + lane, row = slot / UPR;
             const uint32_t unit = (uint32_t)(slot % UPR) ^ swz<UPR>(row);
-            dma16(rs, (uint32_t)(rev ? n - 1 - row : row) * ts + unit * 16, lds + NT * 16 * i);
+            dma16(rs, (uint32_t)(REV ? n - 1 - row : row) * ts + unit * 16, lds + NT * 16 * i);
         }
     }
     __device__ __forceinline__ void stage(T *t, int tid) const {
@@ -297,7 +299,7 @@ struct Rows {
     }
 };
 
-template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT, bool REV>
 __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, int slice,
                                          typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds &sm) {
     typedef Walk<T, DA, DC, NS, NQ, OUT, DOT> W;
@@ -313,17 +315,23 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     if (it.seq < 0) return;
     const int64_t t0 = it.bos + it.seg * w.seg_tok;
     const int64_t t1 = t0 + w.seg_tok < it.eos ? t0 + w.seg_tok : it.eos;
-    const bool at_end = w.rev ? it.seg == 0 : t1 == it.eos;  // the walk's last segment of the sequence
+    const bool at_end = REV ? it.seg == 0 : t1 == it.eos;  // the walk's last segment of the sequence
     if (!OUT && at_end) return;  // no segment is entered from it
-    const int64_t len = t1 - t0;
+    const int len = (int)(t1 - t0);
     // batch row and the token offset inside it (packed rows are one batch row)
     const int64_t bi = w.cu ? 0 : it.seq, tb0 = w.cu ? t0 : t0 - it.bos;
     const int64_t eos_in = w.cu ? it.eos : w.T;
 
-    const T *pa = (const T *)w.a.p + bi * w.a.bs + (int64_t)(hv / w.a.div) * DA;
-    const T *pb = (const T *)w.b.p + bi * w.b.bs + (int64_t)(hv / w.b.div) * DA;
-    const T *pc = (const T *)w.c.p + bi * w.c.bs + (int64_t)(hv / w.c.div) * w.dc + slice * DC;
-    const T *px = DOT ? (const T *)w.x.p + bi * w.x.bs + (int64_t)(hv / w.x.div) * w.dc + slice * DC : nullptr;
+    // the segment's lowest row of each tensor, and row r from there
+    auto base_of = [&](const LinRows &r, int d, int first) {
+        return (const T *)r.p + bi * r.bs + tb0 * r.ts + (int64_t)(hv / r.div) * d + first;
+    };
+    const T *pa = OUT ? base_of(w.a, DA, 0) : nullptr, *pb = base_of(w.b, DA, 0), *pc = base_of(w.c, w.dc, slice * DC);
+    const T *px = DOT ? base_of(w.x, w.dc, slice * DC) : nullptr;
+    const uint32_t sa = (uint32_t)w.a.ts, sb = (uint32_t)w.b.ts, sc = (uint32_t)w.c.ts, sx = (uint32_t)w.x.ts;
+    auto row = [](const T *p, uint32_t ts, int r) { return p + (uint64_t)(uint32_t)r * ts; };
+    // lowest of the n rows that follow row c0 of the walk
+    auto lowest = [&](int c0, int n) { return REV ? len - c0 - n : c0; };
     const float *pg = w.g ? w.g + bi * w.g_bs + hv : nullptr;
 
     typedef Rows<T, DA, NT, W::UA> RA;
@@ -336,40 +344,37 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     constexpr int AHEAD = OUT ? 1 : 2;
     Set set[AHEAD];
     // rows [c0, c0 + n) of the walk into registers
-    auto fetch = [&](int64_t c0, int n, Set &r) {
-        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;  // the lowest token
-        const int tid = wave * 64 + lane;
-        r.b.fetch(pb + first * w.b.ts, w.b.ts, n, w.rev, tid);
-        r.c.fetch(pc + first * w.c.ts, w.c.ts, n, w.rev, tid);
+    auto fetch = [&](int c0, int n, Set &r) {
+        const int lo = lowest(c0, n), tid = wave * 64 + lane;
+        r.b.template fetch<REV>(row(pb, sb, lo), sb, n, tid);
+        r.c.template fetch<REV>(row(pc, sc, lo), sc, n, tid);
     };
     // a and x are done with halfway through a chunk: the next rows then go into
     // their tiles directly (b and c, needed to its end, wait in registers)
-    auto fetch_ax = [&](int64_t c0, int n) {
-        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
-        RA::dma(sm.a, pa + first * w.a.ts, w.a.ts, n, w.rev, wave, lane);
-        if constexpr (DOT) RC::dma(sm.x, px + first * w.x.ts, w.x.ts, n, w.rev, wave, lane);
+    auto fetch_ax = [&](int c0, int n) {
+        const int lo = lowest(c0, n);
+        RA::template dma<REV>(sm.a, row(pa, sa, lo), sa, n, wave, lane);
+        if constexpr (DOT) RC::template dma<REV>(sm.x, row(px, sx, lo), sx, n, wave, lane);
     };
     // The segment pass takes its chunks from the last to the first (each row's
     // weight then reaches to the segment's end and the sum is never scaled):
     // the rows walk that follows starts on the rows that were read last, which
     // the last level of cache still holds.
-    const int64_t nch = ceil_div64(len, CT);
-    const int64_t cfirst = OUT || nch == 0 ? 0 : (nch - 1) * CT, cstep = OUT ? CT : -CT;
-    auto rows_of = [&](int64_t c0) { return len - c0 < CT ? (int)(len - c0) : CT; };
+    const int nch = (int)(((uint32_t)len + (CT - 1)) / CT);
+    const int cfirst = OUT || nch == 0 ? 0 : (nch - 1) * CT, cstep = OUT ? CT : -CT;
+    auto rows_of = [&](int c0) { return len - c0 < CT ? len - c0 : CT; };
 
     // The decays of GD chunks at once, one chunk to each of the last GD waves;
     // their log decays (one row a lane) are asked for a group ahead.
     float rg = 0.f;
-    auto fetch_g = [&](int64_t group) {
-        const int64_t k = group * W::GD + wave - (W::WV - W::GD);
+    auto fetch_g = [&](int group) {
+        const int k = group * W::GD + wave - (W::WV - W::GD);
         rg = 0.f;
         if (!pg || wave < W::WV - W::GD || k >= nch) return;
-        const int64_t c0 = cfirst + k * cstep;
-        const int n = rows_of(c0);
-        const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
+        const int c0 = cfirst + k * cstep;
         // backwards, a row is entered through the decay of the row after it
-        const int64_t t = w.rev ? first + n - 1 - lane + 1 : first + lane;
-        if (lane < n && t < eos_in) rg = pg[t * w.g_ts];
+        const int64_t t = tb0 + (REV ? len - c0 - lane : c0 + lane);
+        if (lane < rows_of(c0) && t < eos_in) rg = pg[t * w.g_ts];
     };
     auto decays = [&]() {  // rows past the chunk's end have none, nor have chunks past the walk's
         const int k = wave - (W::WV - W::GD);
@@ -397,6 +402,8 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     // entering state: S^T tiles [kt], rows a = 32 (kt/2) + 8 g4 + 4 (kt%2) + i, column c
     f32x4 s[W::KT];
     const int cw = wave * 16;  // first column of this wave in the slice
+    const uint32_t yrow = (uint32_t)w.HV * w.dc;  // elements of a row of y, and its first one of this wave
+    const int64_t y0 = ((bi * w.T + tb0) * w.HV + hv) * (int64_t)w.dc + slice * DC + cw;
     {
         const int m = lane & 15, g4 = lane >> 4, col = slice * DC + cw + m;
         const float *s0 = nullptr;
@@ -424,9 +431,9 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
     // The barriers order LDS only: the next chunk's rows stay in flight over
     // them, and so do the stores of y.
-    auto chunk = [&](int64_t ch, Set &cur) __attribute__((always_inline)) {
-        const int64_t c0 = cfirst + ch * cstep;  // the chunk's first row
-        const int n = rows_of(c0), buf = (int)(ch % W::GD);
+    auto chunk = [&](int ch, Set &cur) __attribute__((always_inline)) {
+        const int c0 = cfirst + ch * cstep;  // the chunk's first row
+        const int n = rows_of(c0), buf = ch % W::GD;
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
         asm volatile("" : "+v"(lane));
@@ -552,11 +559,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         }
         if constexpr (OUT) {
             // rows of y as a buffer that ends with the chunk, like the inputs' (stores past it are dropped)
-            const int64_t first = w.rev ? tb0 + len - c0 - n : tb0 + c0;
-            const int64_t e = ((bi * w.T + first) * w.HV + hv) * (int64_t)w.dc + slice * DC + cw;
-            const uint32_t es = w.y32 ? 4 : sizeof(T), ys = (uint32_t)w.HV * w.dc * es;
-            const rsrc_t rs = make_rsrc((const char *)w.y + e * es, (uint32_t)(n - 1) * ys + 16 * es);
-            const uint32_t off = (uint32_t)(w.rev ? n - 1 - m : m) * ys + 4 * g4 * es, step = w.rev ? 0u - 16 * ys : 16 * ys;
+            const uint32_t es = w.y32 ? 4 : sizeof(T), ys = yrow * es;
+            const char *yp = (const char *)w.y + (y0 + (uint64_t)(uint32_t)lowest(c0, n) * yrow) * es;
+            const rsrc_t rs = make_rsrc(yp, (uint32_t)(n - 1) * ys + 16 * es);
+            const uint32_t off = (uint32_t)(REV ? n - 1 - m : m) * ys + 4 * g4 * es, step = REV ? 0u - 16 * ys : 16 * ys;
             const float sy = w.sy;
             if (F32_Y<T> || w.y32) {
 #pragma unroll
@@ -582,12 +588,12 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 for (int i = 0; i < W::WV; ++i) q += sm.rho[i * CT + lane];
                 const int ib = lane / 16;
                 for (int jb = 0; jb <= ib; ++jb) q += sm.rho_p[16 * (ib * (ib + 1) / 2 + jb) + lane % 16];
-                const int64_t t = w.rev ? tb0 + len - 1 - c0 - lane : tb0 + c0 + lane;
-                w.rho[((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + t] = q * w.sy;
+                const int64_t r0 = ((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + tb0;
+                w.rho[r0 + (REV ? len - 1 - c0 - lane : c0 + lane)] = q * w.sy;
             }
         }
     };
-    for (int64_t ch = 0; ch < nch; ch += AHEAD) {
+    for (int ch = 0; ch < nch; ch += AHEAD) {
         chunk(ch, set[0]);
         if (AHEAD == 2 && ch + 1 < nch) chunk(ch + 1, set[AHEAD - 1]);
     }
@@ -600,7 +606,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         if (threadIdx.x == 0 && slice == 0) w.seg_tot[(it.slot0 + it.seg) * w.HV + hv] = (float)tot;
     } else if (at_end && w.s_out) {
         so = w.s_out + (it.seq * w.HV + hv) * (int64_t)w.dc * DA;
-        if (w.rev && pg && it.eos > it.bos)  // through the first row's decay too
+        if (REV && pg && it.eos > it.bos)  // through the first row's decay too
             f = __builtin_amdgcn_exp2f((float)decay_log2(pg[(w.cu ? it.bos : 0) * w.g_ts]));
     }
     if (!so) return;
@@ -611,13 +617,13 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 }
 
 // The block's item, value head and column slice.
-template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT, bool REV>
 __device__ __forceinline__ void lin_block(const LinWalk &w, void *lds) {
     const uint32_t b = blockIdx.x, slices = w.dc / DC, per = (uint32_t)w.HV * slices;
     const uint32_t id = b / per, r = b - id * per;
     if (id >= w.items) return;
-    lin_walk<T, DA, DC, NS, NQ, OUT, DOT>(w, id, (int)(r / slices), (int)(r % slices),
-                                          *(typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds *)lds);
+    lin_walk<T, DA, DC, NS, NQ, OUT, DOT, REV>(w, id, (int)(r / slices), (int)(r % slices),
+                                               *(typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds *)lds);
 }
 
 template <typename T, int DA, int DC, int NS, bool OUT>
@@ -625,7 +631,8 @@ __global__ void __launch_bounds__((Walk<T, DA, DC, NS, 1, OUT, false>::NT), (Wal
 gdp_lin_walk_k(LinWalks p) {
     typedef Walk<T, DA, DC, NS, 1, OUT, false> W;
     __shared__ __align__(16) char lds[sizeof(typename W::Lds)];
-    lin_block<T, DA, DC, NS, 1, OUT, false>(p.w[blockIdx.y], lds);
+    if (blockIdx.y == 0) lin_block<T, DA, DC, NS, 1, OUT, false, false>(p.w[0], lds);
+    else if constexpr (!OUT) lin_block<T, DA, DC, NS, 1, OUT, false, true>(p.w[1], lds);
 }
 
 // The three walks of the gradients in one launch: dq and dk (DA = V, slices of
@@ -642,8 +649,9 @@ struct Grads {
 template <typename T, int K, int V, int SL, int NS, int NQ, int ND, bool DOT>
 __global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, ND, DOT>::OCC)) gdp_lin_grads_k(LinWalks p) {
     __shared__ __align__(16) char lds[Grads<T, K, V, SL, NS, NQ, ND, DOT>::BYTES];
-    if (blockIdx.y < 2) lin_block<T, V, SL, NS, NQ, true, DOT>(p.w[blockIdx.y], lds);
-    else lin_block<T, K, SL, ND, 1, true, false>(p.w[2], lds);
+    if (blockIdx.y == 0) lin_block<T, V, SL, NS, NQ, true, DOT, false>(p.w[0], lds);
+    else if (blockIdx.y == 1) lin_block<T, V, SL, NS, NQ, true, DOT, true>(p.w[1], lds);
+    else lin_block<T, K, SL, ND, 1, true, false, true>(p.w[2], lds);
 }
 
 // ---------------------------------------------------------------- the scan over segments
