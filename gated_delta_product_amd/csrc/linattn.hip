@@ -466,13 +466,14 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                         e = mma(TC::row8(sm.c, crow, jb, kb), TC::row8(sm.x, crow, ib, kb), e);
                 }
                 const int i = 16 * ib + m, j0 = 16 * jb + 4 * g4;
+                const float sbsy = w.sb * w.sy;
                 const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
                 const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
                 typename Frag<T>::half pv;
                 float q = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r])) * w.sb;
+                    const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r])) * sbsy;
                     const float sc = j0 + r <= i ? (acc[0][r] + acc[1][r]) * d : 0.f;
                     pv[r] = from_f32<T>(sc);
                     if constexpr (DOT) q += j0 + r < i ? sc * e[r] : 0.f;
@@ -506,7 +507,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             }
 #pragma unroll
             for (int ib = 0; ib < W::NB; ++ib) {
-                y[ib] *= sm.eg[buf][16 * ib + m];
+                y[ib] *= sm.eg[buf][16 * ib + m] * w.sy;
                 if constexpr (DOT) {
                     const auto xv = *(const typename Frag<T>::half *)(sm.x + TC::at(16 * ib + m, cw + 4 * g4));
                     float q = 0.f;
@@ -563,18 +564,17 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             const char *yp = (const char *)w.y + (y0 + (uint64_t)(uint32_t)lowest(c0, n) * yrow) * es;
             const rsrc_t rs = make_rsrc(yp, (uint32_t)(n - 1) * ys + 16 * es);
             const uint32_t off = (uint32_t)(REV ? n - 1 - m : m) * ys + 4 * g4 * es, step = REV ? 0u - 16 * ys : 16 * ys;
-            const float sy = w.sy;
             if (F32_Y<T> || w.y32) {
 #pragma unroll
                 for (int ib = 0; ib < W::NB; ++ib) {
-                    const f32x4 v = y[ib] * sy;
+                    const f32x4 v = y[ib];
                     buf_store16(rs, off + ib * step, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
                                                                 __float_as_uint(v[2]), __float_as_uint(v[3])));
                 }
             } else {
 #pragma unroll
                 for (int ib = 0; ib < W::NB; ++ib) {
-                    const f32x4 v = y[ib] * sy;
+                    const f32x4 v = y[ib];
                     const bf16x4 o = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                     buf_store8(rs, off + ib * step, __builtin_bit_cast(uint2, o));
                 }
@@ -589,7 +589,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 const int ib = lane / 16;
                 for (int jb = 0; jb <= ib; ++jb) q += sm.rho_p[16 * (ib * (ib + 1) / 2 + jb) + lane % 16];
                 const int64_t r0 = ((int64_t)slice * w.HV + hv) * (w.B * w.T) + bi * w.T + tb0;
-                w.rho[r0 + (REV ? len - 1 - c0 - lane : c0 + lane)] = q * w.sy;
+                w.rho[r0 + (REV ? len - 1 - c0 - lane : c0 + lane)] = q;
             }
         }
     };
