@@ -457,3 +457,87 @@ def test_graph_replays():
         want = _step(d, cu)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(want, got)), k
+
+
+# ------------------------------------------------------------------ through the C ABI
+
+def _abi(d, cu=None, **kw):
+    t = {k: gpu(d[k]) for k in ("q", "k", "v", "g", "h0", "dht", "do")}
+    B, T, H, K = t["q"].shape
+    HV, V = t["v"].shape[2:]
+    a = G.LinattnArgs(B=B, T=T, H=H, HV=HV, K=K, V=V, scale=0.0, dtype=G._dtype_code(t["q"].dtype),
+                      cu_seqlens=None if cu is None else cu.data_ptr(), num_seqs=0 if cu is None else cu.numel() - 1,
+                      **{x: t[x].data_ptr() for x in ("q", "k", "v", "g", "h0")},
+                      **{"%s_%s_stride" % (x, y): t[x].stride(i) for x in ("q", "k", "v", "g")
+                         for i, y in enumerate("bt")}, **kw)
+    return t, a
+
+
+def _space(a, backward):
+    import ctypes
+    need = G.lib().gdp_linattn_workspace_bytes(ctypes.byref(a), backward)
+    return torch.full((max(need, 256),), 0xA5, dtype=torch.uint8, device=DEV), need
+
+
+@pytest.mark.parametrize("T", [100, 2000])
+def test_final_state_in_place_of_the_initial_one(T):
+    """ht on top of h0, in one pass and in segments, from a workspace full of garbage."""
+    import ctypes
+    d = draws(30, [T], 1, 2, 64, 128, BF16, "token", True, 1)
+    o, ht = run_fwd(d, None)
+    t, a = _abi(d)
+    out = torch.empty_like(o)
+    a.o, a.ht = out.data_ptr(), t["h0"].data_ptr()
+    ws, need = _space(a, 0)
+    assert (need > 0) == (T > 512)
+    G._check(G.lib().gdp_linattn_fwd(ctypes.byref(a), ws.data_ptr(), need, G._stream(torch.device(DEV))))
+    torch.cuda.synchronize()
+    assert torch.equal(out, o) and torch.equal(t["h0"], ht)
+
+
+@pytest.mark.parametrize("T", [100, 2000])
+def test_gradients_that_are_not_wanted(T):
+    """dg without dh0 (the library forms what it needs of it itself), dh0 without dg, and neither."""
+    import ctypes
+    d = draws(31, [T], 1, 2, 64, 64, F32, "token", True, 1)
+    want = G.linattn_bwd(*(gpu(d[x]) for x in ("do", "q", "k", "v", "g")), initial_state=gpu(d["h0"]), dht=gpu(d["dht"]))
+    for with_g, with_h in ((True, False), (False, True), (False, False)):
+        t, a = _abi(d)
+        dq, dk, dv = (torch.empty_like(t[x]) for x in ("q", "k", "v"))
+        dg, dh0 = torch.empty_like(t["g"]), torch.empty_like(t["h0"])
+        r = G.LinattnGrads(dout=t["do"].data_ptr(), do_b_stride=t["do"].stride(0), do_t_stride=t["do"].stride(1),
+                           dht=t["dht"].data_ptr(), dq=dq.data_ptr(), dk=dk.data_ptr(), dv=dv.data_ptr(),
+                           dg=dg.data_ptr() if with_g else None, dh0=dh0.data_ptr() if with_h else None)
+        ws, need = _space(a, 1)
+        G._check(G.lib().gdp_linattn_bwd(ctypes.byref(a), ctypes.byref(r), ws.data_ptr(), need,
+                                         G._stream(torch.device(DEV))))
+        torch.cuda.synchronize()
+        for x, y in ((dq, want[0]), (dk, want[1]), (dv, want[2])):
+            assert float((x.double() - y.double()).norm()) <= 1e-5 * float(y.double().norm())
+        assert not with_g or torch.equal(dg, want[3])
+        assert not with_h or torch.equal(dh0, want[4])
+
+
+def test_many_short_requests():
+    """More requests than a wave has lanes, some empty, none in segments."""
+    gen = torch.Generator().manual_seed(32)
+    lens = torch.randint(0, 9, (150,), generator=gen).tolist()
+    d = draws(33, lens, 1, 1, 64, 64, BF16, "token", True)
+    check_fwd(d)
+    check_bwd(d)
+
+
+def test_norm_of_the_gated_delta_product():
+    """The output norm behind the other mixer: o [B, T, HV, V] of chunk_fwd, normalised per head and gated."""
+    from gated_delta_product_amd import synth
+    from helpers import gates
+    B, T, H, K, V, M = 1, 150, 2, 64, 128, 2
+    c = synth.chunk_draws(B, T, H, H, K, V, M, "bf16", 34)
+    beta, g = gates(c)
+    buf = G.chunk_fwd(*(x.to(DEV) for x in (c["q"], c["k"], c["v"], beta.reshape(B, T * M, H), g)))
+    z, w = torch.randn(B, T, H * V, dtype=BF16, device=DEV), torch.randn(H * V, device=DEV)
+    y = G.group_norm_fwd(buf.o.flatten(2), H, w, gate=z, centered=False)
+    x = buf.o.double()
+    want = (x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-5)).flatten(2) * w.double()
+    want = want * (z.double() / (1 + torch.exp(-z.double())))
+    assert ((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all()
