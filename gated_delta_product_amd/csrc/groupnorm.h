@@ -13,6 +13,7 @@ struct GroupNorm {
     int64_t rows, split;  // rows = n * T; split: row sets side by side
     uint32_t T;
     int groups, D, act;
+    int join;             // row sets of a block whose partial sums it joins (set at launch)
     bool centered, vec, bwd;  // vec: every row of every tensor starts on 16 bytes
     float eps;
     const float *w, *b;
@@ -21,6 +22,6 @@ struct GroupNorm {
 };
 
 int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd);
-hipError_t launch_group_norm(const GroupNorm &p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_group_norm(GroupNorm p, gdp_dtype dtype, hipStream_t stream);
 
 }  // namespace gdp

@@ -154,14 +154,20 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_k(GroupNorm p) {
     }
 }
 
+// Threads of a block backwards: with few elements a thread, large blocks hold
+// the same channels of several rows (p.join) and add those up in LDS before
+// they write partial sums.
+constexpr int bwd_threads(int n) { return n <= 8 ? 512 : 256; }
+
 template <typename T, int E, int LPG, int NU, bool GATE>
-__global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
-    constexpr int N = E * NU;
-    const int64_t set = ((int64_t)blockIdx.x * GNT + threadIdx.x) / LPG;
+__global__ void __launch_bounds__(bwd_threads(E * NU)) gdp_group_norm_bwd_k(GroupNorm p) {
+    constexpr int N = E * NU, NT = bwd_threads(N);
+    const int64_t set = ((int64_t)blockIdx.x * NT + threadIdx.x) / LPG;
     const int l = threadIdx.x % LPG;
     const uint32_t gi = (uint32_t)(set % p.groups);
     const int64_t r0 = set / p.groups;
-    if (r0 >= p.split) return;
+    const bool any = r0 < p.split;
+    if (!any && p.join == 1) return;
     const int col = (int)gi * p.D;
     const int64_t C = (int64_t)p.groups * p.D;
     const float inv = 1.0f / (float)p.D;
@@ -185,8 +191,8 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
         ry.load((const T *)p.dy + row_at((uint32_t)row, p.T, p.dy_ns, p.dy_ts) + col, l, p.D);
         if constexpr (GATE) rz.load((const T *)p.z + row_at((uint32_t)row, p.T, p.z_ns, p.z_ts) + col, l, p.D);
     };
-    if constexpr (AHEAD) load(r0);
-    for (int64_t row = r0; row < p.rows; row += p.split) {
+    if (AHEAD && any) load(r0);
+    for (int64_t row = any ? r0 : p.rows; row < p.rows; row += p.split) {
         if constexpr (!AHEAD) load(row);
         float v[N], dv[N], zv[GATE ? N : 1];
         rx.floats(v);
@@ -232,8 +238,28 @@ __global__ void __launch_bounds__(GNT) gdp_group_norm_bwd_k(GroupNorm p) {
         }
     }
     if (!p.part) return;
-    // this thread's rows, for its channels: [split][2][C]
-    float *part = p.part + r0 * 2 * C + col;
+    if constexpr (NT > GNT) {
+        if (p.join > 1) {
+            // the block's p.join row sets, one after the other in lanes, for each of dw and db
+            __shared__ float red[NT * N];
+            const int per = p.groups * LPG;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                float *v = which ? db : dw;
+                if (which) __syncthreads();
+#pragma unroll
+                for (int i = 0; i < N; ++i) red[i * NT + threadIdx.x] = v[i];
+                __syncthreads();
+                if ((int)threadIdx.x < per)
+                    for (int j = 1; j < p.join; ++j)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) v[i] += red[i * NT + threadIdx.x + j * per];
+            }
+            if ((int)threadIdx.x >= per) return;
+        }
+    }
+    // these rows, for the thread's channels: [split / join][2][C]
+    float *part = p.part + r0 / p.join * 2 * C + col;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
         const int d = (l + k * LPG) * E;
@@ -294,8 +320,10 @@ Shape shape_of(const GroupNorm &p, gdp_dtype dtype) {
 }
 
 template <typename T, int E, int LPG, int NU>
-hipError_t launch(const GroupNorm &p, hipStream_t stream) {
-    const int64_t blocks = (p.split * p.groups * LPG + GNT - 1) / GNT;
+hipError_t launch(GroupNorm &p, hipStream_t stream) {
+    const int nt = p.bwd ? bwd_threads(E * NU) : GNT, sets = nt / LPG;
+    p.join = p.bwd && nt > GNT && sets % p.groups == 0 ? sets / p.groups : 1;
+    const int64_t blocks = (p.split * p.groups * LPG + nt - 1) / nt;
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks);
@@ -303,14 +331,14 @@ hipError_t launch(const GroupNorm &p, hipStream_t stream) {
         if (p.z) hipLaunchKernelGGL((gdp_group_norm_k<T, E, LPG, NU, true>), grid, dim3(GNT), 0, stream, p);
         else hipLaunchKernelGGL((gdp_group_norm_k<T, E, LPG, NU, false>), grid, dim3(GNT), 0, stream, p);
     } else {
-        if (p.z) hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, true>), grid, dim3(GNT), 0, stream, p);
-        else hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, false>), grid, dim3(GNT), 0, stream, p);
+        if (p.z) hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, true>), grid, dim3(nt), 0, stream, p);
+        else hipLaunchKernelGGL((gdp_group_norm_bwd_k<T, E, LPG, NU, false>), grid, dim3(nt), 0, stream, p);
     }
     return hipGetLastError();
 }
 
 template <typename T, int E>
-hipError_t launch_shape(const GroupNorm &p, const Shape &s, hipStream_t stream) {
+hipError_t launch_shape(GroupNorm &p, const Shape &s, hipStream_t stream) {
     if (s.nu == 1) {
         switch (s.lpg) {
         case 1: return launch<T, E, 1, 1>(p, stream);
@@ -347,15 +375,15 @@ int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
     return s < rows ? s : rows;
 }
 
-hipError_t launch_group_norm(const GroupNorm &p, gdp_dtype dtype, hipStream_t stream) {
+hipError_t launch_group_norm(GroupNorm p, gdp_dtype dtype, hipStream_t stream) {
     const Shape s = shape_of(p, dtype);
     hipError_t e;
     if (dtype == GDP_BF16) e = s.vec ? launch_shape<bf16, 8>(p, s, stream) : launch_shape<bf16, 1>(p, s, stream);
     else e = s.vec ? launch_shape<float, 4>(p, s, stream) : launch_shape<float, 1>(p, s, stream);
     if (e != hipSuccess || !(p.dw || p.db)) return e;
     const int64_t C = (int64_t)p.groups * p.D;
-    hipLaunchKernelGGL(gdp_group_norm_sum_k, dim3((unsigned)((C + 63) / 64), 2), dim3(64 * GSW), 0, stream, p.part, p.split,
-                       C, p.dw, p.db);
+    hipLaunchKernelGGL(gdp_group_norm_sum_k, dim3((unsigned)((C + 63) / 64), 2), dim3(64 * GSW), 0, stream, p.part,
+                       (p.split + p.join - 1) / p.join, C, p.dw, p.db);
     return hipGetLastError();
 }
 
