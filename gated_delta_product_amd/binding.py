@@ -805,9 +805,9 @@ def _token_rows(t, name):
         lead.insert(0, 1)
         strides.insert(0, 0)
     while len(lead) > 2:
-        if strides[0] != strides[1] * lead[1] and lead[0] > 1:
+        if strides[0] != strides[1] * lead[1] and lead[0] > 1 and lead[1] > 1:
             raise ValueError("the leading dimensions of %s must fold into [n, T]" % name)
-        lead[:2], strides[:2] = [lead[0] * lead[1]], [strides[1]]
+        lead[:2], strides[:2] = [lead[0] * lead[1]], [strides[1] if lead[1] > 1 else strides[0]]
     return lead[0], lead[1], strides[0], strides[1]
 
 

@@ -75,6 +75,15 @@ Plan plan_of(const gdp_linattn_args &a, bool backward) {
     return p;
 }
 
+// Whether every launch of a call fits: the walks (4 max(K, V) threads a head and item), dg (512), the scan (256 a head
+// and sequence), and backwards the passes over the tokens of packed requests and of shared heads.
+bool launches_fit(const gdp_linattn_args &a, const Plan &p, bool backward) {
+    const int64_t wide = 4 * (int64_t)(a.K > a.V ? a.K : a.V), n = p.items > p.nseq ? p.items : p.nseq;
+    if (!fits_launch(n * a.HV * (wide > 512 ? wide : 512))) return false;
+    return !backward || (fits_launch((a.T + 63) / 64 * 256) &&
+                         (a.H == a.HV || fits_launch(a.B * a.T * a.H * (a.K / 4) + 255)));
+}
+
 struct FwdSpace {
     float *seg, *tot;
 };
@@ -121,18 +130,19 @@ gdp_status check_dims(const char *name, int32_t H, int32_t HV, int32_t K, int32_
     return ok();
 }
 
-// Rows of a strided input: base and strides on 16 bytes, no overlap, and a chunk of rows within 32-bit offsets.
-gdp_status check_rows(const char *name, const char *what, const void *p, int64_t bs, int64_t ts, int64_t T,
+// Rows of a strided [B, T, width] input: base and strides on 16 bytes, no overlap, and a chunk of rows within 32-bit
+// offsets.  The stride of a dimension of one element does not matter.
+gdp_status check_rows(const char *name, const char *what, const void *p, int64_t bs, int64_t ts, int64_t B, int64_t T,
                       int64_t width, gdp_dtype dtype) {
     const int64_t unit = 16 / (int64_t)dsize(dtype);
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
     if (bs < 0 || ts < 0) return fail(GDP_ERR_INVALID, "%s: strides of %s must be >= 0", name, what);
-    if (!aligned16(p) || bs % unit || ts % unit)
+    if (!aligned16(p) || (B > 1 && bs % unit) || (T > 1 && ts % unit))
         return fail(GDP_ERR_INVALID, "%s: rows of %s are not 16-byte aligned", name, what);
     if (T > 1 && ts < width)
         return fail(GDP_ERR_INVALID, "%s: rows of %s overlap (stride %lld < width %lld)", name, what, (long long)ts,
                     (long long)width);
-    if (ts > (1 << 23)) return fail(GDP_ERR_UNSUPPORTED, "%s: token stride of %s over 2^23 elements", name, what);
+    if (T > 1 && ts > (1 << 23)) return fail(GDP_ERR_UNSUPPORTED, "%s: token stride of %s over 2^23 elements", name, what);
     return ok();
 }
 
@@ -162,9 +172,9 @@ gdp_status check_linattn(const char *name, const gdp_linattn_args *a, bool forwa
         return fail(GDP_ERR_INVALID, "%s: g, g_head or cu_seqlens is not 4-byte aligned", name);
     if (!aligned16(a->h0) || !aligned16(a->ht)) return fail(GDP_ERR_INVALID, "%s: h0 or ht is not 16-byte aligned", name);
     if (a->T == 0 || (forward ? nseq : a->B) == 0) return ok();
-    if ((st = check_rows(name, "q", a->q, a->q_b_stride, a->q_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->T, (int64_t)a->HV * a->V, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "q", a->q, a->q_b_stride, a->q_t_stride, a->B, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->B, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->B, a->T, (int64_t)a->HV * a->V, a->dtype)) != GDP_OK) return st;
     if (forward && (!a->o || !aligned16(a->o))) return fail(GDP_ERR_INVALID, "%s: o is NULL or not 16-byte aligned", name);
     return ok();
 }
@@ -218,6 +228,10 @@ extern "C" {
 int64_t gdp_linattn_workspace_bytes(const gdp_linattn_args *a, int32_t backward) {
     if (check_sizes("gdp_linattn_workspace_bytes", a) != GDP_OK) return -1;
     const Plan p = plan_of(*a, backward != 0);
+    if (!launches_fit(*a, p, backward != 0)) {
+        fail(GDP_ERR_UNSUPPORTED, "gdp_linattn_workspace_bytes: problem too large for one launch");
+        return -1;
+    }
     FwdSpace f;
     BwdSpace b;
     return backward ? lay_bwd(*a, p, nullptr, &b) : lay_fwd(*a, p, nullptr, &f);
@@ -230,6 +244,7 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
     gdp_linattn_args a = *args;
     if (!(a.scale > 0.f)) a.scale = 1.0f / std::sqrt((float)a.K);
     const Plan p = plan_of(a, false);
+    if (!launches_fit(a, p, false)) return fail(GDP_ERR_UNSUPPORTED, "%s: problem too large for one launch", name);
     FwdSpace ws;
     if ((st = check_space(name, workspace, workspace_bytes, lay_fwd(a, p, workspace, &ws))) != GDP_OK) return st;
     if (p.nseq == 0 || (a.T == 0 && !a.ht)) return ok();
@@ -278,8 +293,9 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
         return fail(GDP_ERR_INVALID, "%s: dh0 may not be dht or h0", name);
     if (!(a.scale > 0.f)) a.scale = 1.0f / std::sqrt((float)a.K);
     const Plan p = plan_of(a, true);
+    if (!launches_fit(a, p, true)) return fail(GDP_ERR_UNSUPPORTED, "%s: problem too large for one launch", name);
     if (a.B > 0 && a.T > 0) {
-        if ((st = check_rows(name, "dout", d->dout, d->do_b_stride, d->do_t_stride, a.T, (int64_t)a.HV * a.V,
+        if ((st = check_rows(name, "dout", d->dout, d->do_b_stride, d->do_t_stride, a.B, a.T, (int64_t)a.HV * a.V,
                              a.dtype)) != GDP_OK) return st;
         if (!d->dq || !d->dk || !d->dv || !aligned16(d->dq) || !aligned16(d->dk) || !aligned16(d->dv))
             return fail(GDP_ERR_INVALID, "%s: dq, dk or dv is NULL or not 16-byte aligned", name);
@@ -407,7 +423,8 @@ gdp_status gdp_linattn_decode(const gdp_linattn_decode_args *args, void *stream)
     gdp_status st = check_dims(name, a.H, a.HV, a.K, a.V, a.scale, a.dtype);
     if (st != GDP_OK) return st;
     if (a.n < 0 || a.S < 0) return fail(GDP_ERR_INVALID, "%s: n and S must be >= 0", name);
-    if (a.S > 4096 || a.n > 0x7fffffff / a.V) return fail(GDP_ERR_UNSUPPORTED, "%s: step too large (n or S)", name);
+    // up to K/4 threads for each state row
+    if (a.S > 4096 || a.n > 0xffffffffll / ((int64_t)a.V * (a.K / 4))) return fail(GDP_ERR_UNSUPPORTED, "%s: step too large (n or S)", name);
     if (a.pool < 0 || (!a.slots && a.pool < a.n)) return fail(GDP_ERR_INVALID, "%s: state pool too small", name);
     if (a.g && a.g_head) return fail(GDP_ERR_INVALID, "%s: at most one of g and g_head", name);
     if (a.g && (a.g_n_stride < 0 || a.g_t_stride < 0))
@@ -415,9 +432,9 @@ gdp_status gdp_linattn_decode(const gdp_linattn_decode_args *args, void *stream)
     if (((uintptr_t)a.g | (uintptr_t)a.g_head | (uintptr_t)a.slots) & 3)
         return fail(GDP_ERR_INVALID, "%s: g, g_head or slots is not 4-byte aligned", name);
     if (a.n == 0 || a.S == 0) return ok();
-    if ((st = check_rows(name, "q", a.q, a.q_n_stride, a.q_t_stride, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "k", a.k, a.k_n_stride, a.k_t_stride, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
-    if ((st = check_rows(name, "v", a.v, a.v_n_stride, a.v_t_stride, a.S, (int64_t)a.HV * a.V, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "q", a.q, a.q_n_stride, a.q_t_stride, a.n, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "k", a.k, a.k_n_stride, a.k_t_stride, a.n, a.S, (int64_t)a.H * a.K, a.dtype)) != GDP_OK) return st;
+    if ((st = check_rows(name, "v", a.v, a.v_n_stride, a.v_t_stride, a.n, a.S, (int64_t)a.HV * a.V, a.dtype)) != GDP_OK) return st;
     if ((!a.state && a.pool > 0) || !aligned16(a.state))
         return fail(GDP_ERR_INVALID, "%s: state is NULL or not 16-byte aligned", name);
     if (!a.o || !aligned16(a.o)) return fail(GDP_ERR_INVALID, "%s: o is NULL or not 16-byte aligned", name);
@@ -440,7 +457,7 @@ gdp_status check_norm(const char *name, const gdp_group_norm_args *a) {
     if (!(a->eps >= 0.f) || std::isinf(a->eps)) return fail(GDP_ERR_INVALID, "%s: eps must be finite and >= 0", name);
     if (a->D > 4096) return fail(GDP_ERR_UNSUPPORTED, "%s: D=%d over 4096", name, a->D);
     if (a->n > 0x7fffffff || a->T > 0x7fffffff || (a->T > 0 && a->n * a->T > 0x7fffffff) ||
-        (int64_t)a->groups * a->D > 0x7fffffff)
+        (int64_t)a->groups * a->D > (1 << 27))
         return fail(GDP_ERR_UNSUPPORTED, "%s: problem too large for one launch", name);
     return ok();
 }

@@ -11,7 +11,10 @@
 // element where a row is not made of aligned units), so a group is read once
 // and reduced inside a wave; neighbouring groups of a token sit in
 // neighbouring lanes.  Both directions move each tensor once and are bound by
-// that.
+// that: 32768 rows of 16 x 128 bf16 with a gate, forwards 82 us (403 MB, 4.9
+// TB/s, a large copy reaching 5.1), backwards 170 us (671 MB, 4.0 TB/s; 111
+// registers for three inputs, the next row's too and two sums leave four waves a
+// SIMD).  256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
 #include "gdp_common.h"
 #include "gdp_internal.h"
 #include "groupnorm.h"
@@ -324,7 +327,7 @@ hipError_t launch(GroupNorm &p, hipStream_t stream) {
     const int nt = p.bwd ? bwd_threads(E * NU) : GNT, sets = nt / LPG;
     p.join = p.bwd && nt > GNT && sets % p.groups == 0 ? sets / p.groups : 1;
     const int64_t blocks = (p.split * p.groups * LPG + nt - 1) / nt;
-    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    if (blocks * nt > 0xffffffffll) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks);
     if (!p.bwd) {

@@ -546,7 +546,8 @@ int64_t gdp_num_state_chunks(const int32_t *cu_seqlens_host, int64_t num_seqs,
  * Inputs must be finite (an infinity or a NaN may reach every row of its
  * 64-token chunk and the rows after it).
  * Sizes: K in {64, 128}, V in {64, 128, 256}, both dtypes; HV max(K, V) at
- * most 2^22.
+ * most 2^22.  A call that would launch 2^32 threads at once (512 or, if more,
+ * 4 V a head and sequence or segment) is GDP_ERR_UNSUPPORTED.
  */
 typedef struct gdp_linattn_args {
     int64_t B;
@@ -628,7 +629,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *a, const gdp_linattn_grads *d
  *          zero.  Slots of one call must be distinct.
  *   o      [n, S, HV, V] dtype, contiguous
  *   scale  <= 0 selects 1/sqrt(K).
- * Sizes as gdp_linattn_fwd, S <= 4096, n * V < 2^31.
+ * Sizes as gdp_linattn_fwd, S <= 4096, n * V * K < 2^34.
  */
 typedef struct gdp_linattn_decode_args {
     int64_t n;
@@ -673,7 +674,7 @@ gdp_status gdp_linattn_decode(const gdp_linattn_decode_args *a, void *stream);
  *   y      [n, T, C] dtype, contiguous.  May be x or z where that is
  *          contiguous too.
  * Statistics and sums are float32, the output is rounded once.
- * Sizes: D <= 4096, n*T < 2^31.
+ * Sizes: D <= 4096, C <= 2^27, n*T < 2^31.
  */
 typedef enum gdp_activation {
     GDP_ACT_NONE = 0,

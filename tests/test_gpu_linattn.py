@@ -368,6 +368,26 @@ def test_decode(n, S, H, HV, K, V, dtype, decay):
     assert torch.equal(st.cpu(), want)  # the other slots are left alone
 
 
+def test_one_token_of_any_stride():
+    """Time-major projections, one token: the stride over tokens passes every limit and does not matter."""
+    n, H, HV, K, V = 3, 2, 4, 64, 128
+    d = draws(27, [1], H, HV, K, V, BF16, "token", False, n)
+    far = torch.empty(1 << 24, dtype=BF16, device=DEV)
+
+    def major(x):
+        v = torch.as_strided(far, x.shape, (x[0, 0].numel() + 8, (1 << 23) + 3, x.shape[3], 1))
+        return v.copy_(gpu(x))
+
+    want = G.linattn_fwd(gpu(d["q"]), gpu(d["k"]), gpu(d["v"]), gpu(d["g"]), output_final_state=True)
+    state = torch.zeros(n, HV, V, K, device=DEV)
+    step = G.linattn_decode(gpu(d["q"]), gpu(d["k"]), gpu(d["v"]), state.clone(), gpu(d["g"]))
+    for name in ("q", "k", "v"):
+        ins = [major(d[x]) if x == name else gpu(d[x]) for x in ("q", "k", "v")]
+        got = G.linattn_fwd(*ins, gpu(d["g"]), output_final_state=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(G.linattn_decode(*ins, state.clone(), gpu(d["g"])), step)
+
+
 def test_decode_far_slots():
     """A pool of more than 2^31 state elements."""
     HV, K, V, pool = 4, 128, 128, 33000

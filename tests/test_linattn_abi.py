@@ -92,6 +92,35 @@ def test_linattn_rejects_outputs_and_workspaces():
         assert L.gdp_linattn_bwd(ctypes.byref(no_h0), ctypes.byref(d), 0x1000000, 1 << 40, None) == INV, kw
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1 << 20, T=1, H=64, HV=64), dict(cu_seqlens=0x1000, num_seqs=1 << 20, T=1 << 20, H=64, HV=64),
+    dict(B=1 << 19, T=600, H=4, HV=32, V=256)], ids=["rows of one token", "packed", "V=256"])
+def test_linattn_refuses_launches_over_2_32_threads(kw):
+    L = B.lib()
+    w, v = kw["H"] * 64, kw["HV"] * kw.get("V", 128)
+    a = lin(q_t_stride=w, k_t_stride=w, v_t_stride=v, **kw)
+    d = B.LinattnGrads(dout=0x90000, do_t_stride=v, dq=0xA0000, dk=0xB0000, dv=0xC0000)
+    assert L.gdp_linattn_fwd(ctypes.byref(a), 0x1000000, 1 << 60, None) == UNS
+    assert b"one launch" in L.gdp_last_error()
+    assert L.gdp_linattn_bwd(ctypes.byref(a), ctypes.byref(d), 0x1000000, 1 << 60, None) == UNS
+    assert L.gdp_linattn_workspace_bytes(ctypes.byref(a), 0) == -1
+
+
+def test_strides_of_single_elements_do_not_matter():
+    """One token or one row: its stride may be anything (the calls get as far as the missing output)."""
+    L = B.lib()
+    odd = dict(q_t_stride=3, k_t_stride=1 << 40, v_t_stride=0, q_b_stride=5, o=None)
+    for a in (lin(T=1, B=1, **odd), lin(T=128, B=1, q_b_stride=7, k_b_stride=1, o=None)):
+        assert L.gdp_linattn_fwd(ctypes.byref(a), None, 0, None) == INV
+        assert b"o is NULL" in L.gdp_last_error()
+    a = dec(S=1, q_t_stride=3, k_t_stride=1 << 40, v_t_stride=1, o=None)
+    assert L.gdp_linattn_decode(ctypes.byref(a), None) == INV
+    assert b"o is NULL" in L.gdp_last_error()
+    for kw in (dict(T=2, B=1, q_t_stride=132), dict(T=1, B=2, v_b_stride=12)):
+        assert L.gdp_linattn_fwd(ctypes.byref(lin(o=None, **kw)), None, 0, None) == INV
+        assert b"aligned" in L.gdp_last_error()
+
+
 def test_linattn_nothing_to_do():
     L = B.lib()
     assert L.gdp_linattn_fwd(ctypes.byref(lin(B=0)), None, 0, None) == B.GDP_OK
@@ -111,7 +140,7 @@ def dec(**kw):
 
 @pytest.mark.parametrize("name,kw,status", [
     ("K", dict(K=32), UNS), ("V", dict(V=96), UNS), ("HV", dict(HV=5), INV), ("dtype", dict(dtype=5), INV),
-    ("n<0", dict(n=-1), INV), ("S", dict(S=5000), UNS), ("n", dict(n=1 << 30), UNS), ("pool", dict(pool=-1), INV),
+    ("n<0", dict(n=-1), INV), ("S", dict(S=5000), UNS), ("n", dict(n=1 << 30), UNS), ("threads", dict(n=1 << 21), UNS), ("pool", dict(pool=-1), INV),
     ("pool without slots", dict(pool=2, slots=None), INV), ("two decays", dict(g_head=0x41000), INV),
     ("state NULL", dict(state=None), INV), ("state alignment", dict(state=0x50004), INV), ("o", dict(o=None), INV),
     ("q", dict(q=0x10002), INV), ("k stride", dict(k_n_stride=4), INV), ("v", dict(v=None), INV),
@@ -139,7 +168,7 @@ def norm(**kw):
 @pytest.mark.parametrize("name,kw,status", [
     ("dtype", dict(dtype=4), INV), ("activation", dict(activation=7), INV), ("groups", dict(groups=0), INV),
     ("D=0", dict(D=0), INV), ("D", dict(D=4097), UNS), ("eps", dict(eps=-1.0), INV), ("eps nan", dict(eps=float("nan")), INV),
-    ("n<0", dict(n=-1), INV), ("rows", dict(n=1 << 20, T=1 << 20), UNS), ("x NULL", dict(x=None), INV),
+    ("C", dict(groups=1 << 20, D=256), UNS), ("n<0", dict(n=-1), INV), ("rows", dict(n=1 << 20, T=1 << 20), UNS), ("x NULL", dict(x=None), INV),
     ("x alignment", dict(x=0x10001), INV), ("z stride", dict(z_t_stride=-1), INV), ("w", dict(w=0x30002), INV)])
 def test_group_norm_rejects(name, kw, status):
     L = B.lib()
@@ -165,6 +194,16 @@ def test_group_norm_rejects_outputs_and_workspaces():
         assert L.gdp_group_norm_bwd(ctypes.byref(norm()), ctypes.byref(d), ws, n, None) == INV
     assert L.gdp_group_norm_bwd(ctypes.byref(norm()), None, 0x1000000, need, None) == INV
     assert L.gdp_group_norm_fwd(ctypes.byref(norm(n=0)), None) == B.GDP_OK
+
+
+def test_leading_dimensions_fold():
+    x = torch.zeros(4, 5, 7, 16)
+    assert B._token_rows(x, "x") == (20, 7, 112, 16)
+    assert B._token_rows(x[:, :1], "x") == (4, 7, 560, 16)
+    assert B._token_rows(x[:1, :2, 1:3], "x") == (2, 2, 112, 16)
+    assert B._token_rows(x[0, 0], "x") == (1, 7, 0, 16)
+    with pytest.raises(ValueError):
+        B._token_rows(x[:, :2], "x")
 
 
 def test_binding_wants_gpu_tensors():
