@@ -12,9 +12,8 @@
 // and reduced inside a wave; neighbouring groups of a token sit in
 // neighbouring lanes.  Both directions move each tensor once and are bound by
 // that: 32768 rows of 16 x 128 bf16 with a gate, forwards 82 us (403 MB, 4.9
-// TB/s, a large copy reaching 5.1), backwards 170 us (671 MB, 4.0 TB/s; 111
-// registers for three inputs, the next row's too and two sums leave four waves a
-// SIMD).  256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
+// TB/s, a large copy reaching 5.1), backwards 154 us (671 MB, 4.4 TB/s;
+// three inputs, the next row's too, and two sums a channel take 111 registers).  256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
 #include "gdp_common.h"
 #include "gdp_internal.h"
 #include "groupnorm.h"
@@ -368,14 +367,18 @@ hipError_t launch_shape(GroupNorm &p, const Shape &s, hipStream_t stream) {
 
 // Row sets that run side by side: threads of one set walk rows r0, r0 + split, ...
 int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
-    // about 16 rows a thread forwards and 8 backwards once the card is full
-    // (32768 x 2048: 4 / 8 / 16 / 32 rows forwards 107 / 95 / 90 / 91 us);
-    // backwards at least 4, and each split costs 8 bytes a channel of partial sums
-    const int64_t per_row = (int64_t)groups * D / 8 > 0 ? (int64_t)groups * D / 8 : 1;
-    const int64_t fill = (bwd ? 131072 : 262144) / per_row + 1;
+    // about 16 rows a thread forwards once the card is full (32768 x 2048: 4 / 8
+    // / 16 / 32 rows 107 / 95 / 90 / 91 us).  Backwards no more threads than two
+    // waves a SIMD (each set of rows costs 8 bytes a channel of partial sums;
+    // one, two or three times as many 154, 163, 166 us, and 173 with one block
+    // too many, that runs alone at the end) and at least 4 rows.
+    const int64_t fill = (bwd ? 131072 : 262144) * 8 / ((int64_t)groups * D);
     const int64_t few = (rows + (bwd ? 3 : 15)) / (bwd ? 4 : 16);
-    const int64_t s = bwd ? (few < fill ? few : fill) : (few > fill ? few : fill);
-    return s < rows ? s : rows;
+    int64_t s = bwd ? (few < fill ? few : fill) : (few > fill ? few : fill);
+    s = s < 1 ? 1 : s;
+    if (s >= rows) return rows;
+    const int64_t each = (rows + s - 1) / s;  // as many rows for every thread
+    return (rows + each - 1) / each;
 }
 
 hipError_t launch_group_norm(GroupNorm p, gdp_dtype dtype, hipStream_t stream) {
