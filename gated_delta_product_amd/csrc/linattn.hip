@@ -445,6 +445,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     auto chunk = [&](int ch, Set &cur) __attribute__((always_inline)) {
         const int c0 = cfirst + ch * cstep;  // the chunk's first row
         const int n = rows_of(c0), buf = ch % W::GD;
+        const bool few = !W::F32 && n <= 32;
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
         asm volatile("" : "+v"(lane));
@@ -460,11 +461,17 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
         f32x4 y[W::NB];
         if constexpr (OUT) {
-            // score tiles at and below the diagonal: P^T (rows j, columns i)
+            // score tiles at and below the diagonal: P^T (rows j, columns i).
+            // A chunk of at most 32 rows keeps what its scores' rounding left
+            // in the tiles 32 rows further down (tile 4, the one of those
+            // above the diagonal, comes out as zeros): with few scores their
+            // rounding does not average out (a request of 1 to 5 tokens was
+            // up to 2.7e-3 off, 1.7e-3 with two parts).
 #pragma unroll
             for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
                 const int t = W::WV * k + wave;
                 if (t >= W::NP) break;
+                if (few && t >= 3 && t != 4) break;
                 const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
                 f32x4 acc[2] = {zero4(), zero4()}, e = zero4();
 #pragma unroll
@@ -480,16 +487,18 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 const float sbsy = w.sb * w.sy;
                 const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
                 const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
-                typename Frag<T>::half pv;
+                typename Frag<T>::half pv, pl;
                 float q = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r])) * sbsy;
                     const float sc = j0 + r <= i ? (acc[0][r] + acc[1][r]) * d : 0.f;
                     pv[r] = from_f32<T>(sc);
+                    pl[r] = from_f32<T>(sc - to_f32(pv[r]));
                     if constexpr (DOT) q += j0 + r < i ? sc * e[r] : 0.f;
                 }
                 *(typename Frag<T>::half *)(sm.p + TP::at(i, j0)) = pv;
+                if (few && t < 3) *(typename Frag<T>::half *)(sm.p + TP::at(i + 32, j0)) = pl;
                 if constexpr (DOT) {
                     q = xor32_sum(xor16_sum(q));
                     if (g4 == 0) sm.rho_p[16 * t + m] = q;
@@ -555,6 +564,10 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
                 for (int ib = 2 * tb; ib < W::NB; ++ib)
                     y[ib] = mma(fc, TP::row8(sm.p, prow, ib, tb), y[ib]);
+                if (few && tb == 0)
+#pragma unroll
+                    for (int ib = 0; ib < W::NB / 2; ++ib)
+                        y[ib] = mma(fc, TP::row8(sm.p, prow, ib + 2, 0), y[ib]);
             }
             // KG tiles at a time, so that a tile's parts are not back to back
 #pragma unroll

@@ -266,6 +266,62 @@ def test_rows_outside_the_requests_are_left():
         assert not x[:, :7].any() and not x[:, 110:].any()
 
 
+@pytest.mark.parametrize("lens", [[130, 90, 77], [700, 1100, 650], [1, 64, 1]], ids=["one pass", "segments", "rows"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_nan_stays_in_its_request(lens, dtype):
+    """NaN in one request (or batch row) and outside every request: the others keep their bits."""
+    a, b = 5 + lens[0], 5 + lens[0] + lens[1]
+    d = draws(28, [5] + lens + [9], 1, 2, 64, 128, dtype, "token", False)
+    cu = torch.tensor([5, a, b, b + lens[2]], dtype=torch.int32, device=DEV)
+    clean = [gpu(d[x]) for x in ("do", "q", "k", "v", "g")]
+    bad = [x.clone() for x in clean]
+    for x in bad:
+        x[:, :5] = x[:, a:b] = x[:, b + lens[2]:] = float("nan")
+    state = torch.randn(3, 2, 128, 64, device=DEV)
+
+    def run(ins, cu):
+        o, ht = G.linattn_fwd(*ins[1:], cu_seqlens=cu, initial_state=state, output_final_state=True)
+        return [o, ht] + list(G.linattn_bwd(*ins, cu_seqlens=cu, initial_state=state, dht=state))
+
+    for i, (x, y) in enumerate(zip(run(bad, cu), run(clean, cu))):
+        if i in (1, 6):  # by request
+            assert torch.equal(x[0], y[0]) and torch.equal(x[2], y[2])
+        else:
+            for t in (slice(5, a), slice(b, b + lens[2])):
+                assert torch.equal(x[:, t], y[:, t])
+    rows = [torch.cat([x[:, :lens[1]]] * 3) for x in clean]
+    nan = [x.clone() for x in rows]
+    for x in nan:
+        x[1] = float("nan")
+    for x, y in zip(run(nan, None), run(rows, None)):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[2], y[2])
+
+
+def test_gradients_past_32_bits():
+    """Over 2^31 elements of v: the last of two requests against its plain form."""
+    T, L, H, HV, K, V = 264000, 150, 32, 64, 128, 128
+    d = draws(29, [L], H, HV, K, V, BF16, "token", True)
+    ins = []
+    for name in ("do", "q", "k", "v", "g"):
+        x = torch.zeros(1, T, *d[name].shape[2:], dtype=d[name].dtype, device=DEV)
+        x[:, T - L:] = gpu(d[name])
+        ins.append(x)
+    cu = torch.tensor([0, T - L, T], dtype=torch.int32, device=DEV)
+    h0, dht = (torch.cat([torch.zeros(1, HV, V, K), d[x]]).to(DEV) for x in ("h0", "dht"))
+    o, ht = G.linattn_fwd(*ins[1:], cu_seqlens=cu, initial_state=h0, output_final_state=True)
+    grads = G.linattn_bwd(*ins, cu_seqlens=cu, initial_state=h0, dht=dht)
+    (at, r), = sequences(d)
+    (ro, rht), (ao, aht) = r.forward(), r.forward_abs()
+    within("o", o[0, T - L:], ro, ao, L + K, BF16)
+    within("ht", ht[1], rht, aht, L + K, F32)
+    ref, A = r.backward(d["do"][at], d["dht"][0]), r.backward_abs(d["do"][at], d["dht"][0])
+    for name, x, y, a in zip(("dq", "dk", "dv"), grads, ref, A):
+        within(name, x[0, T - L:], y, a, L + K + V, BF16)
+        assert not x[0, :T - L].any()
+    within("dh0", grads[4][1], ref[4], A[4], L + K + V, F32)
+    within("dg", grads[3][0, T - L:], ref[3], A[3].max(0).values.expand_as(A[3]) * 2, 8 * (L + K + V), F32)
+
+
 def test_unordered_offsets_stay_in_bounds():
     """Offsets that overlap or run backwards give some result and touch nothing outside."""
     d = draws(14, [4096], 1, 2, 64, 64, BF16, "token", False, 1)
