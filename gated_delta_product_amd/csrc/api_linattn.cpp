@@ -96,7 +96,7 @@ int64_t lay_fwd(const gdp_linattn_args &a, const Plan &p, void *ws, FwdSpace *s)
 }
 
 struct BwdSpace {
-    float *s, *s_tot, *r, *r_tot, *rho_q, *rho_k, *dq, *dk, *dh0;
+    float *s, *s_tot, *r, *r_tot, *rho_q, *rho_k, *rho_in, *dq, *dk, *dh0;
     double *part;
     int nq, nk;
 };
@@ -110,6 +110,7 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
     s->nq = s->nk = a.K / gdp::lin_grads_slice(a.K, a.V);
     s->rho_q = m.take<float>(s->nq * BTH);
     s->rho_k = m.take<float>(s->nk * BTH);
+    s->rho_in = m.take<float>(s->nq * BTH);
     s->part = m.take<double>(p.items * a.HV);
     const bool shared = a.HV != a.H;
     s->dq = m.take<float>(shared ? BTH * a.K : 0);
@@ -361,6 +362,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     f.y = shared ? (void *)ws.dq : d->dq;
     f.y32 = shared;
     f.rho = ws.rho_q;
+    f.rho_in_chunk = d->dg_head ? ws.rho_in : nullptr;
     gdp::LinWalk w = f;
     w.a = v;
     w.b = o;
@@ -406,6 +408,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     g.g_ts = base.g_ts;
     g.rho_q = ws.rho_q;
     g.rho_k = ws.rho_k;
+    g.rho_in_chunk = d->dg_head ? ws.rho_in : nullptr;
     g.s_in = ws.s;
     g.r_in = ws.r;
     g.h0 = a.h0;

@@ -35,6 +35,8 @@ struct LinWalk {
     float *s_out;      // [nseq, HV, dc, da] or NULL: state after the walk
     float *seg_out;    // segment pass: [slots, HV, dc, da] and [slots, HV]
     float *seg_tot;
+    float *rho_in_chunk;  // as rho, or NULL: then rho holds every pair, else those of two chunks (the walk
+                          // forwards writes the others here, weighed by their distance)
 };
 
 // The walks of a launch: one forwards, with a second one of its shape backwards
@@ -63,6 +65,7 @@ struct LinDg {
     const float *g;
     int64_t g_bs, g_ts;
     const float *rho_q, *rho_k;
+    const float *rho_in_chunk;        // or NULL
     const float *s_in, *r_in;         // states entering each segment, forwards and backwards
     const float *h0, *dh0;            // [nseq, HV, V, K] (both, or neither is used)
     bool end_zero;                    // no gradient enters behind the last row
