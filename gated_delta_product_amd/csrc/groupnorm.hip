@@ -12,7 +12,7 @@
 // and reduced inside a wave; neighbouring groups of a token sit in
 // neighbouring lanes.  Both directions move each tensor once and are bound by
 // that: 32768 rows of 16 x 128 bf16 with a gate, forwards 82 us (403 MB, 4.9
-// TB/s, a large copy reaching 5.1), backwards 154 us (671 MB, 4.4 TB/s;
+// TB/s, a large copy reaching 5.1), backwards 140 us (671 MB, 4.8 TB/s;
 // three inputs, the next row's too, and two sums a channel take 111 registers).  256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
 #include "gdp_common.h"
 #include "gdp_internal.h"
