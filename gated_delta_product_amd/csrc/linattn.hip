@@ -118,6 +118,63 @@ struct Tile {
     }
 };
 
+// The scores P of a chunk as operands: 16 x 32 tiles (rows i, 32 rows j) at
+// and below the diagonal, each value in NP bf16 parts (all first parts, then
+// all second ones); in float32, rows as above.  The tiles (0, 0) and (2, 1)
+// hold 16 columns, the lanes of the other 16 read the zeros behind them: two
+// parts then take 10 KB, and two blocks of the widest walk fit a compute unit.
+template <typename T, int CT>
+struct Scores {
+    typedef Tile<T, CT> TP;
+    typedef typename Frag<T>::type frag;
+    typedef typename Frag<T>::half half;
+    static constexpr int PARTS = 1, SIZE = CT * CT;
+    struct Lane {
+        int full;
+    };
+    static __device__ __forceinline__ Lane lane_of(int m, int g4) { return Lane{TP::at(m, 8 * g4)}; }
+    static __device__ __forceinline__ void clear(T *p, int tid, int nt) {
+        for (int i = tid; i < SIZE; i += nt) p[i] = 0.f;
+    }
+    // columns 16 jb + 4 g4 .. + 3 of row 16 ib + m
+    static __device__ __forceinline__ void put(T *p, int ib, int jb, int m, int g4, f32x4 x) {
+        *(half *)(p + TP::at(16 * ib + m, 16 * jb + 4 * g4)) = x;
+    }
+    static __device__ __forceinline__ frag get(const T *p, Lane l, int ib, int tb, int) { return TP::row8(p, l.full, ib, tb); }
+};
+template <>
+struct Scores<bf16, 64> {
+    static constexpr int PARTS = 2, HALF = 16 * 16 + 8, FULL = 16 * 32, PART = 2 * HALF + 4 * FULL, SIZE = PARTS * PART;
+    struct Lane {
+        int full, half;
+    };
+    // (0, 0), (2, 1); (1, 0), (2, 0), (3, 0), (3, 1)
+    static constexpr __device__ __forceinline__ bool is_half(int ib, int tb) { return ib == 2 * tb; }
+    static constexpr __device__ __forceinline__ int at(int ib, int tb) {
+        return is_half(ib, tb) ? HALF * tb : 2 * HALF + FULL * (ib - 1 + tb);
+    }
+    static __device__ __forceinline__ Lane lane_of(int m, int g4) {
+        return Lane{32 * m + 8 * g4, g4 < 2 ? 16 * m + 8 * g4 : 16 * 16};
+    }
+    static __device__ __forceinline__ void clear(bf16 *p, int tid, int) {
+        if (tid < 4 * 8) p[(tid >> 4) * PART + (tid >> 3 & 1) * HALF + 16 * 16 + (tid & 7)] = (bf16)0.f;
+    }
+    static __device__ __forceinline__ void put(bf16 *p, int ib, int jb, int m, int g4, f32x4 x) {
+        const int tb = jb >> 1, at0 = at(ib, tb) + (is_half(ib, tb) ? 16 * m : 32 * m + 16 * (jb & 1)) + 4 * g4;
+        bf16x4 hi, lo;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            hi[r] = (bf16)x[r];
+            lo[r] = (bf16)(x[r] - (float)hi[r]);
+        }
+        *(bf16x4 *)(p + at0) = hi;
+        *(bf16x4 *)(p + at0 + PART) = lo;
+    }
+    static __device__ __forceinline__ bf16x8 get(const bf16 *p, Lane l, int ib, int tb, int part) {
+        return *(const bf16x8 *)(p + part * PART + at(ib, tb) + (is_half(ib, tb) ? l.half : l.full));
+    }
+};
+
 // Values x[0..7] as NS parts of the storage type whose sum carries 8 NS
 // bits (bf16); for float storage one part is the value.
 template <typename T, int NS>
@@ -227,8 +284,9 @@ __device__ __forceinline__ LinItem lin_item(const int32_t *cu, int64_t nseq, int
 // DOT: also rho_i = x_i . (y_i without its own row's term), from unrounded
 //      values: the part of the row that the decays scale.
 // NS:  bf16 parts of the decayed c in the state update (16 or 24 bits).
-// NQ:  parts of the state in S a.
+// NQ:  parts of the state in S a (1 in float32, 2 for bf16 rows, 3 for dg).
 template <typename T> constexpr bool F32_Y = sizeof(T) == 4;
+template <typename T> constexpr int ROW_PARTS = sizeof(T) == 4 ? 1 : 2;
 
 template <typename T, int DA, int DC, int NS, int NQ, bool OUT, bool DOT>
 struct Walk {
@@ -239,7 +297,9 @@ struct Walk {
     static constexpr int TB = CT / 32;           // 32-row blocks
     static constexpr int KT = DA / 16;           // 16-row tiles of S^T
     static constexpr int WV = DC / 16;           // waves
-    static constexpr int GD = 4;                 // chunks whose decays are formed together, by a wave each
+    // chunks whose decays are formed together, by a wave each (fewer where
+    // their tables would cost a compute unit a block)
+    static constexpr int GD = F32 ? 4 : DOT ? 3 : DA == 128 && WV == 4 ? 2 : 4;
     static constexpr int NT = 64 * WV;
     // waves a SIMD: two blocks to a compute unit where their LDS fits (and
     // with 256 rows of S^T a wave needs the registers of two)
@@ -250,7 +310,7 @@ struct Walk {
     static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
-    typedef Tile<T, CT> TP;
+    typedef Scores<T, CT> TP;
     typedef typename Frag<T>::type frag;
 
     struct Lds {
@@ -258,7 +318,7 @@ struct Walk {
         T c[CT * DC];
         T a[OUT ? CT * DA : 8];
         T x[DOT ? CT * DC : 8];
-        T p[OUT ? CT * CT : 8];
+        T p[OUT ? TP::SIZE : 8];
         // decays of GD chunks: G as two floats, 2^G_i, sb 2^(G_end - G_i), G_end
         float gh[OUT ? GD : 1][CT], gl[OUT ? GD : 1][CT], eg[OUT ? GD : 1][CT], wg[GD][CT];
         double gend[GD];
@@ -436,16 +496,13 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             for (int kt = 0; kt < W::KT; ++kt) s[kt] = *(const f32x4 *)(q + 32 * (kt / 2) + 4 * (kt % 2));
         }
     }
-    // tiles above the diagonal of P stay zero (a 32-row contraction of an even block reads one)
-    if constexpr (OUT) {
-        for (int i = threadIdx.x; i < CT * CT; i += NT) sm.p[i] = from_f32<T>(0.f);
-    }
+    // what is read of P above the diagonal stays zero (a 32-row contraction of an even block reads 16 rows)
+    if constexpr (OUT) TP::clear(sm.p, threadIdx.x, NT);
 
     // The barriers order LDS only: the next chunk's rows stay in flight over
     // them, and so do the stores of y.
     auto chunk = [&](int ch, Set &cur) __attribute__((always_inline)) {
         const int lo = low(ch), n = count(lo), buf = ch % W::GD;
-        const bool few = !W::F32 && n <= 32;
         // rho of a decay per head: pairs inside a chunk weighed by their distance, see gdp_lin_dg_k
         const bool apart = DOT && w.rho_in_chunk;
         // LDS addresses are formed anew in each chunk: held over it they would
@@ -463,17 +520,11 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 
         f32x4 y[W::NB];
         if constexpr (OUT) {
-            // score tiles at and below the diagonal: P^T (rows j, columns i).
-            // A chunk of at most 32 rows keeps what its scores' rounding left
-            // in the tiles 32 rows further down (tile 4, the one of those
-            // above the diagonal, comes out as zeros): with few scores their
-            // rounding does not average out (a request of 1 to 5 tokens was
-            // up to 2.7e-3 off, 1.7e-3 with two parts).
+            // score tiles at and below the diagonal: P^T (rows j, columns i)
 #pragma unroll
             for (int k = 0; k < (W::NP + W::WV - 1) / W::WV; ++k) {
                 const int t = W::WV * k + wave;
                 if (t >= W::NP) break;
-                if (few && t >= 3 && t != 4) break;
                 const int ib = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jb = t - ib * (ib + 1) / 2;
                 f32x4 acc[2] = {zero4(), zero4()}, e = zero4();
 #pragma unroll
@@ -489,18 +540,16 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                 const float sbsy = w.sb * w.sy;
                 const float ghi = sm.gh[buf][i], gli = sm.gl[buf][i];
                 const f32x4 ghj = *(const f32x4 *)&sm.gh[buf][j0], glj = *(const f32x4 *)&sm.gl[buf][j0];
-                typename Frag<T>::half pv, pl;
+                f32x4 pv;
                 float q = 0.f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = __builtin_amdgcn_exp2f((ghi - ghj[r]) + (gli - glj[r])) * sbsy;
                     const float sc = j0 + r <= i ? (acc[0][r] + acc[1][r]) * d : 0.f;
-                    pv[r] = from_f32<T>(sc);
-                    pl[r] = from_f32<T>(sc - to_f32(pv[r]));
+                    pv[r] = sc;
                     if constexpr (DOT) q += j0 + r < i ? sc * e[r] * (apart ? (float)(i - j0 - r) : 1.f) : 0.f;
                 }
-                *(typename Frag<T>::half *)(sm.p + TP::at(i, j0)) = pv;
-                if (few && t < 3) *(typename Frag<T>::half *)(sm.p + TP::at(i + 32, j0)) = pl;
+                TP::put(sm.p, ib, jb, m, g4, pv);
                 if constexpr (DOT) {
                     q = xor32_sum(xor16_sum(q));
                     if (g4 == 0) sm.rho_p[16 * t + m] = q;
@@ -546,7 +595,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
         // the rows c as operands, once for P c and (decayed) for the state
         const auto ccol = TC::template cols<4>(lane, cw);
         const auto bcol = TA::template cols<8>(lane, 0);
-        const int prow = TP::row_base(lane);
+        const auto prow = TP::lane_of(m, g4);
         if constexpr (OUT) {
             const float dec = sm.eg[buf][CT - 1];
 #pragma unroll
@@ -564,12 +613,9 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
             split8<T, NS>(v, fw);
             if constexpr (OUT) {
 #pragma unroll
-                for (int ib = 2 * tb; ib < W::NB; ++ib)
-                    y[ib] = mma(fc, TP::row8(sm.p, prow, ib, tb), y[ib]);
-                if (few && tb == 0)
+                for (int part = TP::PARTS - 1; part >= 0; --part)
 #pragma unroll
-                    for (int ib = 0; ib < W::NB / 2; ++ib)
-                        y[ib] = mma(fc, TP::row8(sm.p, prow, ib + 2, 0), y[ib]);
+                    for (int ib = 2 * tb; ib < W::NB; ++ib) y[ib] = mma(fc, TP::get(sm.p, prow, ib, tb, part), y[ib]);
             }
             // KG tiles at a time, so that a tile's parts are not back to back
 #pragma unroll
@@ -655,12 +701,13 @@ __device__ __forceinline__ void lin_block(const LinWalk &w, void *lds) {
 }
 
 template <typename T, int DA, int DC, int NS, bool OUT>
-__global__ void __launch_bounds__((Walk<T, DA, DC, NS, 1, OUT, false>::NT), (Walk<T, DA, DC, NS, 1, OUT, false>::OCC))
+__global__ void __launch_bounds__((Walk<T, DA, DC, NS, ROW_PARTS<T>, OUT, false>::NT),
+                                  (Walk<T, DA, DC, NS, ROW_PARTS<T>, OUT, false>::OCC))
 gdp_lin_walk_k(LinWalks p) {
-    typedef Walk<T, DA, DC, NS, 1, OUT, false> W;
-    __shared__ __align__(16) char lds[sizeof(typename W::Lds)];
-    if (blockIdx.y == 0) lin_block<T, DA, DC, NS, 1, OUT, false, false>(p.w[0], lds);
-    else if constexpr (!OUT) lin_block<T, DA, DC, NS, 1, OUT, false, true>(p.w[1], lds);
+    constexpr int NQ = ROW_PARTS<T>;
+    __shared__ __align__(16) char lds[sizeof(typename Walk<T, DA, DC, NS, NQ, OUT, false>::Lds)];
+    if (blockIdx.y == 0) lin_block<T, DA, DC, NS, NQ, OUT, false, false>(p.w[0], lds);
+    else if constexpr (!OUT) lin_block<T, DA, DC, NS, NQ, OUT, false, true>(p.w[1], lds);
 }
 
 // The three walks of the gradients in one launch: dq and dk (DA = V, slices of
@@ -669,7 +716,7 @@ gdp_lin_walk_k(LinWalks p) {
 template <typename T, int K, int V, int SL, int NS, int NQ, int ND, bool DOT>
 struct Grads {
     typedef Walk<T, V, SL, NS, NQ, true, DOT> QK;
-    typedef Walk<T, K, SL, ND, 1, true, false> D;
+    typedef Walk<T, K, SL, ND, ROW_PARTS<T>, true, false> D;
     static constexpr int OCC = QK::OCC < D::OCC ? QK::OCC : D::OCC;
     static constexpr int BYTES = sizeof(typename QK::Lds) > sizeof(typename D::Lds) ? sizeof(typename QK::Lds)
                                                                                    : sizeof(typename D::Lds);
@@ -679,7 +726,7 @@ __global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, ND, DOT>::
     __shared__ __align__(16) char lds[Grads<T, K, V, SL, NS, NQ, ND, DOT>::BYTES];
     if (blockIdx.y == 0) lin_block<T, V, SL, NS, NQ, true, DOT, false>(p.w[0], lds);
     else if (blockIdx.y == 1) lin_block<T, V, SL, NS, NQ, true, DOT, true>(p.w[1], lds);
-    else lin_block<T, K, SL, ND, 1, true, false, true>(p.w[2], lds);
+    else lin_block<T, K, SL, ND, ROW_PARTS<T>, true, false, true>(p.w[2], lds);
 }
 
 // ---------------------------------------------------------------- the scan over segments
@@ -975,17 +1022,19 @@ static hipError_t launch_grads_dims(const LinWalks &w, hipStream_t stream) {
 }
 // Parts of bf16 in the state's products.  What leaves in float32 (ht, dh0, and
 // dg through rho) takes three, 24 bits: with two, dg was 1e-5 off and ht 2e-6
-// (relative to 64 bits; with three 1e-6 and 2e-7, as float32 sums are).  States
-// that only reach bf16 rows take two, and one as the operand of S a: that
-// rounding, the scores' and the result's are of one size (2.3e-3 for 1.7e-3
-// of the result's alone).
+// (relative to 64 bits; with three 1e-6 and 2e-7, as float32 sums are).  What
+// only reaches bf16 rows takes two, 16 bits: the scores, the decayed rows and
+// the state as the operand of S a.  A row is then off by its own rounding,
+// 1.65e-3; with scores and operand in one part it was 2.3e-3, and elements
+// whose terms cancel were off by many times their rounding.  The second parts
+// cost 3 to 9% of a call (packed prompts 119 to 129 us, 32768 tokens 210 to 229).
 hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream) {
     if (w.w[0].items == 0) return hipSuccess;
     if (dtype == GDP_F32)
         return dot ? launch_grads_dims<float, 1, 1, 1, true>(w, stream) : launch_grads_dims<float, 1, 1, 1, false>(w, stream);
     if (w.w[2].s_out)
-        return dot ? launch_grads_dims<bf16, 3, 3, 3, true>(w, stream) : launch_grads_dims<bf16, 2, 1, 3, false>(w, stream);
-    return dot ? launch_grads_dims<bf16, 3, 3, 2, true>(w, stream) : launch_grads_dims<bf16, 2, 1, 2, false>(w, stream);
+        return dot ? launch_grads_dims<bf16, 3, 3, 3, true>(w, stream) : launch_grads_dims<bf16, 2, 2, 3, false>(w, stream);
+    return dot ? launch_grads_dims<bf16, 3, 3, 2, true>(w, stream) : launch_grads_dims<bf16, 2, 2, 2, false>(w, stream);
 }
 
 hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
