@@ -96,9 +96,9 @@ int64_t lay_fwd(const gdp_linattn_args &a, const Plan &p, void *ws, FwdSpace *s)
 }
 
 struct BwdSpace {
-    float *s, *s_tot, *r, *r_tot, *rho_q, *rho_k, *rho_in, *dq, *dk, *dh0;
+    float *s, *s_tot, *r, *r_tot, *rho_q, *rho_k, *rho_in, *s_mid, *r_mid, *dq, *dk, *dh0;
     double *part;
-    int nq, nk;
+    int nq, nk, spans;
 };
 int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s) {
     Arena m{(char *)ws};
@@ -110,8 +110,13 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
     s->nq = s->nk = a.K / gdp::lin_grads_slice(a.K, a.V);
     s->rho_q = m.take<float>(s->nq * BTH);
     s->rho_k = m.take<float>(s->nk * BTH);
-    s->rho_in = m.take<float>(s->nq * BTH);
-    s->part = m.take<double>(p.items * a.HV);
+    // a decay per head (or none yet): the pairs of a chunk apart, and the states at the borders of spans
+    s->spans = (int)cdiv(p.seg_tok, gdp::LIN_SPAN);
+    const int64_t mids = a.g || s->spans == 1 ? 0 : a.B * a.T / gdp::LIN_SPAN + 1;
+    s->rho_in = m.take<float>(a.g ? 0 : s->nq * BTH);
+    s->s_mid = m.take<float>(mids * a.HV * E);
+    s->r_mid = m.take<float>(mids * a.HV * E);
+    s->part = m.take<double>(a.g ? 0 : p.items * s->spans * a.HV);
     const bool shared = a.HV != a.H;
     s->dq = m.take<float>(shared ? BTH * a.K : 0);
     s->dk = m.take<float>(shared ? BTH * a.K : 0);
@@ -314,6 +319,8 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     g.elems = (int64_t)a.K * a.V;
     g.items = p.items;  // 0 without sequences: dg_head is zero then
     g.HV = a.HV;
+    g.spans = ws.spans;
+    g.chunk = a.dtype == GDP_F32 ? 32 : 64;
 
     const int r = a.HV / a.H;
     const int64_t wk = (int64_t)a.H * a.K, wv = (int64_t)a.HV * a.V;
@@ -363,6 +370,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     f.y32 = shared;
     f.rho = ws.rho_q;
     f.rho_in_chunk = d->dg_head ? ws.rho_in : nullptr;
+    f.mid = d->dg_head && ws.spans > 1 ? ws.s_mid : nullptr;
     gdp::LinWalk w = f;
     w.a = v;
     w.b = o;
@@ -374,6 +382,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     w.sy = 1.0f;
     w.y = shared ? (void *)ws.dk : d->dk;
     w.rho = ws.rho_k;
+    w.mid = f.mid ? ws.r_mid : nullptr;
     // dv: (k, q, do) backwards
     gdp::LinWalk x = w;
     x.a = k;
@@ -385,7 +394,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     x.trans = false;
     x.y = d->dv;
     x.y32 = false;
-    x.rho = nullptr;
+    x.rho = x.mid = nullptr;
     // <h0, dh0> anchors dg where one segment has a state before it and a gradient behind it
     x.s_out = d->dh0 ? d->dh0 : want_g && d->dht && a.h0 ? ws.dh0 : nullptr;
     if ((st = hip_status(gdp::launch_lin_grads({{f, w, x}, 3}, a.dtype, want_g, s), name)) != GDP_OK) return st;
@@ -408,14 +417,16 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
     g.g_ts = base.g_ts;
     g.rho_q = ws.rho_q;
     g.rho_k = ws.rho_k;
-    g.rho_in_chunk = d->dg_head ? ws.rho_in : nullptr;
+    g.rho_in_chunk = ws.rho_in;
     g.s_in = ws.s;
     g.r_in = ws.r;
+    g.s_mid = ws.s_mid;
+    g.r_mid = ws.r_mid;
     g.h0 = a.h0;
-    g.dh0 = d->dh0 ? d->dh0 : ws.dh0;
+    g.dh0 = x.s_out;
     g.end_zero = !d->dht;
     g.dg = d->dg;
-    g.part = d->dg_head ? ws.part : nullptr;
+    g.part = ws.part;
     return hip_status(gdp::launch_lin_dg(g, d->dg_head, s), name);
 }
 

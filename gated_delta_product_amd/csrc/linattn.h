@@ -15,6 +15,11 @@ struct LinRows {
     int div = 1;
 };
 
+// Rows of a span: a segment's states are kept at every border between two of
+// its spans (the one before its t-th token in slot t / LIN_SPAN, which no two
+// borders share: they lie a span apart).
+constexpr int LIN_SPAN = 512;
+
 // One walk (linattn.hip): y_i = sum D(i,j) (a_i.b_j) c_j over every sequence,
 // cut into segments of seg_tok rows.
 struct LinWalk {
@@ -37,6 +42,7 @@ struct LinWalk {
     float *seg_tot;
     float *rho_in_chunk;  // as rho, or NULL: then rho holds every pair, else those of two chunks (the walk
                           // forwards writes the others here, weighed by their distance)
+    float *mid;        // [B T / LIN_SPAN + 1, HV, dc, da] or NULL: states at the borders of spans
 };
 
 // The walks of a launch: one forwards, with a second one of its shape backwards
@@ -62,15 +68,17 @@ struct LinDg {
     const int32_t *cu;
     int64_t B, T, nseq, seg_tok, elems, items;
     int HV, nq, nk;    // slices of rho_q and rho_k
+    int spans, chunk;  // of a segment, and rows of a chunk (a decay per head)
     const float *g;
     int64_t g_bs, g_ts;
     const float *rho_q, *rho_k;
-    const float *rho_in_chunk;        // or NULL
+    const float *rho_in_chunk;        // a decay per head
     const float *s_in, *r_in;         // states entering each segment, forwards and backwards
-    const float *h0, *dh0;            // [nseq, HV, V, K] (both, or neither is used)
+    const float *s_mid, *r_mid;       // and its spans after the first (a decay per head)
+    const float *h0, *dh0;            // [nseq, HV, V, K] or NULL
     bool end_zero;                    // no gradient enters behind the last row
-    float *dg;         // [B, T, HV] or NULL
-    double *part;      // [items, HV] or NULL: sums over each segment
+    float *dg;         // [B, T, HV], or NULL for a decay per head
+    double *part;      // [items, spans, HV]: sums over each span (a decay per head)
 };
 
 // y[i] [B*T, H, D] = sums over r neighbouring heads of x[i] [B*T, H*r, D]

@@ -306,7 +306,7 @@ struct Walk {
     static constexpr int OCC = DA == 256 ? (WV == 8 ? 2 : 1) : WV / 2;
     // tiles whose operands are loaded together: fewer where registers are
     // short (a spill's reload would wait for every row in flight)
-    static constexpr int KG = DOT && OCC >= 4 ? 2 : 4, IG = DOT && OCC >= 4 ? 2 : NB;
+    static constexpr int KG = !OUT || (DOT && OCC >= 4) ? 2 : 4, IG = DOT && OCC >= 4 ? 2 : NB;
     static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
@@ -555,9 +555,12 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                     if (g4 == 0) sm.rho_p[16 * t + m] = q;
                 }
             }
-            // S a: S^T tiles as the operand, rounded to NQ parts
+            // S a: S^T tiles as the operand, rounded to NQ parts.  For dg the
+            // smaller parts have a sum of their own: a row of rho is then off by
+            // the roundings of the first parts only (2.0e-7 -> 1.4e-7).
+            f32x4 yl[W::NB];
 #pragma unroll
-            for (int ib = 0; ib < W::NB; ++ib) y[ib] = zero4();
+            for (int ib = 0; ib < W::NB; ++ib) y[ib] = yl[ib] = zero4();
 #pragma unroll
             for (int kb = 0; kb < DA / 32; ++kb) {
                 float v[8];
@@ -573,11 +576,14 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
                     for (int p = NQ - 1; p >= 0; --p)
 #pragma unroll
-                        for (int i = 0; i < W::IG; ++i) y[i0 + i] = mma(sp[p], fa[i], y[i0 + i]);
+                        for (int i = 0; i < W::IG; ++i)
+                            if (DOT && p) yl[i0 + i] = mma(sp[p], fa[i], yl[i0 + i]);
+                            else y[i0 + i] = mma(sp[p], fa[i], y[i0 + i]);
                 }
             }
 #pragma unroll
             for (int ib = 0; ib < W::NB; ++ib) {
+                if constexpr (DOT) y[ib] += yl[ib];
                 y[ib] *= sm.eg[buf][16 * ib + m] * w.sy;
                 if constexpr (DOT) {
                     const auto xv = *(const typename Frag<T>::half *)(sm.x + TC::at(16 * ib + m, cw + 4 * g4));
@@ -617,17 +623,31 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
                     for (int ib = 2 * tb; ib < W::NB; ++ib) y[ib] = mma(fc, TP::get(sm.p, prow, ib, tb, part), y[ib]);
             }
-            // KG tiles at a time, so that a tile's parts are not back to back
+            // KG tiles at a time, so that a tile's parts are not back to back.
+            // The segment pass never scales its sum: there the parts round into
+            // it together (states of 2048 rows 5.5e-7 -> 2.1e-7 off).
 #pragma unroll
             for (int k0 = 0; k0 < W::KT; k0 += W::KG) {
                 frag fb[W::KG];
 #pragma unroll
                 for (int k = 0; k < W::KG; ++k)
                     fb[k] = TA::template col8<8>(sm.b, bcol, lane, tb, (k0 + k) / 2, 4 * (k % 2));
+                if constexpr (OUT) {
 #pragma unroll
-                for (int p = NS - 1; p >= 0; --p)
+                    for (int p = NS - 1; p >= 0; --p)
 #pragma unroll
-                    for (int k = 0; k < W::KG; ++k) s[k0 + k] = mma(fb[k], fw[p], s[k0 + k]);
+                        for (int k = 0; k < W::KG; ++k) s[k0 + k] = mma(fb[k], fw[p], s[k0 + k]);
+                } else {
+                    f32x4 e[W::KG];
+#pragma unroll
+                    for (int k = 0; k < W::KG; ++k) e[k] = zero4();
+#pragma unroll
+                    for (int p = NS - 1; p >= 0; --p)
+#pragma unroll
+                        for (int k = 0; k < W::KG; ++k) e[k] = mma(fb[k], fw[p], e[k]);
+#pragma unroll
+                    for (int k = 0; k < W::KG; ++k) s[k0 + k] += e[k];
+                }
             }
         }
         if constexpr (OUT) {
@@ -650,6 +670,16 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
                     const bf16x4 o = {(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
                     buf_store8(rs, off + ib * step, __builtin_bit_cast(uint2, o));
                 }
+            }
+        }
+        if constexpr (DOT) {
+            // the state that crosses a span's border
+            const int at = REV ? lo : lo + CT;
+            if (w.mid && at % LIN_SPAN == 0 && at > 0 && at < len) {
+                float *so = w.mid + ((uint64_t)(bi * w.T + tb0 + at) / LIN_SPAN * w.HV + hv) * ((uint64_t)w.dc * DA) +
+                            (slice * DC + cw + m) * DA + 8 * g4;
+#pragma unroll
+                for (int kt = 0; kt < W::KT; ++kt) *(f32x4 *)(so + 32 * (kt / 2) + 4 * (kt % 2)) = s[kt];
             }
         }
         lds_barrier();
@@ -800,14 +830,43 @@ __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
 // so the running sums (64 bits) stay as short as a segment.  A block per
 // segment and head: the product <S, R> (2 K V floats) and rho move once; 19 us
 // at 8192 tokens of 32 heads and 128 x 256 states.
-//
-// A decay per head wants only the sum of dg over the rows, where each pair
-// counts i - j times.  Beside strong decays the running sums are mostly the
-// rounding of pairs that ended long before, so there the pairs inside a chunk
-// are weighed and summed by themselves (rho_in_chunk) and rho holds the pairs
-// that cross a chunk's border (median error of one head over 300 rows 7e-6 to
-// 3e-6, over 1280 rows 2.6e-6 to 0.7e-6; of 32 heads over 8192 rows 1e-6).
 constexpr int DGT = 512;
+
+// <S, R> of one head, for thread 0 (red: a double for each wave; every thread of the block calls it)
+__device__ __forceinline__ double state_product(const float *S, const float *R, int64_t elems, double *red) {
+    // 4 elements a thread and step, four steps' loads in flight (elems: 4096 to 32768)
+    float acc = 0.f;
+    for (int64_t i0 = (int64_t)threadIdx.x * 4; i0 < elems; i0 += 16 * DGT) {
+        f32x4 u[4], v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t i = i0 + k * 4 * DGT;
+            u[k] = v[k] = zero4();
+            if (i < elems) {
+                u[k] = *(const f32x4 *)(S + i);
+                v[k] = *(const f32x4 *)(R + i);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            acc += (u[k][0] * v[k][0] + u[k][1] * v[k][1]) + (u[k][2] * v[k][2] + u[k][3] * v[k][3]);
+    }
+    double x = acc;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+    if (lane_id() == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double c = 0.0;
+    if (threadIdx.x == 0)
+#pragma unroll 1
+        for (int i = 0; i < DGT / 64; ++i) c += red[i];
+    return c;
+}
+// What row t's decay scales a border's product by.
+__device__ __forceinline__ double row_decay(const LinDg &p, int64_t bi, int64_t t, int hv) {
+    return p.g ? (double)__builtin_amdgcn_exp2f((float)decay_log2(p.g[bi * p.g_bs + t * p.g_ts + hv])) : 1.0;
+}
+
 __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
     const uint32_t b = blockIdx.x;
     const int64_t id = b / (uint32_t)p.HV;
@@ -815,10 +874,7 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
     __shared__ double s_red[DGT / 64];
     __shared__ double s_carry;
     const LinItem it = lin_item(p.cu, p.nseq, p.T, p.seg_tok, id);
-    if (it.seq < 0) {
-        if (p.part && threadIdx.x == 0) p.part[id * p.HV + hv] = 0.0;
-        return;
-    }
+    if (it.seq < 0) return;
     const int64_t t0 = it.bos + it.seg * p.seg_tok;
     const int64_t t1 = t0 + p.seg_tok < it.eos ? t0 + p.seg_tok : it.eos;
     const int64_t bi = p.cu ? 0 : it.seq, tb0 = p.cu ? t0 : t0 - it.bos, tb1 = tb0 + (t1 - t0);
@@ -841,41 +897,10 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
         S = p.h0 + (it.seq * p.HV + hv) * p.elems;
         R = p.dh0 + (it.seq * p.HV + hv) * p.elems;
     }
-    double x = 0.0;
-    if (S) {
-        // 4 elements a thread and step, four steps' loads in flight (elems: 4096 to 32768)
-        float acc = 0.f;
-        for (int64_t i0 = (int64_t)threadIdx.x * 4; i0 < p.elems; i0 += 16 * DGT) {
-            f32x4 u[4], v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t i = i0 + k * 4 * DGT;
-                u[k] = v[k] = zero4();
-                if (i < p.elems) {
-                    u[k] = *(const f32x4 *)(S + i);
-                    v[k] = *(const f32x4 *)(R + i);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                acc += (u[k][0] * v[k][0] + u[k][1] * v[k][1]) + (u[k][2] * v[k][2] + u[k][3] * v[k][3]);
-        }
-        x = acc;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-    }
-    if (lane_id() == 0) s_red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double c = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < DGT / 64; ++i) c += s_red[i];
-        if (through >= 0 && p.g) c *= (double)__builtin_amdgcn_exp2f((float)decay_log2(p.g[bi * p.g_bs + through * p.g_ts + hv]));
-        s_carry = c;
-    }
+    const double c = S ? state_product(S, R, p.elems, s_red) : 0.0;
+    if (threadIdx.x == 0) s_carry = through >= 0 ? c * row_decay(p, bi, through, hv) : c;
     __syncthreads();
     // the rows from the anchored border, DGT at a time
-    double sum = 0.0;
     const int64_t BT = p.B * p.T;
     for (int64_t k0 = 0; k0 < tb1 - tb0; k0 += DGT) {
         const int64_t k = k0 + threadIdx.x, t = fwd ? tb0 + k : tb1 - 1 - k;
@@ -886,8 +911,6 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
             for (int i = 0; i < p.nq; ++i) d += (double)p.rho_q[at + (int64_t)i * p.HV * BT];
             for (int i = 0; i < p.nk; ++i) d -= (double)p.rho_k[at + (int64_t)i * p.HV * BT];
             if (fwd) d = -d;
-            if (p.rho_in_chunk)
-                for (int i = 0; i < p.nq; ++i) sum += (double)p.rho_in_chunk[at + (int64_t)i * p.HV * BT];
         }
         const double incl = wave_inclusive_sum_f64(d);
         const double tot = __shfl(incl, 63, 64);
@@ -897,15 +920,90 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
 #pragma unroll 1
         for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) upto += s_red[i];
         const double v = fwd ? upto - d : upto;
-        if (in) {
-            if (p.dg) p.dg[(bi * p.T + t) * p.HV + hv] = (float)v;
-            sum += v;
-        }
+        if (in) p.dg[(bi * p.T + t) * p.HV + hv] = (float)v;
         __syncthreads();
         if (threadIdx.x == DGT - 1) s_carry = upto;
         __syncthreads();
     }
-    if (!p.part) return;
+}
+
+// A decay per head wants the sum of dg over the rows: every pair, i - j times.
+// Pairs inside a chunk are weighed and summed by themselves (rho_in_chunk);
+// rho holds the pairs that cross a chunk's border.  For those, a span of n rows
+// between borders whose products B, B' are known gives, with d = rho_q - rho_k of
+// its s-th row, sum dg_t = (n+1)/2 B + (n-1)/2 B' + sum (s - (n+1)/2) d_s: the running
+// sum from B', with its mismatch at B spread evenly over the rows.  An error of d
+// thus counts n/2 times at most, so spans are short (LIN_SPAN rows, the walks
+// leave the states at their borders).  Where nothing is known of one border
+// (h0 without dh0, dht), the sum runs from the other.  A decay that takes a
+// whole chunk below 2^-24 leaves no pairs over it: then rows weigh by their
+// distance to their own chunk's ends, sum s rho_q + (n - s) rho_k, and no
+// difference is taken at all.
+// 8192 rows of 32 heads, 128 x 256: 1.3 to 3.3e-6 off with one anchor to 2048
+// rows, 3 to 6e-7 now, for 5% of the call (the walks' 100 MB of states).  A block a
+// span and head, bound by its border's states: 32 us there (134 MB, 4.2 TB/s).
+__global__ void __launch_bounds__(DGT) gdp_lin_dg_head_span_k(LinDg p) {
+    const uint32_t b = blockIdx.x, sp = blockIdx.y;
+    const int64_t id = b / (uint32_t)p.HV;
+    const int hv = (int)(b % (uint32_t)p.HV);
+    __shared__ double s_red[DGT / 64];
+    double *out = p.part + (id * gridDim.y + sp) * p.HV + hv;
+    const LinItem it = lin_item(p.cu, p.nseq, p.T, p.seg_tok, id);
+    const int64_t t0 = it.bos + it.seg * p.seg_tok;
+    const int64_t t1 = t0 + p.seg_tok < it.eos ? t0 + p.seg_tok : it.eos;
+    const int64_t a0 = t0 + (int64_t)sp * LIN_SPAN, a1 = a0 + LIN_SPAN < t1 ? a0 + LIN_SPAN : t1;
+    if (it.seq < 0 || a0 >= a1) {
+        if (threadIdx.x == 0) *out = 0.0;
+        return;
+    }
+    const int n = (int)(a1 - a0);
+    const bool first = a0 == it.bos, last = a1 == it.eos, end_known = !last || p.end_zero;
+    const bool start_known = !p.h0 || p.dh0;  // of a sequence
+    const bool none_over = decay_log2(p.g[hv]) * p.chunk < -24.0, apart = none_over && end_known;
+    const int64_t bi = p.cu ? 0 : it.seq, tb0 = p.cu ? a0 : a0 - it.bos;
+
+    // the product at the span's first row: its weight in this span and in the one before
+    double wb = 0.0;
+    if (!apart && (!first || start_known)) wb = end_known ? 0.5 * (n + 1) : (double)n;
+    if (!first && !none_over) {
+        const int before = sp > 0 ? LIN_SPAN : (int)(p.seg_tok - (int64_t)(gridDim.y - 1) * LIN_SPAN);
+        wb += a0 - before > it.bos || start_known ? 0.5 * (before - 1) : (double)before;
+    }
+    const float *S = nullptr, *R = nullptr;
+    if (wb != 0.0) {
+        const int64_t slot = it.slot0 + it.seg;
+        if (sp > 0) {
+            const int64_t at = ((bi * p.T + tb0) / LIN_SPAN * p.HV + hv) * p.elems;
+            S = p.s_mid + at;
+            R = p.r_mid + at;
+        } else if (!first) {
+            S = p.s_in + (slot * p.HV + hv) * p.elems;
+            R = p.r_in + ((slot - 1) * p.HV + hv) * p.elems;
+        } else if (p.h0) {  // dh0 has the first row's decay in it
+            S = p.h0 + (it.seq * p.HV + hv) * p.elems;
+            R = p.dh0 + (it.seq * p.HV + hv) * p.elems;
+        }
+    }
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < n; k += DGT) {
+        const int64_t BT = p.B * p.T, at = (int64_t)hv * BT + bi * p.T + tb0 + k;
+        double q = 0.0, r = 0.0;
+        for (int i = 0; i < p.nq; ++i) q += (double)p.rho_q[at + (int64_t)i * p.HV * BT];
+        for (int i = 0; i < p.nk; ++i) r += (double)p.rho_k[at + (int64_t)i * p.HV * BT];
+        for (int i = 0; i < p.nq; ++i) sum += (double)p.rho_in_chunk[at + (int64_t)i * p.HV * BT];
+        if (apart) {
+            const int lo = k / p.chunk * p.chunk, rows = n - lo < p.chunk ? n - lo : p.chunk;
+            sum += (k - lo + 1) * q + (rows - 1 - (k - lo)) * r;
+        } else {
+            const double w = !end_known ? k + 1 - n : first && !start_known ? k + 1 : k + 1 - 0.5 * (n + 1);
+            sum += w * (q - r);
+        }
+    }
+    if (S) {
+        const double c = state_product(S, R, p.elems, s_red);
+        if (threadIdx.x == 0) sum += wb * (first ? c : c * row_decay(p, bi, tb0, hv));
+        __syncthreads();
+    }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
     if (lane_id() == 0) s_red[threadIdx.x >> 6] = sum;
@@ -913,11 +1011,11 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
     if (threadIdx.x == 0) {
         double t = 0.0;
         for (int i = 0; i < DGT / 64; ++i) t += s_red[i];
-        p.part[id * p.HV + hv] = t;
+        *out = t;
     }
 }
 
-// dg of a decay per head: the sum over every segment, in a fixed order
+// dg of a decay per head: the sum over every span, in a fixed order
 __global__ void __launch_bounds__(256) gdp_lin_dg_head_k(const double *part, int64_t items, int HV, float *out) {
     __shared__ double s_red[4];
     const int hv = blockIdx.x;
@@ -1046,12 +1144,14 @@ hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
 
 hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream) {
     if (p.items > 0) {
-        hipLaunchKernelGGL(gdp_lin_dg_k, dim3((unsigned)(p.items * p.HV)), dim3(DGT), 0, stream, p);
+        const unsigned blocks = (unsigned)(p.items * p.HV);
+        if (p.dg) hipLaunchKernelGGL(gdp_lin_dg_k, dim3(blocks), dim3(DGT), 0, stream, p);
+        else hipLaunchKernelGGL(gdp_lin_dg_head_span_k, dim3(blocks, p.spans), dim3(DGT), 0, stream, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!dg_head) return hipSuccess;
-    hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items, p.HV, dg_head);
+    hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items * p.spans, p.HV, dg_head);
     return hipGetLastError();
 }
 

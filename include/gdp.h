@@ -602,8 +602,9 @@ typedef struct gdp_linattn_grads {
 
 /* Device workspace in bytes that gdp_linattn_fwd (backward == 0) or
  * gdp_linattn_bwd (backward != 0) needs for the sizes and pointers of a; 0:
- * none.  -1 on bad arguments.  Only the sizes, num_seqs and whether cu_seqlens
- * and h0 are NULL count, so it can be asked before the tensors exist. */
+ * none.  -1 on bad arguments.  Only the sizes, num_seqs and whether cu_seqlens,
+ * h0 and g are NULL count, so it can be asked before the tensors exist: with g
+ * NULL the size serves every kind of decay. */
 int64_t gdp_linattn_workspace_bytes(const gdp_linattn_args *a, int32_t backward);
 
 /* o and ht.  Long sequences are cut into segments that run in parallel: each
