@@ -29,9 +29,26 @@ from helpers import log
 from linref import inv_sqrt
 from linref_long import C, Long
 from test_gpu_linattn import BF16, DEV, F32, draws, gpu
-from test_gpu_linattn_precision import norm_close, rows_close
+from test_gpu_linattn_precision import norm_close, parts_of, rows_close
 
 SPAN = 512
+
+CASES = [  # lens, H, HV, K, V, dtype, decay, B, h0, dht
+    ([900, 0, 260, 3, 700], 2, 4, 128, 128, BF16, "token", None, True, True),
+    ([1300, 150], 1, 2, 64, 64, BF16, "head", None, True, True),
+    ([1300, 150], 1, 2, 64, 64, F32, "head", None, True, False),
+    ([130, 1000, 64], 1, 3, 64, 256, BF16, "token", None, True, False),
+    ([1000], 1, 2, 64, 256, F32, "head", 2, False, True),
+    ([777, 500], 2, 2, 128, 64, BF16, "head", None, False, True),
+    ([777, 500], 2, 4, 128, 64, F32, "token", None, False, False),
+    ([640, 900], 1, 2, 128, 256, BF16, "head", None, True, True),
+    ([640, 900], 2, 2, 128, 256, F32, "token", None, True, True),
+    ([2050], 2, 4, 128, 128, F32, "token", 1, True, True),
+    ([1500, 40, 0, 1100], 1, 4, 128, 128, BF16, "none", None, True, True),
+    ([2600], 1, 2, 64, 128, BF16, "head", 2, False, False),
+]
+IDS = ["%s-H%d-%d-K%d-V%d-%s-%s-%s" % ("x".join(map(str, c[0])), c[1], c[2], c[3], c[4],
+                                       "bf16" if c[5] == BF16 else "f32", c[6], c[7]) for c in CASES]
 
 
 def sequences(d):
@@ -112,6 +129,15 @@ def check(d, cu=None):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_segments(case):
+    lens, H, HV, K, V, dtype, decay, B, h0, dht = case
+    d = draws(51, lens, H, HV, K, V, dtype, decay, True, B)
+    d["h0"], d["dht"] = (d[x] if y else None for x, y in (("h0", h0), ("dht", dht)))
+    check(d)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ends", ["none", "h0", "dht", "both"])
 @pytest.mark.parametrize("lens,HV,K,V,dtype,B", [
     ([9000], 32, 64, 64, BF16, 1), ([1300], 32, 64, 64, BF16, 14), ([2500, 700, 4000, 1], 48, 64, 128, BF16, None),
@@ -146,3 +172,32 @@ def test_decay_per_head_against_differences():
         want = (loss(d["g"].double() + e) - loss(d["g"].double() - e)) / 2e-6
         # third derivatives: (rows of memory)^2 e^2 of the value; 64-bit sums over 1e-6: 1e-9 of the loss's terms
         assert abs(want - float(dg[h])) <= 1e-4 * abs(want) + 1e-4, h
+
+
+def test_bounds_need_three_parts():
+    """Two bf16 parts in a state's updates, or in the state behind rho, do not pass the bounds above; three do."""
+    d = draws(54, [600], 1, 2, 64, 64, BF16, "token", True, 1)
+    at = (0, slice(0, 600))
+    r = Long(d["q"][at], d["k"][at], d["v"][at], d["g"][at], inv_sqrt(64), d["h0"][0], d["do"][at], d["dht"][0])
+    (_, ht), (_, aht) = r.forward(), r.absolute().forward()
+    ref = r.backward()[3]
+
+    def state(parts):
+        E = parts_of(r.v * r.out[..., None], parts).transpose(2, 3) @ r.k
+        S = [r.h0]
+        for c in range(r.nc):
+            S.append(S[-1] * r.all[:, c, None, None] + E[:, c])
+        return S
+
+    def decays(parts):  # d of the rows from states in parts, run from the front of each chunk
+        S = torch.stack([parts_of(x, parts) for x in r.states()], 1)[:, :-1]
+        R = torch.stack([parts_of(x, parts) for x in r.gradients()], 1)[:, 1:]
+        q = (r.scale * (r.do @ S) * r.inn[..., None] * r.q).sum(-1)
+        k = ((r.v @ R) * r.out[..., None] * r.k).sum(-1)
+        err = (q - r.rho_q) - (k - r.rho_k)
+        return float(err.flip(-1).cumsum(-1).norm() / ref.norm())
+
+    state_close("ht", state(3)[-1], ht, aht, 600 + 64)
+    with pytest.raises(AssertionError):
+        state_close("ht", state(2)[-1], ht, aht, 600 + 64)
+    assert decays(3) < 3e-6 < decays(2), (decays(3), decays(2))
