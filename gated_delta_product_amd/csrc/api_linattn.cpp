@@ -116,7 +116,7 @@ int64_t lay_bwd(const gdp_linattn_args &a, const Plan &p, void *ws, BwdSpace *s)
     s->rho_in = m.take<float>(a.g ? 0 : s->nq * BTH);
     s->s_mid = m.take<float>(mids * a.HV * E);
     s->r_mid = m.take<float>(mids * a.HV * E);
-    s->part = m.take<double>(a.g ? 0 : p.items * s->spans * a.HV);
+    s->part = m.take<double>(a.g ? 0 : p.items * a.HV);
     const bool shared = a.HV != a.H;
     s->dq = m.take<float>(shared ? BTH * a.K : 0);
     s->dk = m.take<float>(shared ? BTH * a.K : 0);

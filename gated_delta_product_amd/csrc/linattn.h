@@ -78,7 +78,7 @@ struct LinDg {
     const float *h0, *dh0;            // [nseq, HV, V, K] or NULL
     bool end_zero;                    // no gradient enters behind the last row
     float *dg;         // [B, T, HV], or NULL for a decay per head
-    double *part;      // [items, spans, HV]: sums over each span (a decay per head)
+    double *part;      // [items, HV]: sums over each segment (a decay per head)
 };
 
 // y[i] [B*T, H, D] = sums over r neighbouring heads of x[i] [B*T, H*r, D]

@@ -941,68 +941,70 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
 // difference is taken at all.
 // 8192 rows of 32 heads, 128 x 256: 1.3 to 3.3e-6 off with one anchor to 2048
 // rows, 3 to 6e-7 now, for 5% of the call (the walks' 100 MB of states).  A block a
-// span and head, bound by its border's states: 32 us there (134 MB, 4.2 TB/s).
-__global__ void __launch_bounds__(DGT) gdp_lin_dg_head_span_k(LinDg p) {
-    const uint32_t b = blockIdx.x, sp = blockIdx.y;
+// segment and head, its spans one after the other (a block to each was 33 us for
+// 34 here, but 596 for 177 with 1000 requests of 20 rows); bound by the borders'
+// states, 134 MB here (4 TB/s).
+__global__ void __launch_bounds__(DGT) gdp_lin_dg_spans_k(LinDg p) {
+    const uint32_t b = blockIdx.x;
     const int64_t id = b / (uint32_t)p.HV;
     const int hv = (int)(b % (uint32_t)p.HV);
     __shared__ double s_red[DGT / 64];
-    double *out = p.part + (id * gridDim.y + sp) * p.HV + hv;
     const LinItem it = lin_item(p.cu, p.nseq, p.T, p.seg_tok, id);
     const int64_t t0 = it.bos + it.seg * p.seg_tok;
-    const int64_t t1 = t0 + p.seg_tok < it.eos ? t0 + p.seg_tok : it.eos;
-    const int64_t a0 = t0 + (int64_t)sp * LIN_SPAN, a1 = a0 + LIN_SPAN < t1 ? a0 + LIN_SPAN : t1;
-    if (it.seq < 0 || a0 >= a1) {
-        if (threadIdx.x == 0) *out = 0.0;
-        return;
-    }
-    const int n = (int)(a1 - a0);
-    const bool first = a0 == it.bos, last = a1 == it.eos, end_known = !last || p.end_zero;
+    const int64_t t1 = it.seq < 0 ? t0 : t0 + p.seg_tok < it.eos ? t0 + p.seg_tok : it.eos;
+    const int64_t bi = p.cu ? 0 : it.seq, BT = p.B * p.T;
     const bool start_known = !p.h0 || p.dh0;  // of a sequence
-    const bool none_over = decay_log2(p.g[hv]) * p.chunk < -24.0, apart = none_over && end_known;
-    const int64_t bi = p.cu ? 0 : it.seq, tb0 = p.cu ? a0 : a0 - it.bos;
+    const bool none_over = decay_log2(p.g[hv]) * p.chunk < -24.0;
 
-    // the product at the span's first row: its weight in this span and in the one before
-    double wb = 0.0;
-    if (!apart && (!first || start_known)) wb = end_known ? 0.5 * (n + 1) : (double)n;
-    if (!first && !none_over) {
-        const int before = sp > 0 ? LIN_SPAN : (int)(p.seg_tok - (int64_t)(gridDim.y - 1) * LIN_SPAN);
-        wb += a0 - before > it.bos || start_known ? 0.5 * (before - 1) : (double)before;
-    }
-    const float *S = nullptr, *R = nullptr;
-    if (wb != 0.0) {
-        const int64_t slot = it.slot0 + it.seg;
-        if (sp > 0) {
-            const int64_t at = ((bi * p.T + tb0) / LIN_SPAN * p.HV + hv) * p.elems;
-            S = p.s_mid + at;
-            R = p.r_mid + at;
-        } else if (!first) {
-            S = p.s_in + (slot * p.HV + hv) * p.elems;
-            R = p.r_in + ((slot - 1) * p.HV + hv) * p.elems;
-        } else if (p.h0) {  // dh0 has the first row's decay in it
-            S = p.h0 + (it.seq * p.HV + hv) * p.elems;
-            R = p.dh0 + (it.seq * p.HV + hv) * p.elems;
-        }
-    }
     double sum = 0.0;
-    for (int k = threadIdx.x; k < n; k += DGT) {
-        const int64_t BT = p.B * p.T, at = (int64_t)hv * BT + bi * p.T + tb0 + k;
-        double q = 0.0, r = 0.0;
-        for (int i = 0; i < p.nq; ++i) q += (double)p.rho_q[at + (int64_t)i * p.HV * BT];
-        for (int i = 0; i < p.nk; ++i) r += (double)p.rho_k[at + (int64_t)i * p.HV * BT];
-        for (int i = 0; i < p.nq; ++i) sum += (double)p.rho_in_chunk[at + (int64_t)i * p.HV * BT];
-        if (apart) {
-            const int lo = k / p.chunk * p.chunk, rows = n - lo < p.chunk ? n - lo : p.chunk;
-            sum += (k - lo + 1) * q + (rows - 1 - (k - lo)) * r;
-        } else {
-            const double w = !end_known ? k + 1 - n : first && !start_known ? k + 1 : k + 1 - 0.5 * (n + 1);
-            sum += w * (q - r);
+    for (int sp = 0; sp < p.spans; ++sp) {
+        const int64_t a0 = t0 + (int64_t)sp * LIN_SPAN, a1 = a0 + LIN_SPAN < t1 ? a0 + LIN_SPAN : t1;
+        if (a0 >= a1) break;
+        const int n = (int)(a1 - a0);
+        const bool first = a0 == it.bos, end_known = a1 < it.eos || p.end_zero, apart = none_over && end_known;
+        const int64_t tb0 = p.cu ? a0 : a0 - it.bos;
+
+        // the product at the span's first row: its weight in this span and in the one before
+        double wb = 0.0;
+        if (!apart && (!first || start_known)) wb = end_known ? 0.5 * (n + 1) : (double)n;
+        if (!first && !none_over) {
+            const int before = sp > 0 ? LIN_SPAN : (int)(p.seg_tok - (int64_t)(p.spans - 1) * LIN_SPAN);
+            wb += a0 - before > it.bos || start_known ? 0.5 * (before - 1) : (double)before;
         }
-    }
-    if (S) {
-        const double c = state_product(S, R, p.elems, s_red);
-        if (threadIdx.x == 0) sum += wb * (first ? c : c * row_decay(p, bi, tb0, hv));
-        __syncthreads();
+        const float *S = nullptr, *R = nullptr;
+        if (wb != 0.0) {
+            const int64_t slot = it.slot0 + it.seg;
+            if (sp > 0) {
+                const int64_t at = ((bi * p.T + tb0) / LIN_SPAN * p.HV + hv) * p.elems;
+                S = p.s_mid + at;
+                R = p.r_mid + at;
+            } else if (!first) {
+                S = p.s_in + (slot * p.HV + hv) * p.elems;
+                R = p.r_in + ((slot - 1) * p.HV + hv) * p.elems;
+            } else if (p.h0) {  // dh0 has the first row's decay in it
+                S = p.h0 + (it.seq * p.HV + hv) * p.elems;
+                R = p.dh0 + (it.seq * p.HV + hv) * p.elems;
+            }
+        }
+        for (int k = threadIdx.x; k < n; k += DGT) {
+            const int64_t at = (int64_t)hv * BT + bi * p.T + tb0 + k;
+            double q = 0.0, r = 0.0;
+            for (int i = 0; i < p.nq; ++i) q += (double)p.rho_q[at + (int64_t)i * p.HV * BT];
+            for (int i = 0; i < p.nk; ++i) r += (double)p.rho_k[at + (int64_t)i * p.HV * BT];
+            for (int i = 0; i < p.nq; ++i) sum += (double)p.rho_in_chunk[at + (int64_t)i * p.HV * BT];
+            if (apart) {
+                const int lo = k / p.chunk * p.chunk, rows = n - lo < p.chunk ? n - lo : p.chunk;
+                sum += (k - lo + 1) * q + (rows - 1 - (k - lo)) * r;
+            } else {
+                const double w = !end_known ? k + 1 - n : first && !start_known ? k + 1 : k + 1 - 0.5 * (n + 1);
+                sum += w * (q - r);
+            }
+        }
+        if (S) {
+            const double c = state_product(S, R, p.elems, s_red);
+            if (threadIdx.x == 0) sum += wb * (first ? c : c * row_decay(p, bi, tb0, hv));
+            __syncthreads();
+        }
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
@@ -1011,11 +1013,11 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_head_span_k(LinDg p) {
     if (threadIdx.x == 0) {
         double t = 0.0;
         for (int i = 0; i < DGT / 64; ++i) t += s_red[i];
-        *out = t;
+        p.part[id * p.HV + hv] = t;
     }
 }
 
-// dg of a decay per head: the sum over every span, in a fixed order
+// dg of a decay per head: the sum over every segment, in a fixed order
 __global__ void __launch_bounds__(256) gdp_lin_dg_head_k(const double *part, int64_t items, int HV, float *out) {
     __shared__ double s_red[4];
     const int hv = blockIdx.x;
@@ -1144,14 +1146,14 @@ hipError_t launch_lin_scan(const LinScan &p, hipStream_t stream) {
 
 hipError_t launch_lin_dg(const LinDg &p, float *dg_head, hipStream_t stream) {
     if (p.items > 0) {
-        const unsigned blocks = (unsigned)(p.items * p.HV);
-        if (p.dg) hipLaunchKernelGGL(gdp_lin_dg_k, dim3(blocks), dim3(DGT), 0, stream, p);
-        else hipLaunchKernelGGL(gdp_lin_dg_head_span_k, dim3(blocks, p.spans), dim3(DGT), 0, stream, p);
+        const dim3 grid((unsigned)(p.items * p.HV));
+        if (p.dg) hipLaunchKernelGGL(gdp_lin_dg_k, grid, dim3(DGT), 0, stream, p);
+        else hipLaunchKernelGGL(gdp_lin_dg_spans_k, grid, dim3(DGT), 0, stream, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!dg_head) return hipSuccess;
-    hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items * p.spans, p.HV, dg_head);
+    hipLaunchKernelGGL(gdp_lin_dg_head_k, dim3((unsigned)p.HV), dim3(256), 0, stream, p.part, p.items, p.HV, dg_head);
     return hipGetLastError();
 }
 
