@@ -709,10 +709,9 @@ def _lin_args(q, k, v, g, scale, cu_seqlens, initial_state):
 
 
 def _workspace(need, dev):
-    if need < 0:
-        raise GdpError(GDP_ERR_INVALID, lib().gdp_last_error().decode())
-    # torch's caching allocator returns 512-byte aligned blocks
-    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    # torch's caching allocator returns 512-byte aligned blocks.  Sizes that are
+    # refused (need < 0) get none: the call itself then says so, with its status.
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
 
 
 def linattn_fwd(q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=None, output_final_state=False, o=None):
