@@ -268,7 +268,7 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
         gdp::LinWalks e{{w, {}, {}}, 1};
         e.w[0].seg_out = ws.seg;
         e.w[0].seg_tot = ws.tot;
-        if ((st = hip_status(gdp::launch_lin_walks(e, a.dtype, false, a.ht != nullptr, s), name)) != GDP_OK) return st;
+        if ((st = hip_status(gdp::launch_lin_segments(e, a.dtype, a.ht != nullptr, false, s), name)) != GDP_OK) return st;
         gdp::LinScan c = scan_base(a, p);
         c.n = 1;
         c.s[0] = {false, a.h0, ws.seg, ws.tot};
@@ -278,7 +278,7 @@ gdp_status gdp_linattn_fwd(const gdp_linattn_args *args, void *workspace, int64_
     w.sy = a.scale;
     w.y = a.o;
     w.s_out = a.ht;
-    return hip_status(gdp::launch_lin_walks({{w, {}, {}}, 1}, a.dtype, true, a.ht != nullptr, s), name);
+    return hip_status(gdp::launch_lin_rows({{w, {}, {}}, 1}, a.dtype, a.ht != nullptr, s), name);
 }
 
 gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads *d, void *workspace,
@@ -346,7 +346,7 @@ gdp_status gdp_linattn_bwd(const gdp_linattn_args *args, const gdp_linattn_grads
         b.sb = a.scale;
         b.seg_out = ws.r;
         b.seg_tot = ws.r_tot;
-        if ((st = hip_status(gdp::launch_lin_walks({{f, b, {}}, 2}, a.dtype, false, want_g || d->dh0, s), name)) != GDP_OK)
+        if ((st = hip_status(gdp::launch_lin_segments({{f, b, {}}, 2}, a.dtype, d->dh0 != nullptr, want_g, s), name)) != GDP_OK)
             return st;
         gdp::LinScan c = scan_base(a, p);
         c.n = 2;

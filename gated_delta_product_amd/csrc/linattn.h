@@ -100,8 +100,10 @@ struct LinOutside {
 };
 hipError_t launch_lin_outside(const LinOutside &p, hipStream_t stream);
 
-// out: the rows y (else each segment's state only); exact: states to 24 bits
-hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, bool exact, hipStream_t stream);
+// the rows y; exact: states to 24 bits
+hipError_t launch_lin_rows(const LinWalks &w, gdp_dtype dtype, bool exact, hipStream_t stream);
+// each segment's own state; dg: it is to serve dg too
+hipError_t launch_lin_segments(const LinWalks &w, gdp_dtype dtype, bool exact, bool dg, hipStream_t stream);
 // w[0] dq, w[1] dk, w[2] dv; dot: rho of dq and dk too
 int lin_grads_slice(int K, int V);
 hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream);

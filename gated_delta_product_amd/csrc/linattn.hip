@@ -119,7 +119,7 @@ struct Tile {
 };
 
 // The scores P of a chunk as operands: 16 x 32 tiles (rows i, 32 rows j) at
-// and below the diagonal, each value in NP bf16 parts (all first parts, then
+// and below the diagonal, each value in two bf16 parts (all first parts, then
 // all second ones); in float32, rows as above.  The tiles (0, 0) and (2, 1)
 // hold 16 columns, the lanes of the other 16 read the zeros behind them: two
 // parts then take 10 KB, and two blocks of the widest walk fit a compute unit.
@@ -285,6 +285,10 @@ __device__ __forceinline__ LinItem lin_item(const int32_t *cu, int64_t nseq, int
 //      values: the part of the row that the decays scale.
 // NS:  bf16 parts of the decayed c in the state update (16 or 24 bits).
 // NQ:  parts of the state in S a (1 in float32, 2 for bf16 rows, 3 for dg).
+//      The segment pass has no such product; with 3, states that dg is formed
+//      from, it rounds a chunk's parts into its state together (that state is
+//      never scaled, and each part by itself rounds relative to all of it:
+//      5.5e-7 -> 2.1e-7 off after 2048 rows, for 10% of the pass).
 template <typename T> constexpr bool F32_Y = sizeof(T) == 4;
 template <typename T> constexpr int ROW_PARTS = sizeof(T) == 4 ? 1 : 2;
 
@@ -306,7 +310,8 @@ struct Walk {
     static constexpr int OCC = DA == 256 ? (WV == 8 ? 2 : 1) : WV / 2;
     // tiles whose operands are loaded together: fewer where registers are
     // short (a spill's reload would wait for every row in flight)
-    static constexpr int KG = !OUT || (DOT && OCC >= 4) ? 2 : 4, IG = DOT && OCC >= 4 ? 2 : NB;
+    static constexpr bool TOGETHER = !OUT && NQ == 3;
+    static constexpr int KG = TOGETHER || (DOT && OCC >= 4) ? 2 : 4, IG = DOT && OCC >= 4 ? 2 : NB;
     static constexpr int UA = CT * DA * (int)sizeof(T) / 16 / NT, UC = CT * DC * (int)sizeof(T) / 16 / NT;
     typedef Tile<T, DA> TA;
     typedef Tile<T, DC> TC;
@@ -503,7 +508,7 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
     // them, and so do the stores of y.
     auto chunk = [&](int ch, Set &cur) __attribute__((always_inline)) {
         const int lo = low(ch), n = count(lo), buf = ch % W::GD;
-        // rho of a decay per head: pairs inside a chunk weighed by their distance, see gdp_lin_dg_k
+        // rho of a decay per head: pairs inside a chunk weighed by their distance, see gdp_lin_dg_spans_k
         const bool apart = DOT && w.rho_in_chunk;
         // LDS addresses are formed anew in each chunk: held over it they would
         // not fit the registers
@@ -623,16 +628,14 @@ __device__ __forceinline__ void lin_walk(const LinWalk &w, int64_t id, int hv, i
 #pragma unroll
                     for (int ib = 2 * tb; ib < W::NB; ++ib) y[ib] = mma(fc, TP::get(sm.p, prow, ib, tb, part), y[ib]);
             }
-            // KG tiles at a time, so that a tile's parts are not back to back.
-            // The segment pass never scales its sum: there the parts round into
-            // it together (states of 2048 rows 5.5e-7 -> 2.1e-7 off).
+            // KG tiles at a time, so that a tile's parts are not back to back
 #pragma unroll
             for (int k0 = 0; k0 < W::KT; k0 += W::KG) {
                 frag fb[W::KG];
 #pragma unroll
                 for (int k = 0; k < W::KG; ++k)
                     fb[k] = TA::template col8<8>(sm.b, bcol, lane, tb, (k0 + k) / 2, 4 * (k % 2));
-                if constexpr (OUT) {
+                if constexpr (!W::TOGETHER) {
 #pragma unroll
                     for (int p = NS - 1; p >= 0; --p)
 #pragma unroll
@@ -730,11 +733,9 @@ __device__ __forceinline__ void lin_block(const LinWalk &w, void *lds) {
                                                *(typename Walk<T, DA, DC, NS, NQ, OUT, DOT>::Lds *)lds);
 }
 
-template <typename T, int DA, int DC, int NS, bool OUT>
-__global__ void __launch_bounds__((Walk<T, DA, DC, NS, ROW_PARTS<T>, OUT, false>::NT),
-                                  (Walk<T, DA, DC, NS, ROW_PARTS<T>, OUT, false>::OCC))
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT>
+__global__ void __launch_bounds__((Walk<T, DA, DC, NS, NQ, OUT, false>::NT), (Walk<T, DA, DC, NS, NQ, OUT, false>::OCC))
 gdp_lin_walk_k(LinWalks p) {
-    constexpr int NQ = ROW_PARTS<T>;
     __shared__ __align__(16) char lds[sizeof(typename Walk<T, DA, DC, NS, NQ, OUT, false>::Lds)];
     if (blockIdx.y == 0) lin_block<T, DA, DC, NS, NQ, OUT, false, false>(p.w[0], lds);
     else if constexpr (!OUT) lin_block<T, DA, DC, NS, NQ, OUT, false, true>(p.w[1], lds);
@@ -1075,26 +1076,33 @@ __global__ void __launch_bounds__(256) gdp_lin_outside_k(LinOutside p) {
 }
 
 // ---------------------------------------------------------------- launches
-template <typename T, int DA, int DC, int NS, bool OUT>
+template <typename T, int DA, int DC, int NS, int NQ, bool OUT>
 static hipError_t launch_walk_t(const LinWalks &w, hipStream_t stream) {
     const int64_t blocks = w.w[0].items * w.w[0].HV * (w.w[0].dc / DC);
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, OUT>), dim3((unsigned)blocks, w.n), dim3(4 * DC), 0, stream, w);
+    hipLaunchKernelGGL((gdp_lin_walk_k<T, DA, DC, NS, NQ, OUT>), dim3((unsigned)blocks, w.n), dim3(4 * DC), 0, stream, w);
     return hipGetLastError();
 }
 
-template <typename T, int NS, bool OUT>
+template <typename T, int NS, int NQ, bool OUT>
 static hipError_t launch_walk_dims(const LinWalks &w, hipStream_t stream) {
     const int da = w.w[0].da, dc = w.w[0].dc;
-    if (da == 64) return dc == 64 ? launch_walk_t<T, 64, 64, NS, OUT>(w, stream) : launch_walk_t<T, 64, 128, NS, OUT>(w, stream);
-    return dc == 64 ? launch_walk_t<T, 128, 64, NS, OUT>(w, stream) : launch_walk_t<T, 128, 128, NS, OUT>(w, stream);
+    if (da == 64)
+        return dc == 64 ? launch_walk_t<T, 64, 64, NS, NQ, OUT>(w, stream) : launch_walk_t<T, 64, 128, NS, NQ, OUT>(w, stream);
+    return dc == 64 ? launch_walk_t<T, 128, 64, NS, NQ, OUT>(w, stream) : launch_walk_t<T, 128, 128, NS, NQ, OUT>(w, stream);
 }
 
-hipError_t launch_lin_walks(const LinWalks &w, gdp_dtype dtype, bool out, bool exact, hipStream_t stream) {
+hipError_t launch_lin_rows(const LinWalks &w, gdp_dtype dtype, bool exact, hipStream_t stream) {
     if (w.w[0].items == 0) return hipSuccess;
-    if (dtype == GDP_F32) return out ? launch_walk_dims<float, 1, true>(w, stream) : launch_walk_dims<float, 1, false>(w, stream);
-    if (exact) return out ? launch_walk_dims<bf16, 3, true>(w, stream) : launch_walk_dims<bf16, 3, false>(w, stream);
-    return out ? launch_walk_dims<bf16, 2, true>(w, stream) : launch_walk_dims<bf16, 2, false>(w, stream);
+    if (dtype == GDP_F32) return launch_walk_dims<float, 1, 1, true>(w, stream);
+    return exact ? launch_walk_dims<bf16, 3, 2, true>(w, stream) : launch_walk_dims<bf16, 2, 2, true>(w, stream);
+}
+
+hipError_t launch_lin_segments(const LinWalks &w, gdp_dtype dtype, bool exact, bool dg, hipStream_t stream) {
+    if (w.w[0].items == 0) return hipSuccess;
+    if (dtype == GDP_F32) return dg ? launch_walk_dims<float, 1, 3, false>(w, stream) : launch_walk_dims<float, 1, 1, false>(w, stream);
+    if (dg) return launch_walk_dims<bf16, 3, 3, false>(w, stream);
+    return exact ? launch_walk_dims<bf16, 3, 2, false>(w, stream) : launch_walk_dims<bf16, 2, 2, false>(w, stream);
 }
 
 // Columns of c that one walk of the gradients takes: as many waves in each of the three.
