@@ -624,6 +624,9 @@ def decode_update(q, k, v, beta, g, state, M, slots=None, scale=None, o=None):
 # These calls are made once a layer and token in decoding, where the host sets
 # the pace: pointers go over as plain integers and every attribute of a tensor
 # is asked for once.
+#
+# Like every call of this module they record nothing for autograd: results
+# have no graph, also where an input requires gradients, which the _bwd calls give.
 
 def _call(dev, fn, *args):
     """fn(*args, stream) on the tensors' device and its current stream."""
@@ -722,8 +725,11 @@ def linattn_fwd(q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=None
     and batch rows may be strided); g float32 [B, T, HV] natural-log decay per
     token, [HV] per head, or None; cu_seqlens int32 [num_seqs + 1] (B == 1) or
     None; initial_state [nseq, HV, V, K] float32 or None.  ``o`` may hold a
-    preallocated contiguous output.  Returns (o [B, T, HV, V], ht
-    [nseq, HV, V, K] float32 or None)."""
+    preallocated contiguous output.  scale None, or any that is not above zero,
+    is 1/sqrt(K).  Returns (o [B, T, HV, V], ht [nseq, HV, V, K] float32 or
+    None).  Rows of o outside every request are not written: they keep what
+    ``o`` held, or are uninitialised.  Nothing is recorded for autograd; the
+    gradients come from linattn_bwd."""
     dev = _need_cuda(q, k, v, g, cu_seqlens, initial_state, o)
     nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state)
     o = _output(o, "o", (a.B, a.T, a.HV, a.V), q.dtype, dev)
@@ -745,7 +751,8 @@ def linattn_bwd(do, q, k, v, g=None, scale=None, cu_seqlens=None, initial_state=
     dv, dg, dh0): dq, dk [B, T, H, K], summed over the value heads of a key
     head, dv [B, T, HV, V], dg shaped as g (None without g), dh0
     [nseq, HV, V, K] float32 (None without initial_state).  Rows of tokens
-    outside every request hold zeros."""
+    outside every request hold zeros, and those of do are not read.  scale as
+    in linattn_fwd."""
     dev = _need_cuda(q, k, v, g, cu_seqlens, initial_state, do, dht)
     nseq, a = _lin_args(q, k, v, g, scale, cu_seqlens, initial_state)
     ds = _rows(do, "do", v.shape, q.dtype)
@@ -770,7 +777,7 @@ def linattn_decode(q, k, v, state, g=None, slots=None, scale=None, o=None):
     of linattn_fwd.  q, k [n, S, H, K], v [n, S, HV, V] (strided as there); g
     float32 [n, S, HV], [HV] or None; state [pool, HV, V, K] float32, updated
     in place; slots int32 [n] (outside [0, pool): skipped, its o rows zero) or
-    None.  Returns o [n, S, HV, V]."""
+    None; scale as there.  Returns o [n, S, HV, V].  It has no gradients."""
     dev = _need_cuda(q, k, v, g, state, slots, o)
     n, S, H, HV, K, V, code, qs, ks, vs = _qkv(q, k, v)
     pool = state.shape[0] if state.dim() else 0
@@ -837,7 +844,7 @@ def group_norm_fwd(x, groups, weight=None, bias=None, gate=None, activation="sil
     neighbouring channels (centered=False: by the root of the mean square alone), times weight plus bias ([C]
     float32 or None), then times activation(gate), or without a gate through the activation ("silu", "sigmoid",
     "none").  gate is shaped as x; both may be slices of wider rows.  Returns y, contiguous (``out`` if given; it
-    may be x or gate)."""
+    may be x or gate).  Nothing is recorded for autograd; the gradients come from group_norm_bwd."""
     dev = _need_cuda(x, weight, bias, gate, out)
     a = _norm_args(x, groups, weight, bias, gate, activation, centered, eps)
     out = _output(out, "out", x.shape, x.dtype, dev)

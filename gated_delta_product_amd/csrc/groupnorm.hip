@@ -13,7 +13,14 @@
 // neighbouring lanes.  Both directions move each tensor once and are bound by
 // that: 32768 rows of 16 x 128 bf16 with a gate, forwards 82 us (403 MB, 4.9
 // TB/s, a large copy reaching 5.1), backwards 140 us (671 MB, 4.8 TB/s;
-// three inputs, the next row's too, and two sums a channel take 111 registers).  256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
+// three inputs, the next row's too, and two sums a channel take 111 registers).
+// 256 such rows take 5 us, 2048 x 1024 backwards 14 and 5 for the sums.
+// Slower: gradients where the groups do not divide a block's row sets (any but
+// a power of two), whose partial sums are not joined (5.5 M elements, gated: 3 x 40
+// channels 164 us, 4 x 40 34; 3 x 128 67, 4 x 128 25; 24 x 128 28, 16 x 128 26), and
+// groups of over 1024 channels, which one wave holds: from 2049 on the gradients
+// spill (8192 rows of one group of 4096: 69 us forwards, 378 backwards, where 32
+// groups of 128 take 38 and 83).
 #include "gdp_common.h"
 #include "gdp_internal.h"
 #include "groupnorm.h"
@@ -371,7 +378,10 @@ int64_t group_norm_split(int64_t rows, int groups, int D, bool bwd) {
     // / 16 / 32 rows 107 / 95 / 90 / 91 us).  Backwards no more threads than two
     // waves a SIMD (each set of rows costs 8 bytes a channel of partial sums;
     // one, two or three times as many 154, 163, 166 us, and 173 with one block
-    // too many, that runs alone at the end) and at least 4 rows.
+    // too many, that runs alone at the end) and at least 4 rows.  Both rules count
+    // 8 elements a thread, which holds for aligned bf16 groups of at most 512
+    // channels; float32 runs twice as many threads, single elements (rows that do
+    // not start on 16 bytes) up to eight times, wider groups fewer.
     const int64_t fill = (bwd ? 131072 : 262144) * 8 / ((int64_t)groups * D);
     const int64_t few = (rows + (bwd ? 3 : 15)) / (bwd ? 4 : 16);
     int64_t s = bwd ? (few < fill ? few : fill) : (few > fill ? few : fill);

@@ -28,14 +28,19 @@
 //
 // What bounds it: not the bytes but the chain of a chunk (scores, barrier,
 // decayed products, barrier) in 8 to 16 waves a compute unit, with matrix and
-// vector instructions sharing the issue.  Times in microseconds, bf16,
-// K = V = 128 and [what the bytes alone take] at 5.1 TB/s:
-//   32768 tokens, 16 heads, forwards: segment pass 75 [53 for k, v], scan 16,
-//     rows 126 [105]; 210 in all, 2.6 TB/s of what must move, 4.5 of what does
-//   8 requests of 821 to 3562 tokens, H 4, HV 16: 42 + 13 + 71
-//   the same backwards, 3 walks in one launch: 273 at 1.9 GHz, 24-bit states
-//   8192 tokens, 32 heads, V = 256 backwards: 525, its matrix cores a third busy
-//     (256 rows of S^T a wave leave two waves a SIMD) at 1.7 GHz
+// vector instructions sharing the issue.  Kernel times in microseconds in an
+// unbroken run of calls (clock 2.1 to 2.5 GHz; a call takes 3 to 16% more there
+// than in a short run), bf16, K = V = 128, [what the bytes alone take] at 5.1 TB/s
+// and the share of time that the matrix cores are busy:
+//   32768 tokens, 16 heads, forwards: segment pass 83 [53 for k, v] 28%, scan 18,
+//     rows 164 [105] 33%
+//   8 requests of 821 to 3562 tokens, H 4, HV 16: 46 (18%) + 14 + 90 (24%)
+//   the same backwards: segment pass 72 (20%), scan 25, 3 walks in one launch 264
+//     (27%, 24-bit states), head sums 61, dg 18, zeros 5
+//   8192 tokens, 32 heads, V = 256 backwards, decay per head: segment pass 127
+//     (24%), scan 11, walks 477 (29%; 256 rows of S^T a wave leave two waves a
+//     SIMD), dg 41 + 5
+// A third of the LDS cycles of every walk are bank conflicts.
 #include "gdp_common.h"
 #include "gdp_internal.h"
 #include "linattn.h"
@@ -764,8 +769,11 @@ __global__ void __launch_bounds__(SL * 4, (Grads<T, K, V, SL, NS, NQ, ND, DOT>::
 // Each sequence's segments in walk order: entering state of the first is h0
 // (or zero), then S <- 2^tot S + E.  The E of a segment is replaced by the
 // state entering it.  One thread per 4 state elements: the states go in and
-// out once and the chain over the segments is short (16 to 32), so it is the
-// bytes: 16 us for 32 segments of 16 heads (34 MB, 4.2 TB/s both ways).
+// out once.  With 16 heads and more the chain over the segments is short (16 to
+// 32) and the bytes bound it: 18 us for 32 segments of 16 heads (34 MB, 3.8 TB/s
+// both ways).  With one or two heads a row has up to 256 segments and more, and
+// the chain, 8 loads at a time, bounds it: 79 us at 32768 tokens of one head,
+// beside 11 and 18 us of walks.
 __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
     const int64_t seq = blockIdx.x / p.HV;
     const int hv = (int)(blockIdx.x % p.HV);
@@ -829,8 +837,8 @@ __global__ void __launch_bounds__(256) gdp_lin_scan_k(LinScan p) {
 // less what it gives to later ones.  Each segment is anchored at one border,
 // where the sum is the product of the state and the gradient that meet there,
 // so the running sums (64 bits) stay as short as a segment.  A block per
-// segment and head: the product <S, R> (2 K V floats) and rho move once; 19 us
-// at 8192 tokens of 32 heads and 128 x 256 states.
+// segment and head: the product <S, R> (2 K V floats) and rho move once; 18 us
+// for 20 segments of 16 heads and 128 x 128 states.
 constexpr int DGT = 512;
 
 // <S, R> of one head, for thread 0 (red: a double for each wave; every thread of the block calls it)
@@ -944,7 +952,7 @@ __global__ void __launch_bounds__(DGT) gdp_lin_dg_k(LinDg p) {
 // rows, 3 to 6e-7 now, for 5% of the call (the walks' 100 MB of states).  A block a
 // segment and head, its spans one after the other (a block to each was 33 us for
 // 34 here, but 596 for 177 with 1000 requests of 20 rows); bound by the borders'
-// states, 134 MB here (4 TB/s).
+// states, 134 MB here (33 us, 41 in an unbroken run of calls).
 __global__ void __launch_bounds__(DGT) gdp_lin_dg_spans_k(LinDg p) {
     const uint32_t b = blockIdx.x;
     const int64_t id = b / (uint32_t)p.HV;
@@ -1135,7 +1143,7 @@ static hipError_t launch_grads_dims(const LinWalks &w, hipStream_t stream) {
 // the state as the operand of S a.  A row is then off by its own rounding,
 // 1.65e-3; with scores and operand in one part it was 2.3e-3, and elements
 // whose terms cancel were off by many times their rounding.  The second parts
-// cost 3 to 9% of a call (packed prompts 119 to 129 us, 32768 tokens 210 to 229).
+// cost 3 to 10% of a call (packed prompts 119 to 129 us, 32768 tokens 210 to 230).
 hipError_t launch_lin_grads(const LinWalks &w, gdp_dtype dtype, bool dot, hipStream_t stream) {
     if (w.w[0].items == 0) return hipSuccess;
     if (dtype == GDP_F32)
