@@ -37,3 +37,18 @@ def test_refusals_keep_the_library_s_status(host, name, call, status):
         call()
     assert e.value.status == status, str(e.value)
     assert "workspace" not in str(e.value)
+
+
+@pytest.mark.parametrize("T,H,HV,K,V", [(100, 1, 2, 64, 64), (9000, 32, 32, 64, 64), (8192, 8, 32, 128, 256)])
+def test_workspace_without_g_serves_every_decay(T, H, HV, K, V):
+    """Asked before the tensors exist, the size covers a decay per token and one per head."""
+    import ctypes
+    L = B.lib()
+
+    def need(**kw):
+        a = B.LinattnArgs(B=1, T=T, H=H, HV=HV, K=K, V=V, dtype=B.GDP_BF16, **kw)
+        return L.gdp_linattn_workspace_bytes(ctypes.byref(a), 1)
+
+    before, token, head = need(), need(g=0x1000), need(g_head=0x1000)
+    assert before == head >= token > 0
+    assert need(h0=0x1000) > before
