@@ -104,6 +104,71 @@ class GroupNormGrads(ctypes.Structure):
     ]
 
 
+class LinrecArgs(ctypes.Structure):
+    """Mirror of gdp_linrec_args (include/gdp.h)."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("C", _i32), ("dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+        ("decay", ctypes.c_int), ("complement", _i32), ("cu_seqlens", _vp), ("num_seqs", _i64),
+        ("x", _vp), ("x_b_stride", _i64), ("x_t_stride", _i64), ("g", _vp), ("g_b_stride", _i64), ("g_t_stride", _i64),
+        ("h0", _vp), ("y", _vp), ("ht", _vp),
+    ]
+
+
+class LinrecGrads(ctypes.Structure):
+    """Mirror of gdp_linrec_grads (include/gdp.h)."""
+    _fields_ = [
+        ("dy", _vp), ("dy_b_stride", _i64), ("dy_t_stride", _i64), ("dht", _vp), ("dx", _vp), ("dg", _vp), ("dh0", _vp),
+    ]
+
+
+class LinrecDecodeArgs(ctypes.Structure):
+    """Mirror of gdp_linrec_decode_args (include/gdp.h)."""
+    _fields_ = [
+        ("n", _i64), ("S", _i64), ("C", _i32), ("dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+        ("decay", ctypes.c_int), ("complement", _i32), ("pool", _i64),
+        ("x", _vp), ("x_n_stride", _i64), ("x_t_stride", _i64), ("g", _vp), ("g_n_stride", _i64), ("g_t_stride", _i64),
+        ("state", _vp), ("slots", _vp), ("y", _vp),
+    ]
+
+
+class ConvArgs(ctypes.Structure):
+    """Mirror of gdp_conv_args (include/gdp.h)."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("C", _i32), ("W", _i32), ("dtype", ctypes.c_int), ("activation", ctypes.c_int),
+        ("cu_seqlens", _vp), ("num_seqs", _i64), ("x", _vp), ("x_b_stride", _i64), ("x_t_stride", _i64),
+        ("w", _vp), ("b", _vp), ("h0", _vp), ("y", _vp), ("ht", _vp),
+    ]
+
+
+class ConvGrads(ctypes.Structure):
+    """Mirror of gdp_conv_grads (include/gdp.h)."""
+    _fields_ = [
+        ("dy", _vp), ("dy_b_stride", _i64), ("dy_t_stride", _i64), ("dht", _vp), ("dx", _vp), ("dw", _vp), ("db", _vp),
+        ("dh0", _vp),
+    ]
+
+
+class ConvDecodeArgs(ctypes.Structure):
+    """Mirror of gdp_conv_decode_args (include/gdp.h)."""
+    _fields_ = [
+        ("n", _i64), ("S", _i64), ("C", _i32), ("W", _i32), ("dtype", ctypes.c_int), ("activation", ctypes.c_int),
+        ("pool", _i64), ("x", _vp), ("x_n_stride", _i64), ("x_t_stride", _i64), ("w", _vp), ("b", _vp),
+        ("state", _vp), ("slots", _vp), ("y", _vp),
+    ]
+
+
+class RotaryArgs(ctypes.Structure):
+    """Mirror of gdp_rotary_args (include/gdp.h)."""
+    _fields_ = [
+        ("B", _i64), ("T", _i64), ("H", _i32), ("HK", _i32), ("D", _i32), ("R", _i32), ("dtype", ctypes.c_int),
+        ("interleaved", _i32), ("inverse", _i32), ("scale", _f32), ("cu_seqlens", _vp), ("num_seqs", _i64),
+        ("positions", _vp), ("pos_b_stride", _i64), ("pos_t_stride", _i64), ("offsets", _vp), ("freq", _vp),
+        ("q", _vp), ("q_b_stride", _i64), ("q_t_stride", _i64), ("k", _vp), ("k_b_stride", _i64), ("k_t_stride", _i64),
+        ("qo", _vp), ("qo_b_stride", _i64), ("qo_t_stride", _i64), ("ko", _vp), ("ko_b_stride", _i64),
+        ("ko_t_stride", _i64),
+    ]
+
+
 class GdpError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__("gdp status %d: %s" % (status, msg))
@@ -171,6 +236,24 @@ def lib():
         L.gdp_group_norm_workspace_bytes.argtypes = [ctypes.POINTER(GroupNormArgs)]
         L.gdp_group_norm_bwd.restype = ctypes.c_int
         L.gdp_group_norm_bwd.argtypes = [ctypes.POINTER(GroupNormArgs), ctypes.POINTER(GroupNormGrads), _vp, _i64, _vp]
+        L.gdp_linrec_workspace_bytes.restype = _i64
+        L.gdp_linrec_workspace_bytes.argtypes = [ctypes.POINTER(LinrecArgs), _i32]
+        L.gdp_linrec_fwd.restype = ctypes.c_int
+        L.gdp_linrec_fwd.argtypes = [ctypes.POINTER(LinrecArgs), _vp, _i64, _vp]
+        L.gdp_linrec_bwd.restype = ctypes.c_int
+        L.gdp_linrec_bwd.argtypes = [ctypes.POINTER(LinrecArgs), ctypes.POINTER(LinrecGrads), _vp, _i64, _vp]
+        L.gdp_linrec_decode.restype = ctypes.c_int
+        L.gdp_linrec_decode.argtypes = [ctypes.POINTER(LinrecDecodeArgs), _vp]
+        L.gdp_conv_fwd.restype = ctypes.c_int
+        L.gdp_conv_fwd.argtypes = [ctypes.POINTER(ConvArgs), _vp]
+        L.gdp_conv_workspace_bytes.restype = _i64
+        L.gdp_conv_workspace_bytes.argtypes = [ctypes.POINTER(ConvArgs)]
+        L.gdp_conv_bwd.restype = ctypes.c_int
+        L.gdp_conv_bwd.argtypes = [ctypes.POINTER(ConvArgs), ctypes.POINTER(ConvGrads), _vp, _i64, _vp]
+        L.gdp_conv_decode.restype = ctypes.c_int
+        L.gdp_conv_decode.argtypes = [ctypes.POINTER(ConvDecodeArgs), _vp]
+        L.gdp_rotary.restype = ctypes.c_int
+        L.gdp_rotary.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
         L.gdp_last_error.restype = ctypes.c_char_p
         L.gdp_last_error.argtypes = []
         L.gdp_version.restype = ctypes.c_char_p
@@ -870,3 +953,296 @@ def group_norm_bwd(dy, x, groups, weight=None, bias=None, gate=None, activation=
     ws = _workspace(need, dev)
     _call(dev, L.gdp_group_norm_bwd, pa, ctypes.byref(d), _at(ws), need)
     return dx, dz, dw, db
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+
+DECAYS = {"log": 0, "sigmoid": 1}
+
+
+def _channels(t, name, shape, dtypes):
+    """Checks a [n, T, C] tensor with a contiguous last dimension; its batch and token strides."""
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s is %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
+    s = t.stride()
+    if s[2] != 1 and shape[2] > 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return s[0], s[1]
+
+
+def _sequences(cu_seqlens, B):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    _contig(cu_seqlens, "cu_seqlens")
+    return cu_seqlens.numel() - 1
+
+
+def _state_of(t, name, shape, dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s %s" % (name, dtype, list(shape)))
+
+
+def _slots_of(slots, n):
+    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (n,) or not slots.is_contiguous()):
+        raise ValueError("slots must be a contiguous int32 [n]")
+
+
+def _rec_input(x, g, decay):
+    if x.dim() != 3:
+        raise ValueError("x must be 3-D")
+    if decay not in DECAYS:
+        raise ValueError("decay must be one of %s" % sorted(DECAYS))
+    code = _dtype_code(x.dtype)
+    return code, _channels(x, "x", x.shape, (x.dtype,)), _channels(g, "g", x.shape, (x.dtype, torch.float32))
+
+
+def _rec_args(x, g, decay, complement, cu_seqlens, initial_state):
+    code, xs, gs = _rec_input(x, g, decay)
+    B, T, C = x.shape
+    nseq = _sequences(cu_seqlens, B)
+    _state_of(initial_state, "initial_state", (nseq, C), torch.float32)
+    return nseq, LinrecArgs(B, T, C, code, _dtype_code(g.dtype), DECAYS[decay], 1 if complement else 0,
+                            _at(cu_seqlens), nseq, x.data_ptr(), xs[0], xs[1], g.data_ptr(), gs[0], gs[1],
+                            _at(initial_state))
+
+
+def linrec_fwd(x, g, decay="log", complement=False, cu_seqlens=None, initial_state=None, output_final_state=False,
+               y=None):
+    """gdp_linrec_fwd: the gated linear recurrence h_t = a_t h_{t-1} + c_t x_t, y_t = h_t, a state of one number per
+    channel.
+
+    x [B, T, C] (bf16 or f32; tokens and batch rows may be strided); g [B, T, C] of that dtype or float32: a = e^g
+    (decay="log") or 1 / (1 + e^-g) (decay="sigmoid"); c is 1, or 1 - a with complement=True; cu_seqlens int32
+    [num_seqs + 1] (B == 1) or None; initial_state [nseq, C] float32 or None.  ``y`` may hold a preallocated contiguous
+    output, also x itself, or g.  Returns (y [B, T, C], ht [nseq, C] float32 or None).  Rows of y outside every request
+    are not written: they keep what ``y`` held, or are uninitialised.  Nothing is recorded for autograd; the gradients
+    come from linrec_bwd."""
+    dev = _need_cuda(x, g, cu_seqlens, initial_state, y)
+    nseq, a = _rec_args(x, g, decay, complement, cu_seqlens, initial_state)
+    y = _output(y, "y", x.shape, x.dtype, dev)
+    a.y = y.data_ptr()
+    ht = None
+    if output_final_state:
+        ht = torch.empty((nseq, a.C), dtype=torch.float32, device=dev)
+        a.ht = ht.data_ptr()
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_linrec_workspace_bytes(pa, 0)
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_linrec_fwd, pa, _at(ws), need)
+    return y, ht
+
+
+def linrec_bwd(dy, x, g, decay="log", complement=False, cu_seqlens=None, initial_state=None, dht=None):
+    """gdp_linrec_bwd: the gradients of linrec_fwd for those of y (dy, shaped as x, strided) and of ht (dht, or None).
+    Returns (dx, dg, dh0): dx and dg as x and g, contiguous, zero in rows outside every request; dh0 [nseq, C] float32
+    (None without initial_state)."""
+    dev = _need_cuda(x, g, cu_seqlens, initial_state, dy, dht)
+    nseq, a = _rec_args(x, g, decay, complement, cu_seqlens, initial_state)
+    ds = _channels(dy, "dy", x.shape, (x.dtype,))
+    _state_of(dht, "dht", (nseq, a.C), torch.float32)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    dh0 = None if initial_state is None else torch.empty_like(initial_state)
+    d = LinrecGrads(dy.data_ptr(), ds[0], ds[1], _at(dht), dx.data_ptr(), dg.data_ptr(), _at(dh0))
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_linrec_workspace_bytes(pa, 1)
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_linrec_bwd, pa, ctypes.byref(d), _at(ws), need)
+    return dx, dg, dh0
+
+
+def linrec_decode(x, g, state, decay="log", complement=False, slots=None, y=None):
+    """gdp_linrec_decode: S new tokens of each request through the recurrence of linrec_fwd.  x, g [n, S, C] (strided
+    as there); state [pool, C] float32, updated in place; slots int32 [n] (outside [0, pool): skipped, its y rows zero)
+    or None.  Returns y [n, S, C].  It has no gradients."""
+    dev = _need_cuda(x, g, state, slots, y)
+    code, xs, gs = _rec_input(x, g, decay)
+    n, S, C = x.shape
+    pool = state.shape[0] if state.dim() else 0
+    _state_of(state, "state", (pool, C), torch.float32)
+    _slots_of(slots, n)
+    y = _output(y, "y", x.shape, x.dtype, dev)
+    a = LinrecDecodeArgs(n, S, C, code, _dtype_code(g.dtype), DECAYS[decay], 1 if complement else 0, pool, x.data_ptr(),
+                         xs[0], xs[1], g.data_ptr(), gs[0], gs[1], state.data_ptr(), _at(slots), y.data_ptr())
+    _call(dev, lib().gdp_linrec_decode, ctypes.byref(a))
+    return y
+
+
+# ------------------------------------------------------------------ short causal convolution
+
+def _taps(weight, bias, C):
+    if weight.dim() != 2 or weight.shape[0] != C or weight.dtype != torch.float32 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 [C, W]")
+    if bias is not None and (bias.shape != (C,) or bias.dtype != torch.float32 or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 [C]")
+    return weight.shape[1]
+
+
+def _activation(name):
+    act = ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError("activation must be one of %s" % sorted(k for k in ACTIVATIONS if k))
+    return act
+
+
+def _conv_args(x, weight, bias, activation, cu_seqlens, initial_state):
+    if x.dim() != 3:
+        raise ValueError("x must be 3-D")
+    B, T, C = x.shape
+    act, W = _activation(activation), _taps(weight, bias, C)
+    xs = _channels(x, "x", x.shape, (x.dtype,))
+    nseq = _sequences(cu_seqlens, B)
+    _state_of(initial_state, "initial_state", (nseq, W - 1, C), x.dtype)
+    return nseq, ConvArgs(B, T, C, W, _dtype_code(x.dtype), act, _at(cu_seqlens), nseq, x.data_ptr(), xs[0], xs[1],
+                          weight.data_ptr(), _at(bias), _at(initial_state))
+
+
+def conv_fwd(x, weight, bias=None, activation="silu", cu_seqlens=None, initial_state=None, output_final_state=False,
+             y=None):
+    """gdp_conv_fwd: the short causal convolution in front of a mixer, y_t = act(bias + sum_j weight[:, j]
+    x_{t-W+1+j}), depthwise and channels last.
+
+    x [B, T, C] (bf16 or f32; tokens and batch rows may be strided); weight [C, W] float32, W 2 to 4; bias [C] float32
+    or None; activation "silu", "sigmoid" or "none"; cu_seqlens int32 [num_seqs + 1] (B == 1) or None; initial_state
+    [nseq, W - 1, C] of x's dtype, the inputs before each sequence, oldest first, or None (zeros).  ``y`` may hold a
+    preallocated contiguous output that does not overlap x.  Returns (y [B, T, C], ht [nseq, W - 1, C] or None); rows of
+    y outside every request are not written.  Nothing is recorded for autograd; the gradients come from conv_bwd."""
+    dev = _need_cuda(x, weight, bias, cu_seqlens, initial_state, y)
+    nseq, a = _conv_args(x, weight, bias, activation, cu_seqlens, initial_state)
+    y = _output(y, "y", x.shape, x.dtype, dev)
+    a.y = y.data_ptr()
+    ht = None
+    if output_final_state:
+        ht = torch.empty((nseq, max(a.W - 1, 0), a.C), dtype=x.dtype, device=dev)
+        a.ht = ht.data_ptr()
+    _call(dev, lib().gdp_conv_fwd, ctypes.byref(a))
+    return y, ht
+
+
+def conv_bwd(dy, x, weight, bias=None, activation="silu", cu_seqlens=None, initial_state=None, dht=None):
+    """gdp_conv_bwd: the gradients of conv_fwd for those of y (dy, shaped as x, strided) and of ht (dht, or None).
+    Returns (dx, dweight, dbias, dh0): dx as x, contiguous, zero in rows outside every request; dweight [C, W] and dbias
+    [C] float32 (None without bias); dh0 [nseq, W - 1, C] (None without initial_state)."""
+    dev = _need_cuda(x, weight, bias, cu_seqlens, initial_state, dy, dht)
+    nseq, a = _conv_args(x, weight, bias, activation, cu_seqlens, initial_state)
+    ds = _channels(dy, "dy", x.shape, (x.dtype,))
+    _state_of(dht, "dht", (nseq, a.W - 1, a.C), x.dtype)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    dh0 = None if initial_state is None else torch.empty_like(initial_state)
+    d = ConvGrads(dy.data_ptr(), ds[0], ds[1], _at(dht), dx.data_ptr(), dw.data_ptr(), _at(db), _at(dh0))
+    L, pa = lib(), ctypes.byref(a)
+    need = L.gdp_conv_workspace_bytes(pa)
+    ws = _workspace(need, dev)
+    _call(dev, L.gdp_conv_bwd, pa, ctypes.byref(d), _at(ws), need)
+    return dx, dw, db, dh0
+
+
+def conv_decode(x, state, weight, bias=None, activation="silu", slots=None, y=None):
+    """gdp_conv_decode: S new tokens of each request through the convolution of conv_fwd.  x [n, S, C] (strided as
+    there); state [pool, W - 1, C] of x's dtype, updated in place; slots int32 [n] (outside [0, pool): skipped, its y
+    rows zero) or None.  Returns y [n, S, C] (``y`` may be x).  It has no gradients."""
+    dev = _need_cuda(x, weight, bias, state, slots, y)
+    if x.dim() != 3:
+        raise ValueError("x must be 3-D")
+    n, S, C = x.shape
+    act, W = _activation(activation), _taps(weight, bias, C)
+    xs = _channels(x, "x", x.shape, (x.dtype,))
+    pool = state.shape[0] if state.dim() else 0
+    _state_of(state, "state", (pool, W - 1, C), x.dtype)
+    _slots_of(slots, n)
+    y = _output(y, "y", x.shape, x.dtype, dev)
+    a = ConvDecodeArgs(n, S, C, W, _dtype_code(x.dtype), act, pool, x.data_ptr(), xs[0], xs[1], weight.data_ptr(),
+                       _at(bias), state.data_ptr(), _at(slots), y.data_ptr())
+    _call(dev, lib().gdp_conv_decode, ctypes.byref(a))
+    return y
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def rotary_freq(rotated, base=10000.0, scaling=None, factor=1.0, original_length=None, fast=32.0, slow=1.0,
+                device=None):
+    """Frequencies of rotary positions: (freq [rotated / 2] float64 in radians per position, scale of the outputs).
+
+    freq[i] = base^(-2i / rotated), for contexts of ``factor`` times the trained length changed by ``scaling``:
+      None      not at all
+      "linear"  positions pressed together: freq / factor
+      "base"    a larger base, so that the slowest pair is slowed by factor and the fastest not at all
+      "parts"   by what a pair turns over original_length positions: more than ``fast`` times stays, less than ``slow``
+                times is divided by factor, linear in the pair's index between; the scale is 0.1 ln(factor) + 1."""
+    if rotated < 2 or rotated % 2:
+        raise ValueError("rotated must be even and at least 2")
+    if not (base > 0 and factor >= 1):
+        raise ValueError("base must be above 0 and factor at least 1")
+    half = rotated // 2
+    i = torch.arange(half, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base" and half > 1:
+        base = base * factor ** (rotated / (rotated - 2))
+    freq = torch.exp(i * (-2.0 / rotated) * math.log(base))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "parts":
+        if not original_length or not fast > slow > 0:
+            raise ValueError("scaling by parts needs original_length and fast > slow > 0")
+
+        def index(turns):  # of the pair that turns so often over the original length
+            if base == 1:
+                raise ValueError("scaling by parts needs a base other than 1")
+            return rotated * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotated - 1)
+        part = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - part) + freq / factor * part
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base' or 'parts'")
+    return freq.to(device) if device is not None else freq, scale
+
+
+def rotary(q, k, freq, positions=None, offsets=None, cu_seqlens=None, interleaved=False, scale=1.0, inverse=False,
+           out=None):
+    """gdp_rotary: rotary positions of q [B, T, H, D] and k [B, T, HK, D] (k may be None; bf16 or f32, heads contiguous,
+    tokens and batch rows may be strided).  The first 2 len(freq) elements of a head are pairs, (i, i + len(freq)) or,
+    interleaved, (2i, 2i + 1), and pair i turns by position * freq[i] (freq float64, radians; see rotary_freq), times
+    scale.  A token's position is positions[b, t] (int32), or its place in its row or request of cu_seqlens plus
+    offsets[sequence] (int32 [nseq], or None: 0).  inverse=True turns back: given the gradients of the outputs it
+    returns those of q and k.  ``out`` may be (q', k') to write to, strided likewise, also (q, k) themselves.  Returns
+    (q', k'); rows outside every request are not written."""
+    dev = _need_cuda(q, k, freq, positions, offsets, cu_seqlens, *(out or ()))
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k must be 4-D")
+    B, T, H, D = q.shape
+    qs = _rows(q, "q", q.shape, q.dtype)
+    HK = 0 if k is None else k.shape[2]
+    ks = (0, 0) if k is None else _rows(k, "k", (B, T, HK, D), q.dtype)
+    if freq.dim() != 1 or freq.dtype != torch.float64 or not freq.is_contiguous():
+        raise ValueError("freq must be a contiguous float64 [R / 2]")
+    nseq = _sequences(cu_seqlens, B)
+    ps = (0, 0)
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape != (B, T):
+            raise ValueError("positions must be int32 [B, T]")
+        ps = positions.stride()
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (nseq,) or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 [nseq]")
+    if out is None:
+        qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+    else:
+        qo, ko = out
+        if (k is None) != (ko is None):
+            raise ValueError("out must hold an output for each input")
+    qos = _rows(qo, "out", q.shape, q.dtype)
+    kos = (0, 0) if k is None else _rows(ko, "out", k.shape, q.dtype)
+    a = RotaryArgs(B, T, H, HK, D, 2 * freq.shape[0], _dtype_code(q.dtype), 1 if interleaved else 0,
+                   1 if inverse else 0, scale, _at(cu_seqlens), nseq, _at(positions), ps[0], ps[1], _at(offsets),
+                   freq.data_ptr(), q.data_ptr(), qs[0], qs[1], _at(k), ks[0], ks[1], qo.data_ptr(), qos[0], qos[1],
+                   _at(ko), kos[0], kos[1])
+    _call(dev, lib().gdp_rotary, ctypes.byref(a))
+    return qo, ko

@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(HERE, "libgdp.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "prepare.hip", "wy.hip", "chunk_h.hip", "chunk_o.hip", "chunk_ho.hip", "decode.hip",
-           "scan.hip", "api_linattn.cpp", "linattn.hip", "lindecode.hip", "groupnorm.hip"]
+           "scan.hip", "api_linattn.cpp", "linattn.hip", "lindecode.hip", "groupnorm.hip",
+           "api_mixops.cpp", "linrec.hip", "shortconv.hip", "rotary.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -39,6 +39,15 @@ gdp_status hip_status(hipError_t e, const char *what) {
     return ok();
 }
 
+gdp_status check_space(const char *name, const void *ws, int64_t bytes, int64_t need) {
+    if (need == 0) return ok();
+    if (!ws) return fail(GDP_ERR_INVALID, "%s: workspace is NULL", name);
+    if ((uintptr_t)ws & (kAlign - 1)) return fail(GDP_ERR_INVALID, "%s: workspace is not 256-byte aligned", name);
+    if (bytes < need)
+        return fail(GDP_ERR_INVALID, "%s: workspace of %lld bytes, %lld needed", name, (long long)bytes, (long long)need);
+    return ok();
+}
+
 }  // namespace api
 }  // namespace gdp
 

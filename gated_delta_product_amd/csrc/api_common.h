@@ -20,6 +20,9 @@ inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Whether a launch of so many threads along x is allowed (HIP: under 2^32).
 inline bool fits_launch(int64_t threads) { return threads <= 0xffffffffll; }
+constexpr int64_t kAlign = 256;  // of a workspace and of the arrays in it
+// A workspace of `bytes` where `need` (0: none) are used.
+gdp_status check_space(const char *name, const void *ws, int64_t bytes, int64_t need);
 inline size_t dsize(gdp_dtype d) { return d == GDP_BF16 ? 2 : 4; }
 
 }  // namespace api

@@ -14,7 +14,6 @@ using namespace gdp::api;
 
 namespace {
 
-constexpr int64_t kAlign = 256;
 int64_t round_up(int64_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Consecutive arrays of a workspace.
@@ -188,15 +187,6 @@ gdp_status check_linattn(const char *name, const gdp_linattn_args *a, bool forwa
     if ((st = check_rows(name, "k", a->k, a->k_b_stride, a->k_t_stride, a->B, a->T, (int64_t)a->H * a->K, a->dtype)) != GDP_OK) return st;
     if ((st = check_rows(name, "v", a->v, a->v_b_stride, a->v_t_stride, a->B, a->T, (int64_t)a->HV * a->V, a->dtype)) != GDP_OK) return st;
     if (forward && (!a->o || !aligned16(a->o))) return fail(GDP_ERR_INVALID, "%s: o is NULL or not 16-byte aligned", name);
-    return ok();
-}
-
-gdp_status check_space(const char *name, const void *ws, int64_t bytes, int64_t need) {
-    if (need == 0) return ok();
-    if (!ws) return fail(GDP_ERR_INVALID, "%s: workspace is NULL", name);
-    if ((uintptr_t)ws & (kAlign - 1)) return fail(GDP_ERR_INVALID, "%s: workspace is not 256-byte aligned", name);
-    if (bytes < need)
-        return fail(GDP_ERR_INVALID, "%s: workspace of %lld bytes, %lld needed", name, (long long)bytes, (long long)need);
     return ok();
 }
 

@@ -1,0 +1,72 @@
+// mixops.h -- launcher interface of linrec.hip, shortconv.hip and rotary.hip
+// (host side, and the parameters their kernels take).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdp.h"
+
+namespace gdp {
+
+// The sequences of rows [B*T]: B of T rows each, or with cu (B == 1, T = rows)
+// the nseq packed requests.
+struct RowMap {
+    const int32_t *cu;
+    uint32_t T, rows;
+    int nseq;
+};
+
+// [B, T, C]: element (b, t, c) at p + b*bs + t*ts + c
+struct Strided {
+    const void *p;
+    int64_t bs, ts;
+};
+
+struct LinRec {
+    RowMap m;
+    Strided x, g, dy;
+    int C;
+    bool vec;  // every row of every tensor starts on 16 bytes, C in whole units
+    bool g32, sigmoid, complement;
+    int lognx, tiles;  // set at launch
+    const float *h0, *dht;
+    void *y, *dx, *dg;
+    float *ht, *dh0;
+    void *space;
+};
+int64_t linrec_space(const LinRec &p, gdp_dtype dtype, bool backward);
+bool linrec_fits(const LinRec &p, gdp_dtype dtype, bool backward);
+hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_linrec_decode(const gdp_linrec_decode_args &a, bool vec, hipStream_t stream);
+
+struct ShortConv {
+    RowMap m;
+    Strided x, dy;
+    int C, W, act;
+    bool vec;
+    int lognx, tiles;  // set at launch
+    const float *w, *b;
+    const void *h0, *dht;  // [nseq, W - 1, C]
+    void *y, *ht, *dx, *dh0;
+    float *dw, *db, *part;
+};
+int64_t conv_space(const ShortConv &p, gdp_dtype dtype);
+bool conv_fits(const ShortConv &p, gdp_dtype dtype, bool backward);
+hipError_t launch_conv(ShortConv p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_conv_bwd(ShortConv p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_conv_decode(const gdp_conv_decode_args &a, bool vec, hipStream_t stream);
+
+struct Rotary {
+    RowMap m;
+    Strided in[2], out[2];
+    int H[2], D, R;
+    bool interleaved, inverse, vec;
+    float scale;
+    const int32_t *positions, *offsets;
+    int64_t pos_bs, pos_ts;
+    const double *freq;
+};
+hipError_t launch_rotary(const Rotary &p, gdp_dtype dtype, hipStream_t stream);
+
+}  // namespace gdp

@@ -41,6 +41,15 @@
  *   gdp_group_norm_fwd   the norm per head with an activation or a gate that
  *                        follows either mixer, channels last
  *   gdp_group_norm_bwd   its gradients
+ *   gdp_linrec_fwd       gated linear recurrence, a state of one number per
+ *                        channel, prompts and packed requests
+ *   gdp_linrec_bwd       its gradients
+ *   gdp_linrec_decode    its recurrent form over a state pool
+ *   gdp_conv_fwd         the short causal convolution in front of a mixer
+ *                        (the post-conv activations of gdp_prefill_prepare)
+ *   gdp_conv_bwd         its gradients
+ *   gdp_conv_decode      its form for new tokens over a state pool
+ *   gdp_rotary           rotary positions of queries and keys, and back
  *
  * Conventions shared by every entry point
  *   * All tensor pointers are device pointers owned by the caller.  No call
@@ -722,6 +731,266 @@ int64_t gdp_group_norm_workspace_bytes(const gdp_group_norm_args *a);
 /* y of a is not used.  workspace: 256-byte aligned, caller-owned. */
 gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm_grads *d, void *workspace,
                               int64_t workspace_bytes, void *stream);
+
+/*
+ * Gated linear recurrence, a state of one number per channel:
+ *   h_t = a_t h_{t-1} + c_t x_t,   y_t = h_t
+ * over the sequences of gdp_linattn_args: B rows of T tokens, or (B == 1) the
+ * packed requests of cu_seqlens.
+ *   x      [B, T, C] dtype; element (b, t, c) at x + b*x_b_stride +
+ *          t*x_t_stride + c (strides in elements, >= 0)
+ *   g      [B, T, C] g_dtype (dtype, or float32), strided likewise: the decay
+ *          of every token and channel, by `decay`
+ *            GDP_DECAY_LOG      a = e^g  (-inf: the state before is dropped)
+ *            GDP_DECAY_SIGMOID  a = 1 / (1 + e^-g)
+ *   complement  0: c = 1;  else c = 1 - a
+ *   h0     [nseq, C] float32 state before each sequence, or NULL (0)
+ *   y      [B, T, C] dtype, contiguous; tokens outside every request are left
+ *          as they were.  May be x, or g of that dtype, where those are
+ *          contiguous too.
+ *   ht     [nseq, C] float32 state after each sequence, or NULL (h0, or zero,
+ *          for an empty one).  May be h0.
+ * States are float32 and y is rounded once; 1 - a is formed without
+ * cancellation.  Inputs must be finite but for a log decay of -inf; others
+ * reach only later rows of their channel and sequence.
+ * Sizes: C <= 2^20, B*T < 2^31; a call that would launch 2^32 threads at once
+ * is GDP_ERR_UNSUPPORTED.
+ */
+typedef enum gdp_decay {
+    GDP_DECAY_LOG = 0,
+    GDP_DECAY_SIGMOID = 1
+} gdp_decay;
+
+typedef struct gdp_linrec_args {
+    int64_t B;
+    int64_t T;
+    int32_t C;
+    gdp_dtype dtype;
+    gdp_dtype g_dtype;
+    gdp_decay decay;
+    int32_t complement;
+    const int32_t *cu_seqlens;
+    int64_t num_seqs;
+    const void *x;
+    int64_t x_b_stride;
+    int64_t x_t_stride;
+    const void *g;
+    int64_t g_b_stride;
+    int64_t g_t_stride;
+    const float *h0;
+    void *y;
+    float *ht;
+} gdp_linrec_args;
+
+/* Gradients of gdp_linrec_fwd for those of y (dy [B, T, C] dtype, strided) and
+ * of ht (dht [nseq, C] float32, or NULL: zero):
+ *   dx     [B, T, C] dtype, dg [B, T, C] g_dtype, contiguous; zero for tokens
+ *          outside every request, whose dy is not used
+ *   dh0    [nseq, C] float32, or NULL
+ * No output may overlap an input. */
+typedef struct gdp_linrec_grads {
+    const void *dy;
+    int64_t dy_b_stride;
+    int64_t dy_t_stride;
+    const float *dht;
+    void *dx;
+    void *dg;
+    float *dh0;
+} gdp_linrec_grads;
+
+/* Device workspace in bytes of gdp_linrec_fwd (backward == 0) or gdp_linrec_bwd
+ * (0: none); -1 on bad sizes.  Only the sizes and dtypes count, not the
+ * pointers, so it can be asked before the tensors exist. */
+int64_t gdp_linrec_workspace_bytes(const gdp_linrec_args *a, int32_t backward);
+/* workspace: gdp_linrec_workspace_bytes bytes, 256-byte aligned, caller-owned;
+ * its contents do not matter and are not kept.  Calls that may overlap in time
+ * need one each. */
+gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t workspace_bytes, void *stream);
+/* y, ht and the output pointers of a are not used. */
+gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, void *workspace,
+                          int64_t workspace_bytes, void *stream);
+
+/*
+ * gdp_linrec_decode -- S new tokens of each of n requests through the same
+ * recurrence, the state of a request in its slot of a pool:
+ *   x, g   [n, S, C], strided as above
+ *   state  [pool, C] float32, read and written in place
+ *   slots  int32 [n] device: the state slot of each request, or NULL (slot i
+ *          for request i).  A slot outside [0, pool) -- e.g. -1 for a padding
+ *          entry -- skips the request: no state is touched and its y rows are
+ *          zero.  Slots of one call must be distinct.
+ *   y      [n, S, C] dtype, contiguous
+ * Sizes: C <= 2^20, S <= 4096, n*C < 2^32.
+ */
+typedef struct gdp_linrec_decode_args {
+    int64_t n;
+    int64_t S;
+    int32_t C;
+    gdp_dtype dtype;
+    gdp_dtype g_dtype;
+    gdp_decay decay;
+    int32_t complement;
+    int64_t pool;
+    const void *x;
+    int64_t x_n_stride;
+    int64_t x_t_stride;
+    const void *g;
+    int64_t g_n_stride;
+    int64_t g_t_stride;
+    float *state;
+    const int32_t *slots;
+    void *y;
+} gdp_linrec_decode_args;
+
+gdp_status gdp_linrec_decode(const gdp_linrec_decode_args *a, void *stream);
+
+/*
+ * Short causal convolution, depthwise and channels last, with an activation:
+ *   u_t = b + sum_j w[c][j] x_{t-W+1+j},   y_t = act(u_t)
+ * over the sequences of gdp_linrec_args; the rows before a sequence are those
+ * of its state, the W - 1 inputs before it, oldest first.
+ *   x      [B, T, C] dtype, strided as above
+ *   w      [C, W] float32;  b [C] float32, or NULL (0)
+ *   h0     [nseq, W - 1, C] dtype state before each sequence, or NULL (zeros)
+ *   y      [B, T, C] dtype, contiguous, not overlapping x; tokens outside
+ *          every request are left as they were
+ *   ht     [nseq, W - 1, C] dtype state after each sequence (rows of a
+ *          sequence shorter than W - 1 follow those of h0), or NULL.  Not h0.
+ * Sums are float32, the output is rounded once; states are copies.
+ * Sizes: W in {2, 3, 4}, C <= 2^20, B*T < 2^31, launches as above.
+ */
+typedef struct gdp_conv_args {
+    int64_t B;
+    int64_t T;
+    int32_t C;
+    int32_t W;
+    gdp_dtype dtype;
+    gdp_activation activation;
+    const int32_t *cu_seqlens;
+    int64_t num_seqs;
+    const void *x;
+    int64_t x_b_stride;
+    int64_t x_t_stride;
+    const float *w;
+    const float *b;
+    const void *h0;
+    void *y;
+    void *ht;
+} gdp_conv_args;
+
+/* Gradients of gdp_conv_fwd for those of y (dy [B, T, C] dtype, strided) and of
+ * ht (dht [nseq, W - 1, C] dtype, or NULL: zero):
+ *   dx     [B, T, C] dtype, contiguous; zero for tokens outside every request
+ *   dw     [C, W] float32, db [C] float32, each or both NULL (not wanted)
+ *   dh0    [nseq, W - 1, C] dtype, or NULL
+ * No output may overlap an input. */
+typedef struct gdp_conv_grads {
+    const void *dy;
+    int64_t dy_b_stride;
+    int64_t dy_t_stride;
+    const void *dht;
+    void *dx;
+    float *dw;
+    float *db;
+    void *dh0;
+} gdp_conv_grads;
+
+gdp_status gdp_conv_fwd(const gdp_conv_args *a, void *stream);
+/* Device workspace of gdp_conv_bwd for dw and db (where neither is wanted any
+ * size passes); -1 on bad sizes. */
+int64_t gdp_conv_workspace_bytes(const gdp_conv_args *a);
+/* y and ht of a are not used.  workspace: 256-byte aligned, caller-owned. */
+gdp_status gdp_conv_bwd(const gdp_conv_args *a, const gdp_conv_grads *d, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/*
+ * gdp_conv_decode -- S new tokens of each of n requests through the same
+ * convolution, the W - 1 inputs before them in their slot of a pool:
+ *   x      [n, S, C] dtype, strided;  y [n, S, C] dtype, contiguous (may be x
+ *          where that is contiguous too)
+ *   state  [pool, W - 1, C] dtype, oldest row first, read and written in place
+ *   slots  as gdp_linrec_decode: a slot outside [0, pool) touches no state and
+ *          its y rows are zero.
+ * Sizes: W in {2, 3, 4}, C <= 2^20, S <= 4096, n*C < 2^32.
+ */
+typedef struct gdp_conv_decode_args {
+    int64_t n;
+    int64_t S;
+    int32_t C;
+    int32_t W;
+    gdp_dtype dtype;
+    gdp_activation activation;
+    int64_t pool;
+    const void *x;
+    int64_t x_n_stride;
+    int64_t x_t_stride;
+    const float *w;
+    const float *b;
+    void *state;
+    const int32_t *slots;
+    void *y;
+} gdp_conv_decode_args;
+
+gdp_status gdp_conv_decode(const gdp_conv_decode_args *a, void *stream);
+
+/*
+ * gdp_rotary -- rotary positions.  The first R elements of every head are
+ * pairs (u, v), the elements (i, i + R/2), or interleaved (2i, 2i + 1), and
+ * pair i turns by the angle position * freq[i]:
+ *   (u, v) -> scale (u cos - v sin, u sin + v cos)
+ * The elements from R on are copied.  inverse != 0 turns by the negative angle,
+ * with the same scale: given the gradients of the outputs it returns those of
+ * the inputs.
+ *   q      [B, T, H, D] dtype; element (b, t, h, d) at q + b*q_b_stride +
+ *          t*q_t_stride + h*D + d.  k [B, T, HK, D] likewise, or NULL with
+ *          HK == 0.
+ *   qo, ko the outputs, with strides of their own (rows may not overlap).  An
+ *          output may be its input, with the same strides; otherwise no output
+ *          overlaps an input.
+ *   freq   [R/2] float64, radians per position (so a context is stretched by
+ *          smaller ones)
+ *   positions  int32 position of token (b, t) at positions + b*pos_b_stride +
+ *          t*pos_t_stride, or NULL: then a token's position is its place in
+ *          its sequence (a row of T tokens, or a request of cu_seqlens) plus
+ *          offsets[sequence] (int32 [nseq], or NULL: 0).  Not both.
+ * Tokens outside every request are left as they were.  Angles are formed in 64
+ * bits, so any position an int32 holds keeps float32 accuracy; outputs are
+ * rounded once.
+ * Sizes: 2 <= R <= D <= 4096, R even, (H + HK) D <= 2^24, B*T < 2^31.
+ */
+typedef struct gdp_rotary_args {
+    int64_t B;
+    int64_t T;
+    int32_t H;
+    int32_t HK;
+    int32_t D;
+    int32_t R;
+    gdp_dtype dtype;
+    int32_t interleaved;
+    int32_t inverse;
+    float scale;
+    const int32_t *cu_seqlens;
+    int64_t num_seqs;
+    const int32_t *positions;
+    int64_t pos_b_stride;
+    int64_t pos_t_stride;
+    const int32_t *offsets;
+    const double *freq;
+    const void *q;
+    int64_t q_b_stride;
+    int64_t q_t_stride;
+    const void *k;
+    int64_t k_b_stride;
+    int64_t k_t_stride;
+    void *qo;
+    int64_t qo_b_stride;
+    int64_t qo_t_stride;
+    void *ko;
+    int64_t ko_b_stride;
+    int64_t ko_t_stride;
+} gdp_rotary_args;
+
+gdp_status gdp_rotary(const gdp_rotary_args *a, void *stream);
 
 /* Message describing the last non-OK status of this thread ("" if none). */
 const char *gdp_last_error(void);
