@@ -57,19 +57,211 @@ __device__ __forceinline__ float step(float h, float d, float x) {
 struct Run {
     float A, B;
 };
-__device__ __forceinline__ float enter(Run r, float h) { return r.A < 0.f ? r.B : fmaf(r.A, h, r.B); }
+// Zeros come out as +0.
+__device__ __forceinline__ float enter(Run r, float h) { return (r.A < 0.f ? r.B : fmaf(r.A, h, r.B)) + 0.f; }
+// What r does after all
+__device__ __forceinline__ Run after(Run all, Run r) {
+    return {r.A < 0.f || all.A < 0.f ? -1.f : r.A * all.A, enter(r, all.B)};
+}
+
+// ---------------------------------------------------------------- tiles in order
+//
+// Tiles of a strip of channels hand the state on through words in the
+// workspace, cleared before the launch: P of a tile is its Run, H the state
+// after it.  A tile publishes P as soon as its rows are joined, takes the
+// nearest H before it whose successors' P are all there, enters those one
+// after the other, and publishes its own H.  Whichever H that is, the same
+// products and sums are formed in the same order, so the bits do not depend on
+// timing.  A value and its being there are one word, so nothing else has to be
+// ordered: a word of zeros is not there yet, and a zero is kept as -0.
+//
+// Tiles are numbered by a counter in the order in which blocks start, so every
+// tile before one that waits belongs to a block that runs already.
+typedef unsigned long long u64;
+struct Chain {
+    uint32_t *count;  // blocks that have started
+    u64 *P;           // [tiles][C]
+    uint32_t *H;      // [tiles][C]
+};
+constexpr int WINDOW = 8;  // tiles looked back at once
+constexpr int PATIENCE = 1 << 22;  // looks (seconds) before a tile gives up, with NaN
+
+__device__ __forceinline__ uint32_t not_zero(float x) { return x == 0.f ? 0x80000000u : __float_as_uint(x); }
+__device__ __forceinline__ void publish(u64 *at, Run r) {
+    __hip_atomic_store(at, (u64)__float_as_uint(r.B) << 32 | not_zero(r.A), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(uint32_t *at, float h) {
+    __hip_atomic_store(at, not_zero(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The state that enters the pos-th tile of its chain, for the channel of the
+// words P and H (its own); those of the tile before lie `back` further.
+__device__ __forceinline__ float entering(const u64 *P, const uint32_t *H, int64_t back, int pos) {
+    const int n = pos < WINDOW ? pos : WINDOW;
+    for (int look = 0; look < PATIENCE; ++look) {
+        uint32_t h[WINDOW];
+        u64 r[WINDOW];
+#pragma unroll
+        for (int k = 0; k < WINDOW; ++k) {
+            h[k] = 0;
+            r[k] = 0;
+            if (k < n) {
+                h[k] = __hip_atomic_load(H + (k + 1) * back, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                r[k] = __hip_atomic_load(P + (k + 1) * back, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        int at = -1;  // nearest state, -1: none yet
+        bool open = true;
+#pragma unroll
+        for (int k = 0; k < WINDOW; ++k) {
+            if (open && h[k]) at = k;
+            open = open && !h[k] && r[k];
+        }
+        if (at < 0 && open && n == pos) at = n;  // before the first tile nothing is there
+        if (at >= 0) {
+            float x = 0.f;
+#pragma unroll
+            for (int k = WINDOW; k >= 0; --k) {
+                if (k < WINDOW && k == at) x = __uint_as_float(h[k]) + 0.f;
+                if (k < at && k < WINDOW) x = enter({__uint_as_float((uint32_t)r[k]) + 0.f, __uint_as_float((uint32_t)(r[k] >> 32))}, x);
+            }
+            return x;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return __builtin_nanf("");
+}
+
+
+// A block's tile and strip of channels, and the tile's place in its chain: the
+// tiles from the first one on, or from the last one back.
+struct Turn {
+    int tile, strip, pos;
+};
+template <bool BACK>
+__device__ __forceinline__ Turn next_turn(const LinRec &p, uint32_t *count, int strips) {
+    __shared__ uint32_t id;
+    if (p.tiles > 1) {
+        if (threadIdx.x == 0) id = atomicAdd(count, 1u);
+        __syncthreads();
+    }
+    const uint32_t k = p.tiles > 1 ? __builtin_amdgcn_readfirstlane(id) : blockIdx.x;
+    Turn t;
+    t.pos = (int)(k / (uint32_t)strips);
+    t.strip = (int)(k - (uint32_t)t.pos * strips);
+    t.tile = BACK ? p.tiles - 1 - t.pos : t.pos;
+    return t;
+}
+
+// What the rows of a thread are: bit i for its i-th.
+template <int TT>
+struct Kinds {
+    uint32_t in = 0, first = 0, last = 0;
+    __device__ __forceinline__ Kinds(const uint8_t *code) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const uint32_t c = code[i];
+            in |= (c & ROW_IN) << i;
+            first |= (uint32_t)row_first(c) << i;
+            last |= (uint32_t)row_last(c) << i;
+        }
+    }
+};
+
+// A thread's rows from the first to the last: h <- a h + c x
+template <bool COMP, typename T, int E, int TT>
+__device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT], const float (&d)[TT][E], const Kinds<TT> &is,
+                                     const int *seq, const float *h0, int C, int col) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) run[e] = {1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        float x[E];
+        xr[i].to(x);
+        if (is.first >> i & 1) {
+            float h[E];
+            load_state<E>(h, h0, seq[i], C, col);
+#pragma unroll
+            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            run[e].B = step<COMP>(run[e].B, d[i][e], x[e]);
+            run[e].A = run[e].A < 0.f ? -1.f : keep(d[i][e], run[e].A);
+        }
+        if (!(is.in >> i & 1))
+#pragma unroll
+            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
+    }
+}
+// From the last to the first: m <- a (dy + m), the gradient of the state before the row
+template <typename T, int E, int TT>
+__device__ __forceinline__ void walk_back(Run (&run)[E], const Chans<T, E> (&dr)[TT], const float (&d)[TT][E],
+                                          const Kinds<TT> &is, const int *seq, const float *dht, int C, int col) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) run[e] = {1.f, 0.f};
+#pragma unroll
+    for (int i = TT - 1; i >= 0; --i) {
+        float dy[E];
+        dr[i].to(dy);
+        if (is.last >> i & 1) {
+            float h[E];
+            load_state<E>(h, dht, seq[i], C, col);
+#pragma unroll
+            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            run[e].B = keep(d[i][e], dy[e] + run[e].B);
+            run[e].A = run[e].A < 0.f ? -1.f : keep(d[i][e], run[e].A);
+        }
+        if (!(is.in >> i & 1))
+#pragma unroll
+            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
+    }
+}
+
+// The block's runs of every channel, joined in order, one thread a channel:
+// the tile's Run goes out, and rb holds the state that enters each run.
+template <bool BACK>
+__device__ __forceinline__ void join_runs(const float *ra, float *rb, int w, int ny, const Chain &ch, int64_t C, int tiles,
+                                          const Turn &t, int c, bool alone) {
+    const int k = threadIdx.x;
+    float h = 0.f;
+    u64 *P = ch.P + (int64_t)t.tile * C + c;
+    uint32_t *H = ch.H + (int64_t)t.tile * C + c;
+    if (tiles > 1) {
+        Run all{1.f, 0.f};
+        for (int i = 0; i < ny; ++i) {
+            const int y = BACK ? ny - 1 - i : i;
+            all = after(all, {ra[y * w + k], rb[y * w + k]});
+        }
+        if (alone) {  // nothing enters, so this is the state after the tile too
+            publish(H, all.B);
+        } else {
+            publish(P, all);
+            h = entering(P, H, BACK ? C : -C, t.pos);
+            publish(H, enter(all, h));
+        }
+    }
+    for (int i = 0; i < ny; ++i) {
+        const int y = BACK ? ny - 1 - i : i;
+        const Run r{ra[y * w + k], rb[y * w + k]};
+        rb[y * w + k] = h;
+        h = enter(r, h);
+    }
+}
 
 }  // namespace
 
-// PHASE 0: what each tile does to the state -> space [tiles][2][C];
-// PHASE 1: the rows.
-template <typename T, typename G, int E, int TT, bool COMP, int PHASE>
-__global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p) {
+// ROWS: y and the final states; without: only H, the state after every tile.
+template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
+__global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int strips) {
     __shared__ uint8_t code[LNT * TT];
     __shared__ int seq[LNT * TT];
     __shared__ float ra[LNT * E], rb[LNT * E];
-    const Place<LNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
-    const int w = at.nx * E;  // channels of the block
+    const Turn t = next_turn<false>(p, ch.count, strips);
+    const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
+    const int w = at.nx * E, k0 = at.ty * TT;  // channels of the block, the thread's rows in the tile
 
     Chans<T, E> xr[TT];
     Chans<G, E> gr[TT];
@@ -78,108 +270,67 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p) {
     find_rows<LNT>(p.m, at.tile0, at.ny * TT, code, seq);
     __syncthreads();
 
+    const Kinds<TT> is(code + k0);
     float d[TT][E];
-    uint32_t in = 0, first = 0, last = 0;
-    const int k0 = at.ty * TT;
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         gr[i].to(d[i]);
         decays<E>(d[i], p.sigmoid);
-        const uint32_t c = code[k0 + i];
-        in |= (c & ROW_IN) << i;
-        first |= (uint32_t)row_first(c) << i;
-        last |= (uint32_t)row_last(c) << i;
     }
-
     Run run[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) run[e] = {1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        float x[E];
-        xr[i].to(x);
-        if (first >> i & 1) {
-            float h[E];
-            load_state<E>(h, at.live ? p.h0 : nullptr, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            run[e].B = step<COMP>(run[e].B, d[i][e], x[e]);
-            if (run[e].A >= 0.f) run[e].A = keep(d[i][e], run[e].A);
-        }
-        if (!(in >> i & 1))
-#pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
-    }
+    walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         ra[at.ty * w + at.tx * E + e] = run[e].A;
         rb[at.ty * w + at.tx * E + e] = run[e].B;
     }
     __syncthreads();
-
-    // one thread a channel: its runs in order
-    const int c = (int)(blockIdx.y * w) + (int)threadIdx.x;
-    float *agg = (float *)p.space;
-    if ((int)threadIdx.x < w && c < p.C) {
-        if constexpr (PHASE == 0) {
-            Run all{1.f, 0.f};
-            for (int y = 0; y < at.ny; ++y) {
-                const float A = ra[y * w + threadIdx.x], B = rb[y * w + threadIdx.x];
-                all = {A < 0.f ? -1.f : all.A < 0.f ? -1.f : A * all.A, A < 0.f ? B : fmaf(A, all.B, B)};
-            }
-            agg[(int64_t)blockIdx.x * 2 * p.C + c] = all.A;
-            agg[(int64_t)blockIdx.x * 2 * p.C + p.C + c] = all.B;
-        } else {
-            float h = 0.f;
-            for (int64_t t = 0; t < (int64_t)blockIdx.x; ++t) h = enter({agg[t * 2 * p.C + c], agg[t * 2 * p.C + p.C + c]}, h);
-            for (int y = 0; y < at.ny; ++y) {
-                const Run r{ra[y * w + threadIdx.x], rb[y * w + threadIdx.x]};
-                rb[y * w + threadIdx.x] = h;
-                h = enter(r, h);
-            }
-        }
+    const int c = t.strip * w + (int)threadIdx.x;
+    if ((int)threadIdx.x < w && c < p.C)
+        join_runs<false>(ra, rb, w, at.ny, ch, p.C, p.tiles, t, c, row_first(code[0]) || !(code[0] & ROW_IN));
+    if constexpr (!ROWS) return;
+    __syncthreads();
+    if (!at.live) return;
+    float h[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) h[e] = rb[at.ty * w + at.tx * E + e];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        xr[i].forget();
+        forget(d[i]);
     }
-    if constexpr (PHASE == 1) {
-        __syncthreads();
-        if (!at.live) return;
-        float h[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = rb[at.ty * w + at.tx * E + e];
+    for (int i = 0; i < TT; ++i) {
+        if (!(is.in >> i & 1)) continue;
+        float x[E];
+        xr[i].to(x);
+        if (is.first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            if (!(in >> i & 1)) continue;
-            float x[E];
-            xr[i].to(x);
-            if (first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = step<COMP>(h[e], d[i][e], x[e]);
-            Chans<T, E> o;
-            o.from(h);
-            o.store((T *)p.y + (int64_t)(at.row0 + i) * p.C + at.col);
-            if (p.ht && (last >> i & 1)) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
-        }
-        if (p.ht && at.ty == 0)
-            for (int q = blockIdx.x; q < p.m.nseq; q += gridDim.x)
-                if (seq_empty(p.m, q)) {
-                    float z[E];
-                    load_state<E>(z, p.h0, q, p.C, at.col);
-                    store_state<E>(p.ht, q, p.C, at.col, z);
-                }
+        for (int e = 0; e < E; ++e) h[e] = step<COMP>(h[e], d[i][e], x[e]);
+        Chans<T, E> o;
+        o.from(h);
+        o.store((T *)p.y + (int64_t)(at.row0 + i) * p.C + at.col);
+        if (p.ht && (is.last >> i & 1)) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
     }
+    if (p.ht && at.ty == 0)
+        for (int q = t.tile; q < p.m.nseq; q += p.tiles)
+            if (seq_empty(p.m, q)) {
+                float z[E];
+                load_state<E>(z, p.h0, q, p.C, at.col);
+                store_state<E>(p.ht, q, p.C, at.col, z);
+            }
 }
 
-// Backwards.  PHASE 0: what each tile does to the state (forwards) and to a l
-// (from its last row to its first) -> space [tiles][4][C]; PHASE 1: the rows.
-template <typename T, typename G, int E, int TT, bool COMP, int PHASE>
-__global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p) {
+// The gradients, tiles from the last to the first; fwd holds the states after
+// the tiles (gdp_linrec_k without ROWS, in the same tiles).
+template <typename T, typename G, int E, int TT, bool COMP>
+__global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
     __shared__ uint8_t code[LNT * TT];
     __shared__ int seq[LNT * TT];
     __shared__ float ra[2][LNT * E], rb[2][LNT * E];
-    const Place<LNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
-    const int w = at.nx * E;
+    const Turn t = next_turn<true>(p, ch.count, strips);
+    const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
+    const int w = at.nx * E, k0 = at.ty * TT;
 
     Chans<T, E> xr[TT], dr[TT];
     Chans<G, E> gr[TT];
@@ -189,152 +340,99 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p) {
     find_rows<LNT>(p.m, at.tile0, at.ny * TT, code, seq);
     __syncthreads();
 
+    const Kinds<TT> is(code + k0);
     float d[TT][E];
-    uint32_t in = 0, first = 0, last = 0;
-    const int k0 = at.ty * TT;
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         gr[i].to(d[i]);
         decays<E>(d[i], p.sigmoid);
-        const uint32_t c = code[k0 + i];
-        in |= (c & ROW_IN) << i;
-        first |= (uint32_t)row_first(c) << i;
-        last |= (uint32_t)row_last(c) << i;
     }
-    Run run[E], back[E];
+    Run run[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) run[e] = back[e] = {1.f, 0.f};
+    for (int z = 0; z < 2; ++z) {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        float x[E];
-        xr[i].to(x);
-        if (first >> i & 1) {
-            float h[E];
-            load_state<E>(h, at.live ? p.h0 : nullptr, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
-        }
+        for (int i = 0; i < TT; ++i) forget(d[i]);
+        if (z) walk_back(run, dr, d, is, seq + k0, at.live ? p.dht : nullptr, p.C, at.col);
+        else walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = step<COMP>(run[e].B, d[i][e], x[e]);
-            if (run[e].A >= 0.f) run[e].A = keep(d[i][e], run[e].A);
+            ra[z][at.ty * w + at.tx * E + e] = run[e].A;
+            rb[z][at.ty * w + at.tx * E + e] = run[e].B;
         }
-        if (!(in >> i & 1))
+    }
+    __syncthreads();
+    const int c = t.strip * w + (int)threadIdx.x, n = at.ny * TT;
+    if ((int)threadIdx.x < w && c < p.C) {
+        float h = t.tile > 0 ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f;
+        for (int y = 0; y < at.ny; ++y) {
+            const Run r{ra[0][y * w + threadIdx.x], rb[0][y * w + threadIdx.x]};
+            rb[0][y * w + threadIdx.x] = h;
+            h = enter(r, h);
+        }
+        join_runs<true>(ra[1], rb[1], w, at.ny, ch, p.C, p.tiles, t, c, row_last(code[n - 1]) || !(code[n - 1] & ROW_IN));
+    }
+    __syncthreads();
+    if (!at.live) return;
+    float h[E], m[E], hp[TT][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
+    for (int e = 0; e < E; ++e) {
+        h[e] = rb[0][at.ty * w + at.tx * E + e];
+        m[e] = rb[1][at.ty * w + at.tx * E + e];
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        xr[i].forget();
+        dr[i].forget();
+        forget(d[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {  // hp: what da is l times
+        float x[E];
+        xr[i].to(x);
+        if (is.first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            hp[i][e] = COMP ? h[e] - x[e] : h[e];
+            h[e] = step<COMP>(h[e], d[i][e], x[e]);
+        }
     }
 #pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
-        float dy[E];
+        if (at.row0 + i >= p.m.rows) continue;
+        float dy[E], dx[E], dg[E];
         dr[i].to(dy);
-        if (last >> i & 1) {
-            float z[E];
-            load_state<E>(z, at.live ? p.dht : nullptr, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) back[e] = {-1.f, z[e]};
-        }
+        if (is.last >> i & 1) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float l = dy[e] + back[e].B;
-            back[e].B = keep(d[i][e], l);
-            if (back[e].A >= 0.f) back[e].A = keep(d[i][e], back[e].A);
+            const float l = dy[e] + m[e], al = keep(d[i][e], l), cl = rest(d[i][e]);
+            dx[e] = COMP ? cl * l : l;
+            dg[e] = hp[i][e] * (p.sigmoid ? cl * al : al);
+            m[e] = al;
         }
-        if (!(in >> i & 1))
+        if (!(is.in >> i & 1))
 #pragma unroll
-            for (int e = 0; e < E; ++e) back[e] = {-1.f, 0.f};
+            for (int e = 0; e < E; ++e) dx[e] = dg[e] = 0.f;
+        Chans<T, E> ox;
+        Chans<G, E> og;
+        ox.from(dx);
+        og.from(dg);
+        ox.store((T *)p.dx + (int64_t)(at.row0 + i) * p.C + at.col);
+        og.store((G *)p.dg + (int64_t)(at.row0 + i) * p.C + at.col);
+        if (p.dh0 && (is.first >> i & 1)) store_state<E>(p.dh0, seq[k0 + i], p.C, at.col, m);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int k = at.ty * w + at.tx * E + e;
-        ra[0][k] = run[e].A;
-        rb[0][k] = run[e].B;
-        ra[1][k] = back[e].A;
-        rb[1][k] = back[e].B;
-    }
-    __syncthreads();
-    const int c = (int)(blockIdx.y * w) + (int)threadIdx.x;
-    float *agg = (float *)p.space;
-    const int64_t C = p.C;
-    if ((int)threadIdx.x < w && c < p.C) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            if constexpr (PHASE == 0) {
-                Run all{1.f, 0.f};
-                for (int j = 0; j < at.ny; ++j) {
-                    const int y = z ? at.ny - 1 - j : j;
-                    const float A = ra[z][y * w + threadIdx.x], B = rb[z][y * w + threadIdx.x];
-                    all = {A < 0.f ? -1.f : all.A < 0.f ? -1.f : A * all.A, A < 0.f ? B : fmaf(A, all.B, B)};
-                }
-                agg[((int64_t)blockIdx.x * 4 + 2 * z) * C + c] = all.A;
-                agg[((int64_t)blockIdx.x * 4 + 2 * z + 1) * C + c] = all.B;
-            } else {
-                float h = 0.f;
-                if (z == 0)
-                    for (int64_t t = 0; t < (int64_t)blockIdx.x; ++t) h = enter({agg[t * 4 * C + c], agg[(t * 4 + 1) * C + c]}, h);
-                else
-                    for (int64_t t = (int64_t)gridDim.x - 1; t > (int64_t)blockIdx.x; --t)
-                        h = enter({agg[(t * 4 + 2) * C + c], agg[(t * 4 + 3) * C + c]}, h);
-                for (int j = 0; j < at.ny; ++j) {
-                    const int y = z ? at.ny - 1 - j : j;
-                    const Run r{ra[z][y * w + threadIdx.x], rb[z][y * w + threadIdx.x]};
-                    rb[z][y * w + threadIdx.x] = h;
-                    h = enter(r, h);
-                }
+    if (p.dh0 && at.ty == 0)
+        for (int q = t.tile; q < p.m.nseq; q += p.tiles)
+            if (seq_empty(p.m, q)) {
+                float z[E];
+                load_state<E>(z, p.dht, q, p.C, at.col);
+                store_state<E>(p.dh0, q, p.C, at.col, z);
             }
-        }
-    }
-    if constexpr (PHASE == 1) {
-        __syncthreads();
-        if (!at.live) return;
-        float h[E], m[E], hp[TT][E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            h[e] = rb[0][at.ty * w + at.tx * E + e];
-            m[e] = rb[1][at.ty * w + at.tx * E + e];
-        }
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {  // hp: what da is l times
-            float x[E];
-            xr[i].to(x);
-            if (first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                hp[i][e] = COMP ? h[e] - x[e] : h[e];
-                h[e] = step<COMP>(h[e], d[i][e], x[e]);
-            }
-        }
-#pragma unroll
-        for (int i = TT - 1; i >= 0; --i) {
-            if (at.row0 + i >= p.m.rows) continue;
-            float dy[E], dx[E], dg[E];
-            dr[i].to(dy);
-            if (last >> i & 1) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float l = dy[e] + m[e], al = keep(d[i][e], l), c = rest(d[i][e]);
-                dx[e] = COMP ? c * l : l;
-                dg[e] = hp[i][e] * (p.sigmoid ? c * al : al);
-                m[e] = al;
-            }
-            if (!(in >> i & 1))
-#pragma unroll
-                for (int e = 0; e < E; ++e) dx[e] = dg[e] = 0.f;
-            Chans<T, E> ox;
-            Chans<G, E> og;
-            ox.from(dx);
-            og.from(dg);
-            ox.store((T *)p.dx + (int64_t)(at.row0 + i) * p.C + at.col);
-            og.store((G *)p.dg + (int64_t)(at.row0 + i) * p.C + at.col);
-            if (p.dh0 && (first >> i & 1)) store_state<E>(p.dh0, seq[k0 + i], p.C, at.col, m);
-        }
-        if (p.dh0 && at.ty == 0)
-            for (int q = blockIdx.x; q < p.m.nseq; q += gridDim.x)
-                if (seq_empty(p.m, q)) {
-                    float z[E];
-                    load_state<E>(z, p.dht, q, p.C, at.col);
-                    store_state<E>(p.dh0, q, p.C, at.col, z);
-                }
-    }
+}
+
+// The workspace's words before a launch: none there yet.
+__global__ void __launch_bounds__(LNT) gdp_linrec_clear_k(uint4 *p, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * LNT + threadIdx.x;
+    if (i < n) p[i] = uint4{};
 }
 
 // S new tokens of a request, its state in registers between the load from its
@@ -393,17 +491,34 @@ int64_t tiles_of(const LinRec &p, gdp_dtype dtype, bool back) {
     return (p.m.rows + per - 1) / per;
 }
 
+// Words of a chain over `tiles`, whole units of 256 bytes: counter, P, H.
+int64_t chain_bytes(int64_t tiles, int64_t C) {
+    const int64_t n = tiles * C;
+    return 256 + (n * 12 + 255) / 256 * 256;
+}
+Chain chain_at(void *space, int64_t tiles, int64_t C) {
+    char *q = (char *)space;
+    return Chain{(uint32_t *)q, (u64 *)(q + 256), (uint32_t *)(q + 256 + tiles * C * 8)};
+}
+
 template <typename T, typename G, int E, bool COMP>
 hipError_t run_linrec(const LinRec &p, bool back, hipStream_t stream) {
-    const int w = E << p.lognx;
-    const dim3 grid((unsigned)(p.tiles > 0 ? p.tiles : 1), (unsigned)((p.C + w - 1) / w));
+    const int w = E << p.lognx, strips = (p.C + w - 1) / w;
+    const int64_t tiles = p.tiles, words = chain_bytes(tiles, p.C);
+    const dim3 grid((unsigned)(tiles * strips));
     constexpr int TF = rows_of(E, false), TB = rows_of(E, true);
+    Chain one{}, two{};
+    if (tiles > 1) {
+        one = chain_at(p.space, tiles, p.C);
+        if (back) two = chain_at((char *)p.space + words, tiles, p.C);
+        const int64_t n = (back ? 2 : 1) * words / 16;
+        hipLaunchKernelGGL(gdp_linrec_clear_k, dim3((unsigned)((n + LNT - 1) / LNT)), dim3(LNT), 0, stream, (uint4 *)p.space, n);
+    }
     if (back) {
-        if (p.tiles > 1) hipLaunchKernelGGL((gdp_linrec_bwd_k<T, G, E, TB, COMP, 0>), grid, dim3(LNT), 0, stream, p);
-        hipLaunchKernelGGL((gdp_linrec_bwd_k<T, G, E, TB, COMP, 1>), grid, dim3(LNT), 0, stream, p);
+        if (tiles > 1) hipLaunchKernelGGL((gdp_linrec_k<T, G, E, TB, COMP, false>), grid, dim3(LNT), 0, stream, p, one, strips);
+        hipLaunchKernelGGL((gdp_linrec_bwd_k<T, G, E, TB, COMP>), grid, dim3(LNT), 0, stream, p, one, two, strips);
     } else {
-        if (p.tiles > 1) hipLaunchKernelGGL((gdp_linrec_k<T, G, E, TF, COMP, 0>), grid, dim3(LNT), 0, stream, p);
-        hipLaunchKernelGGL((gdp_linrec_k<T, G, E, TF, COMP, 1>), grid, dim3(LNT), 0, stream, p);
+        hipLaunchKernelGGL((gdp_linrec_k<T, G, E, TF, COMP, true>), grid, dim3(LNT), 0, stream, p, one, strips);
     }
     return hipGetLastError();
 }
@@ -413,7 +528,8 @@ hipError_t run_kind(const LinRec &p, bool back, hipStream_t stream) {
 }
 hipError_t run_types(LinRec p, gdp_dtype dtype, bool back, hipStream_t stream) {
     p.lognx = lanes_log(p, dtype);
-    p.tiles = (int)tiles_of(p, dtype, back);
+    const int64_t tiles = tiles_of(p, dtype, back);
+    p.tiles = tiles > 1 ? (int)tiles : 1;
     if (dtype == GDP_F32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);
     if (p.g32) return p.vec ? run_kind<bf16, float, 8>(p, back, stream) : run_kind<bf16, float, 1>(p, back, stream);
     return p.vec ? run_kind<bf16, bf16, 8>(p, back, stream) : run_kind<bf16, bf16, 1>(p, back, stream);
@@ -429,11 +545,12 @@ hipError_t run_decode(const gdp_linrec_decode_args &a, hipStream_t stream) {
 }  // namespace
 
 bool linrec_fits(const LinRec &p, gdp_dtype dtype, bool backward) {
-    return tiles_of(p, dtype, backward) * LNT <= 0xffffffffll;
+    const int64_t w = (int64_t)elems_of(p, dtype) << lanes_log(p, dtype), tiles = tiles_of(p, dtype, backward);
+    return tiles * ((p.C + w - 1) / w) * LNT <= 0xffffffffll && chain_bytes(tiles, p.C) / 8 <= 0xffffffffll;
 }
 int64_t linrec_space(const LinRec &p, gdp_dtype dtype, bool backward) {
     const int64_t tiles = tiles_of(p, dtype, backward);
-    return tiles > 1 ? tiles * (backward ? 4 : 2) * p.C * (int64_t)sizeof(float) : 0;
+    return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, p.C) : 0;
 }
 hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
 hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, true, stream); }

@@ -96,6 +96,13 @@ struct Chans {
 #pragma unroll
         for (int i = 0; i < N; ++i) ((U *)p)[i] = u[i];
     }
+    // Makes the compiler forget what it has formed from the contents, which it
+    // would otherwise keep in registers for a second walk over them.
+    __device__ __forceinline__ void forget() {
+        if constexpr (E > 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) asm volatile("" : "+v"(u[i].x), "+v"(u[i].y), "+v"(u[i].z), "+v"(u[i].w));
+    }
     __device__ __forceinline__ void to(float *f) const {
         if constexpr (E == 1) {
             f[0] = to_f32(u[0]);
@@ -171,6 +178,12 @@ struct RowWalk {
         }
     }
 };
+
+template <int E>
+__device__ __forceinline__ void forget(float (&f)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) asm volatile("" : "+v"(f[e]));
+}
 
 // TT raw rows from row0 on; past the last row, or the last channel, zeros.
 template <typename T, int E, int TT>
