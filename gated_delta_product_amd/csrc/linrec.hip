@@ -73,64 +73,70 @@ __device__ __forceinline__ Run after(Run all, Run r) {
 // after the other, and publishes its own H.  Whichever H that is, the same
 // products and sums are formed in the same order, so the bits do not depend on
 // timing.  A value and its being there are one word, so nothing else has to be
-// ordered: a word of zeros is not there yet, and a zero is kept as -0.
+// ordered: a word of zeros is not there yet, and a zero is kept as -0.  What a
+// tile has published is noted in `flag` too, so that one load of a wave looks
+// at 64 tiles; that is only where to look, and comes in any order.
 //
 // Tiles are numbered by a counter in the order in which blocks start, so every
 // tile before one that waits belongs to a block that runs already.
 typedef unsigned long long u64;
 struct Chain {
     uint32_t *count;  // blocks that have started
+    uint32_t *flag;   // [strips][tiles] 0, 1: P, 2: H
     u64 *P;           // [tiles][C]
     uint32_t *H;      // [tiles][C]
 };
-constexpr int WINDOW = 8;  // tiles looked back at once
 constexpr int PATIENCE = 1 << 22;  // looks (seconds) before a tile gives up, with NaN
 
+template <typename T> __device__ __forceinline__ T look(const T *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T> __device__ __forceinline__ void show(T *p, T x) {
+    __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 __device__ __forceinline__ uint32_t not_zero(float x) { return x == 0.f ? 0x80000000u : __float_as_uint(x); }
-__device__ __forceinline__ void publish(u64 *at, Run r) {
-    __hip_atomic_store(at, (u64)__float_as_uint(r.B) << 32 | not_zero(r.A), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void publish(uint32_t *at, float h) {
-    __hip_atomic_store(at, not_zero(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// The state that enters the pos-th tile of its chain, for the channel of the
-// words P and H (its own); those of the tile before lie `back` further.
-__device__ __forceinline__ float entering(const u64 *P, const uint32_t *H, int64_t back, int pos) {
-    const int n = pos < WINDOW ? pos : WINDOW;
-    for (int look = 0; look < PATIENCE; ++look) {
-        uint32_t h[WINDOW];
-        u64 r[WINDOW];
-#pragma unroll
-        for (int k = 0; k < WINDOW; ++k) {
-            h[k] = 0;
-            r[k] = 0;
-            if (k < n) {
-                h[k] = __hip_atomic_load(H + (k + 1) * back, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                r[k] = __hip_atomic_load(P + (k + 1) * back, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-        }
-        int at = -1;  // nearest state, -1: none yet
-        bool open = true;
-#pragma unroll
-        for (int k = 0; k < WINDOW; ++k) {
-            if (open && h[k]) at = k;
-            open = open && !h[k] && r[k];
-        }
-        if (at < 0 && open && n == pos) at = n;  // before the first tile nothing is there
-        if (at >= 0) {
-            float x = 0.f;
-#pragma unroll
-            for (int k = WINDOW; k >= 0; --k) {
-                if (k < WINDOW && k == at) x = __uint_as_float(h[k]) + 0.f;
-                if (k < at && k < WINDOW) x = enter({__uint_as_float((uint32_t)r[k]) + 0.f, __uint_as_float((uint32_t)(r[k] >> 32))}, x);
-            }
-            return x;
-        }
-        __builtin_amdgcn_s_sleep(1);
-    }
-    return __builtin_nanf("");
+__device__ __forceinline__ u64 word(Run r) { return (u64)__float_as_uint(r.B) << 32 | not_zero(r.A); }
+__device__ __forceinline__ Run run_of(u64 w) {
+    return {__uint_as_float((uint32_t)w) + 0.f, __uint_as_float((uint32_t)(w >> 32))};
 }
 
+// The state that enters the pos-th tile of its chain, a channel a lane, by one
+// wave.  P, H and flag are the tile's own words; those of the tile before lie
+// `back` and `step` further.
+__device__ __forceinline__ float entering(const u64 *P, const uint32_t *H, int64_t back, const uint32_t *flag, int step,
+                                          int pos, bool mine) {
+    const int lane = lane_id();
+    int patience = PATIENCE, near = -1;
+    do {
+        // lane l: the tile l + 1 before; before the first one the state is there, and zero
+        const uint32_t f = lane < pos ? look(flag + (lane + 1) * step) : 2u;
+        const uint64_t some = __ballot(f >= 1), all = __ballot(f == 2);
+        if (all) {
+            const int k = __builtin_ctzll(all);
+            if (!(~some & ((1ull << k) - 1))) near = k;
+        }
+        if (near < 0) __builtin_amdgcn_s_sleep(1);
+    } while (near < 0 && --patience > 0);
+    if (near < 0) return __builtin_nanf("");
+    float h = 0.f;
+    if (near < pos && mine) {
+        uint32_t w;
+        while (!(w = look(H + (near + 1) * back)) && --patience > 0) {}
+        h = w ? __uint_as_float(w) + 0.f : __builtin_nanf("");
+    }
+    for (int k = near; k > 0; k -= 8) {
+        u64 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = k - i > 0 && mine ? look(P + (k - i) * back) : 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k - i > 0 && mine) {
+                while (!w[i] && --patience > 0) w[i] = look(P + (k - i) * back);
+                h = enter(w[i] ? run_of(w[i]) : Run{-1.f, __builtin_nanf("")}, h);
+            }
+    }
+    return h;
+}
 
 // A block's tile and strip of channels, and the tile's place in its chain: the
 // tiles from the first one on, or from the last one back.
@@ -220,35 +226,68 @@ __device__ __forceinline__ void walk_back(Run (&run)[E], const Chans<T, E> (&dr)
     }
 }
 
-// The block's runs of every channel, joined in order, one thread a channel:
-// the tile's Run goes out, and rb holds the state that enters each run.
+// The block's runs of every channel, joined in order, a channel a lane: every
+// wave its own runs, then the waves.
+constexpr int LNW = LNT / 64;
 template <bool BACK>
-__device__ __forceinline__ void join_runs(const float *ra, float *rb, int w, int ny, const Chain &ch, int64_t C, int tiles,
-                                          const Turn &t, int c, bool alone) {
-    const int k = threadIdx.x;
+struct Joint {
+    float *ra, *rb;  // [ny][w], the runs; rb becomes the state that enters each
+    int w, per, y0, k;
+    bool mine;
+    Run *part;       // [LNW][64], the waves' runs
+    __device__ __forceinline__ Joint(float *ra, float *rb, Run *part, int w, int ny)
+        : ra(ra), rb(rb), w(w), per(ny / LNW), y0(wave_id() * (ny / LNW)), k(lane_id() < w ? lane_id() : 0),
+          mine(lane_id() < w), part(part) {}
+    __device__ __forceinline__ int row(int i) const { return (y0 + (BACK ? per - 1 - i : i)) * w + k; }
+    __device__ __forceinline__ void own() const {
+        Run all{1.f, 0.f};
+        for (int i = 0; i < per; ++i) all = after(all, {ra[row(i)], rb[row(i)]});
+        part[wave_id() * 64 + lane_id()] = all;
+    }
+    // From the state that enters the tile
+    __device__ __forceinline__ void enter_own(float h) const {
+#pragma unroll
+        for (int v = 0; v < LNW - 1; ++v) {
+            const int u = BACK ? LNW - 1 - v : v;
+            if (BACK ? u > wave_id() : u < wave_id()) h = enter(part[u * 64 + lane_id()], h);
+        }
+        for (int i = 0; i < per; ++i) {
+            const Run r{ra[row(i)], rb[row(i)]};
+            if (mine) rb[row(i)] = h;
+            h = enter(r, h);
+        }
+    }
+    __device__ __forceinline__ Run all() const {
+        Run r{1.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < LNW; ++v) r = after(r, part[(BACK ? LNW - 1 - v : v) * 64 + lane_id()]);
+        return r;
+    }
+};
+
+// The tile's Run goes out, and the state that enters the tile comes back, to
+// the lane of every channel (first wave only); `wait` is done in between.
+template <bool BACK, typename F>
+__device__ __forceinline__ float hand_on(Run all, const Chain &ch, int64_t C, int tiles, const Turn &t, int c, bool mine,
+                                         bool alone, F wait) {
     float h = 0.f;
     u64 *P = ch.P + (int64_t)t.tile * C + c;
-    uint32_t *H = ch.H + (int64_t)t.tile * C + c;
-    if (tiles > 1) {
-        Run all{1.f, 0.f};
-        for (int i = 0; i < ny; ++i) {
-            const int y = BACK ? ny - 1 - i : i;
-            all = after(all, {ra[y * w + k], rb[y * w + k]});
+    uint32_t *H = ch.H + (int64_t)t.tile * C + c, *flag = ch.flag + (int64_t)t.strip * tiles + t.tile;
+    if (alone || tiles == 1) {  // nothing enters
+        if (tiles > 1) {
+            if (mine) show(H, not_zero(enter(all, h)));
+            if (lane_id() == 0) show(flag, 2u);
         }
-        if (alone) {  // nothing enters, so this is the state after the tile too
-            publish(H, all.B);
-        } else {
-            publish(P, all);
-            h = entering(P, H, BACK ? C : -C, t.pos);
-            publish(H, enter(all, h));
-        }
+        wait();
+        return h;
     }
-    for (int i = 0; i < ny; ++i) {
-        const int y = BACK ? ny - 1 - i : i;
-        const Run r{ra[y * w + k], rb[y * w + k]};
-        rb[y * w + k] = h;
-        h = enter(r, h);
-    }
+    if (mine) show(P, word(all));
+    if (lane_id() == 0) show(flag, 1u);
+    wait();
+    h = entering(P, H, BACK ? C : -C, flag, BACK ? 1 : -1, t.pos, mine);
+    if (mine) show(H, not_zero(enter(all, h)));
+    if (lane_id() == 0) show(flag, 2u);
+    return h;
 }
 
 }  // namespace
@@ -258,7 +297,8 @@ template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
 __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int strips) {
     __shared__ uint8_t code[LNT * TT];
     __shared__ int seq[LNT * TT];
-    __shared__ float ra[LNT * E], rb[LNT * E];
+    __shared__ float ra[LNT * E], rb[LNT * E], enters[64];
+    __shared__ Run part[LNW * 64];
     const Turn t = next_turn<false>(p, ch.count, strips);
     const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
     const int w = at.nx * E, k0 = at.ty * TT;  // channels of the block, the thread's rows in the tile
@@ -285,11 +325,18 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
         rb[at.ty * w + at.tx * E + e] = run[e].B;
     }
     __syncthreads();
-    const int c = t.strip * w + (int)threadIdx.x;
-    if ((int)threadIdx.x < w && c < p.C)
-        join_runs<false>(ra, rb, w, at.ny, ch, p.C, p.tiles, t, c, row_first(code[0]) || !(code[0] & ROW_IN));
+    const Joint<false> join(ra, rb, part, w, at.ny);
+    join.own();
+    __syncthreads();
+    const int c = t.strip * w + lane_id();
+    if (wave_id() == 0) {
+        const float h = hand_on<false>(join.all(), ch, p.C, p.tiles, t, c, join.mine && c < p.C,
+                                       row_first(code[0]) || !(code[0] & ROW_IN), [] {});
+        enters[lane_id()] = h;
+    }
     if constexpr (!ROWS) return;
     __syncthreads();
+    join.enter_own(enters[lane_id()]);
     if (!at.live) return;
     float h[E];
 #pragma unroll
@@ -327,7 +374,8 @@ template <typename T, typename G, int E, int TT, bool COMP>
 __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
     __shared__ uint8_t code[LNT * TT];
     __shared__ int seq[LNT * TT];
-    __shared__ float ra[2][LNT * E], rb[2][LNT * E];
+    __shared__ float ra[2][LNT * E], rb[2][LNT * E], enters[64];
+    __shared__ Run part[2][LNW * 64];
     const Turn t = next_turn<true>(p, ch.count, strips);
     const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
     const int w = at.nx * E, k0 = at.ty * TT;
@@ -361,17 +409,23 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
         }
     }
     __syncthreads();
-    const int c = t.strip * w + (int)threadIdx.x, n = at.ny * TT;
-    if ((int)threadIdx.x < w && c < p.C) {
-        float h = t.tile > 0 ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f;
-        for (int y = 0; y < at.ny; ++y) {
-            const Run r{ra[0][y * w + threadIdx.x], rb[0][y * w + threadIdx.x]};
-            rb[0][y * w + threadIdx.x] = h;
-            h = enter(r, h);
-        }
-        join_runs<true>(ra[1], rb[1], w, at.ny, ch, p.C, p.tiles, t, c, row_last(code[n - 1]) || !(code[n - 1] & ROW_IN));
-    }
+    const Joint<false> to(ra[0], rb[0], part[0], w, at.ny);
+    const Joint<true> back(ra[1], rb[1], part[1], w, at.ny);
+    to.own();
+    back.own();
     __syncthreads();
+    const int c = t.strip * w + lane_id(), n = at.ny * TT;
+    const bool mine = to.mine && c < p.C;
+    auto forwards = [&] {
+        to.enter_own(t.tile > 0 && mine ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f);
+    };
+    if (wave_id() == 0)
+        enters[lane_id()] = hand_on<true>(back.all(), ch, p.C, p.tiles, t, c, mine,
+                                          row_last(code[n - 1]) || !(code[n - 1] & ROW_IN), forwards);
+    else
+        forwards();
+    __syncthreads();
+    back.enter_own(enters[lane_id()]);
     if (!at.live) return;
     float h[E], m[E], hp[TT][E];
 #pragma unroll
@@ -482,35 +536,38 @@ constexpr int rows_of(int E, bool back) { return (E == 1 ? 16 : 8) / (back ? 2 :
 int lanes_log(const LinRec &p, gdp_dtype dtype) {
     const int E = !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4;
     int l = 0;
-    while (l < (E == 1 ? 6 : 4) && (E << l) < p.C) ++l;
+    while ((E << l) < 64 && (E << l) < p.C) ++l;  // at most 64 channels a block: a wave joins them
     return l;
 }
 int elems_of(const LinRec &p, gdp_dtype dtype) { return !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4; }
+int strips_of(const LinRec &p, gdp_dtype dtype) {
+    const int w = elems_of(p, dtype) << lanes_log(p, dtype);
+    return (p.C + w - 1) / w;
+}
 int64_t tiles_of(const LinRec &p, gdp_dtype dtype, bool back) {
     const int64_t per = (int64_t)(LNT >> lanes_log(p, dtype)) * rows_of(elems_of(p, dtype), back);
     return (p.m.rows + per - 1) / per;
 }
 
-// Words of a chain over `tiles`, whole units of 256 bytes: counter, P, H.
-int64_t chain_bytes(int64_t tiles, int64_t C) {
-    const int64_t n = tiles * C;
-    return 256 + (n * 12 + 255) / 256 * 256;
-}
-Chain chain_at(void *space, int64_t tiles, int64_t C) {
-    char *q = (char *)space;
-    return Chain{(uint32_t *)q, (u64 *)(q + 256), (uint32_t *)(q + 256 + tiles * C * 8)};
+// The words of a chain, in whole units of 256 bytes: counter and flags, P, H.
+int64_t units(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+int64_t flag_bytes(int64_t tiles, int64_t strips) { return units(4 * (64 + tiles * strips)); }
+int64_t chain_bytes(int64_t tiles, int64_t strips, int64_t C) { return flag_bytes(tiles, strips) + units(tiles * C * 12); }
+Chain chain_at(char *q, int64_t tiles, int64_t strips, int64_t C) {
+    char *r = q + flag_bytes(tiles, strips);
+    return Chain{(uint32_t *)q, (uint32_t *)q + 64, (u64 *)r, (uint32_t *)(r + tiles * C * 8)};
 }
 
 template <typename T, typename G, int E, bool COMP>
 hipError_t run_linrec(const LinRec &p, bool back, hipStream_t stream) {
     const int w = E << p.lognx, strips = (p.C + w - 1) / w;
-    const int64_t tiles = p.tiles, words = chain_bytes(tiles, p.C);
+    const int64_t tiles = p.tiles, words = chain_bytes(tiles, strips, p.C);
     const dim3 grid((unsigned)(tiles * strips));
     constexpr int TF = rows_of(E, false), TB = rows_of(E, true);
     Chain one{}, two{};
     if (tiles > 1) {
-        one = chain_at(p.space, tiles, p.C);
-        if (back) two = chain_at((char *)p.space + words, tiles, p.C);
+        one = chain_at((char *)p.space, tiles, strips, p.C);
+        if (back) two = chain_at((char *)p.space + words, tiles, strips, p.C);
         const int64_t n = (back ? 2 : 1) * words / 16;
         hipLaunchKernelGGL(gdp_linrec_clear_k, dim3((unsigned)((n + LNT - 1) / LNT)), dim3(LNT), 0, stream, (uint4 *)p.space, n);
     }
@@ -545,12 +602,12 @@ hipError_t run_decode(const gdp_linrec_decode_args &a, hipStream_t stream) {
 }  // namespace
 
 bool linrec_fits(const LinRec &p, gdp_dtype dtype, bool backward) {
-    const int64_t w = (int64_t)elems_of(p, dtype) << lanes_log(p, dtype), tiles = tiles_of(p, dtype, backward);
-    return tiles * ((p.C + w - 1) / w) * LNT <= 0xffffffffll && chain_bytes(tiles, p.C) / 8 <= 0xffffffffll;
+    const int64_t tiles = tiles_of(p, dtype, backward), strips = strips_of(p, dtype);
+    return tiles * strips * LNT <= 0xffffffffll && 2 * chain_bytes(tiles, strips, p.C) / 16 <= 0xffffff00ll;
 }
 int64_t linrec_space(const LinRec &p, gdp_dtype dtype, bool backward) {
     const int64_t tiles = tiles_of(p, dtype, backward);
-    return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, p.C) : 0;
+    return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, strips_of(p, dtype), p.C) : 0;
 }
 hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
 hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, true, stream); }
