@@ -77,15 +77,18 @@ __device__ __forceinline__ Run after(Run all, Run r) {
 // tile has published is noted in `flag` too, so that one load of a wave looks
 // at 64 tiles; that is only where to look, and comes in any order.
 //
-// Tiles are numbered by a counter in the order in which blocks start, so every
-// tile before one that waits belongs to a block that runs already.
+// The tiles of a strip are numbered by a counter in the order in which its
+// blocks start, so every tile before one that waits belongs to a block that runs
+// already.  (One counter for all strips takes 4 ns a block: 64 of 311 us of the
+// gradients of 32768 x 2048.)
 typedef unsigned long long u64;
 struct Chain {
-    uint32_t *count;  // blocks that have started
+    uint32_t *count;  // [strips], COUNT_STEP apart: blocks that have started
     uint32_t *flag;   // [strips][tiles] 0, 1: P, 2: H
     u64 *P;           // [tiles][C]
     uint32_t *H;      // [tiles][C]
 };
+constexpr int COUNT_STEP = 64;     // counters in lines of their own
 constexpr int PATIENCE = 1 << 22;  // looks (seconds) before a tile gives up, with NaN
 
 template <typename T> __device__ __forceinline__ T look(const T *p) {
@@ -146,14 +149,14 @@ struct Turn {
 template <bool BACK>
 __device__ __forceinline__ Turn next_turn(const LinRec &p, uint32_t *count, int strips) {
     __shared__ uint32_t id;
-    if (p.tiles > 1) {
-        if (threadIdx.x == 0) id = atomicAdd(count, 1u);
-        __syncthreads();
-    }
-    const uint32_t k = p.tiles > 1 ? __builtin_amdgcn_readfirstlane(id) : blockIdx.x;
     Turn t;
-    t.pos = (int)(k / (uint32_t)strips);
-    t.strip = (int)(k - (uint32_t)t.pos * strips);
+    t.strip = (int)(blockIdx.x % (uint32_t)strips);
+    t.pos = 0;
+    if (p.tiles > 1) {
+        if (threadIdx.x == 0) id = atomicAdd(count + t.strip * COUNT_STEP, 1u);
+        __syncthreads();
+        t.pos = (int)__builtin_amdgcn_readfirstlane(id);
+    }
     t.tile = BACK ? p.tiles - 1 - t.pos : t.pos;
     return t;
 }
@@ -549,13 +552,13 @@ int64_t tiles_of(const LinRec &p, gdp_dtype dtype, bool back) {
     return (p.m.rows + per - 1) / per;
 }
 
-// The words of a chain, in whole units of 256 bytes: counter and flags, P, H.
+// The words of a chain, in whole units of 256 bytes: counters and flags, P, H.
 int64_t units(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-int64_t flag_bytes(int64_t tiles, int64_t strips) { return units(4 * (64 + tiles * strips)); }
+int64_t flag_bytes(int64_t tiles, int64_t strips) { return units(4 * strips * (COUNT_STEP + tiles)); }
 int64_t chain_bytes(int64_t tiles, int64_t strips, int64_t C) { return flag_bytes(tiles, strips) + units(tiles * C * 12); }
 Chain chain_at(char *q, int64_t tiles, int64_t strips, int64_t C) {
     char *r = q + flag_bytes(tiles, strips);
-    return Chain{(uint32_t *)q, (uint32_t *)q + 64, (u64 *)r, (uint32_t *)(r + tiles * C * 8)};
+    return Chain{(uint32_t *)q, (uint32_t *)q + strips * COUNT_STEP, (u64 *)r, (uint32_t *)(r + tiles * C * 8)};
 }
 
 template <typename T, typename G, int E, bool COMP>
