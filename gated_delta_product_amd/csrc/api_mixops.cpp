@@ -30,30 +30,29 @@ gdp_status check_map(const char *name, int64_t B, int64_t T, const int32_t *cu, 
     return ok();
 }
 
-// A strided [B, T, C] input of whole elements; *vec is cleared where its rows do not start on 16 bytes.  The stride of a
-// dimension of one element does not matter.
+// A strided [B, T, C] input of whole elements; *vec is cleared where its rows do not start on units of so many elements.
+// The stride of a dimension of one element does not matter.
 gdp_status check_input(const char *name, const char *what, const void *p, int64_t bs, int64_t ts, int64_t B, int64_t T,
-                       gdp_dtype dtype, bool *vec, gdp::Strided *out) {
+                       gdp_dtype dtype, bool *vec, gdp::Strided *out, int64_t unit) {
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
     if ((B > 1 && bs < 0) || (T > 1 && ts < 0)) return fail(GDP_ERR_INVALID, "%s: strides of %s must be >= 0", name, what);
     if ((uintptr_t)p % dsize(dtype)) return fail(GDP_ERR_INVALID, "%s: %s is not aligned to its type", name, what);
-    const int64_t unit = 16 / (int64_t)dsize(dtype);
-    if (!aligned16(p) || (B > 1 && bs % unit) || (T > 1 && ts % unit)) *vec = false;
+    if ((uintptr_t)p % (unit * dsize(dtype)) || (B > 1 && bs % unit) || (T > 1 && ts % unit)) *vec = false;
     *out = gdp::Strided{p, B > 1 ? bs : 0, T > 1 ? ts : 0};
     return ok();
 }
-gdp_status check_output(const char *name, const char *what, const void *p, gdp_dtype dtype, bool *vec) {
+// A contiguous array of states, or NULL.
+gdp_status check_states(const char *name, const char *what, const void *p, gdp_dtype dtype, bool *vec, int64_t unit) {
+    if ((uintptr_t)p % dsize(dtype)) return fail(GDP_ERR_INVALID, "%s: %s is not aligned to its type", name, what);
+    if ((uintptr_t)p % (unit * dsize(dtype))) *vec = false;
+    return ok();
+}
+gdp_status check_output(const char *name, const char *what, const void *p, gdp_dtype dtype, bool *vec, int64_t unit) {
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
-    if ((uintptr_t)p % dsize(dtype)) return fail(GDP_ERR_INVALID, "%s: %s is not aligned to its type", name, what);
-    if (!aligned16(p)) *vec = false;
-    return ok();
+    return check_states(name, what, p, dtype, vec, unit);
 }
-// A contiguous array of states (or NULL).
-gdp_status check_states(const char *name, const char *what, const void *p, gdp_dtype dtype, bool *vec) {
-    if ((uintptr_t)p % dsize(dtype)) return fail(GDP_ERR_INVALID, "%s: %s is not aligned to its type", name, what);
-    if (!aligned16(p)) *vec = false;
-    return ok();
-}
+// Elements of 16 bytes
+int64_t unit_of(gdp_dtype d) { return 16 / (int64_t)dsize(d); }
 
 gdp_status check_decode(const char *name, int64_t n, int64_t S, int32_t C, int64_t pool, const int32_t *slots) {
     if (n < 0 || S < 0) return fail(GDP_ERR_INVALID, "%s: n and S must be >= 0", name);
@@ -79,14 +78,14 @@ gdp_status check_linrec(const char *name, const gdp_linrec_args *a, gdp::LinRec 
     p->g32 = a->g_dtype == GDP_F32;
     p->sigmoid = a->decay == GDP_DECAY_SIGMOID;
     p->complement = a->complement != 0;
-    p->vec = a->C % (a->dtype == GDP_BF16 ? 8 : 4) == 0;
+    p->vec = a->C % 4 == 0;
     return ok();
 }
 // What the tensors' alignment leaves open: the larger workspace of both.
-int64_t largest_space(gdp::LinRec p, gdp_dtype dtype, bool backward) {
-    const int64_t n = gdp::linrec_space(p, dtype, backward);
+int64_t largest_space(gdp::LinRec p, bool backward) {
+    const int64_t n = gdp::linrec_space(p, backward);
     p.vec = false;
-    const int64_t m = gdp::linrec_space(p, dtype, backward);
+    const int64_t m = gdp::linrec_space(p, backward);
     return n > m ? n : m;
 }
 
@@ -104,7 +103,7 @@ gdp_status check_conv(const char *name, const gdp_conv_args *a, gdp::ShortConv *
     p->C = a->C;
     p->W = a->W;
     p->act = a->activation;
-    p->vec = a->C % (a->dtype == GDP_BF16 ? 8 : 4) == 0;
+    p->vec = a->C % unit_of(a->dtype) == 0;
     return ok();
 }
 int64_t largest_space(gdp::ShortConv p, gdp_dtype dtype) {
@@ -134,7 +133,7 @@ extern "C" {
 int64_t gdp_linrec_workspace_bytes(const gdp_linrec_args *a, int32_t backward) {
     gdp::LinRec p;
     if (check_linrec("gdp_linrec_workspace_bytes", a, &p) != GDP_OK) return -1;
-    return largest_space(p, a->dtype, backward != 0);
+    return largest_space(p, backward != 0);
 }
 
 gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t workspace_bytes, void *stream) {
@@ -142,17 +141,17 @@ gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t wor
     gdp::LinRec p;
     TRY(check_linrec(name, a, &p));
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x));
-        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g));
-        TRY(check_output(name, "y", a->y, a->dtype, &p.vec));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, 4));
+        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, 4));
+        TRY(check_output(name, "y", a->y, a->dtype, &p.vec, 4));
     }
-    TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec));
-    TRY(check_states(name, "ht", a->ht, GDP_F32, &p.vec));
+    TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
+    TRY(check_states(name, "ht", a->ht, GDP_F32, &p.vec, 1));
     p.h0 = a->h0;
     p.y = a->y;
     p.ht = a->ht;
-    if (!gdp::linrec_fits(p, a->dtype, false)) return too_large(name);
-    TRY(check_space(name, workspace, workspace_bytes, largest_space(p, a->dtype, false)));
+    if (!gdp::linrec_fits(p, false)) return too_large(name);
+    TRY(check_space(name, workspace, workspace_bytes, largest_space(p, false)));
     p.space = workspace;
     if (p.m.nseq == 0 || (p.m.rows == 0 && !p.ht)) return ok();
     return hip_status(gdp::launch_linrec(p, a->dtype, (hipStream_t)stream), name);
@@ -165,15 +164,15 @@ gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, v
     TRY(check_linrec(name, a, &p));
     if (!d) return fail(GDP_ERR_INVALID, "%s: grads is NULL", name);
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x));
-        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g));
-        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy));
-        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec));
-        TRY(check_output(name, "dg", d->dg, a->g_dtype, &p.vec));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, 4));
+        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, 4));
+        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy, 4));
+        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec, 4));
+        TRY(check_output(name, "dg", d->dg, a->g_dtype, &p.vec, 4));
     }
-    TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec));
-    TRY(check_states(name, "dht", d->dht, GDP_F32, &p.vec));
-    TRY(check_states(name, "dh0", d->dh0, GDP_F32, &p.vec));
+    TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
+    TRY(check_states(name, "dht", d->dht, GDP_F32, &p.vec, 1));
+    TRY(check_states(name, "dh0", d->dh0, GDP_F32, &p.vec, 1));
     if (d->dh0 && (d->dh0 == d->dht || d->dh0 == a->h0))
         return fail(GDP_ERR_INVALID, "%s: dh0 may not be dht or h0", name);
     p.h0 = a->h0;
@@ -181,8 +180,8 @@ gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, v
     p.dx = d->dx;
     p.dg = d->dg;
     p.dh0 = d->dh0;
-    if (!gdp::linrec_fits(p, a->dtype, true)) return too_large(name);
-    TRY(check_space(name, workspace, workspace_bytes, largest_space(p, a->dtype, true)));
+    if (!gdp::linrec_fits(p, true)) return too_large(name);
+    TRY(check_space(name, workspace, workspace_bytes, largest_space(p, true)));
     p.space = workspace;
     if (p.m.rows == 0 && !p.dh0) return ok();
     return hip_status(gdp::launch_linrec_bwd(p, a->dtype, (hipStream_t)stream), name);
@@ -197,13 +196,14 @@ gdp_status gdp_linrec_decode(const gdp_linrec_decode_args *a, void *stream) {
         return fail(GDP_ERR_INVALID, "%s: unknown decay %d", name, (int)a->decay);
     TRY(check_decode(name, a->n, a->S, a->C, a->pool, a->slots));
     if (a->n == 0 || a->S == 0) return ok();
-    bool vec = a->C % (a->dtype == GDP_BF16 ? 8 : 4) == 0;
+    const int64_t unit = unit_of(a->dtype);
+    bool vec = a->C % unit == 0;
     gdp::Strided x, g;
-    TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &vec, &x));
-    TRY(check_input(name, "g", a->g, a->g_n_stride, a->g_t_stride, a->n, a->S, a->g_dtype, &vec, &g));
-    TRY(check_output(name, "y", a->y, a->dtype, &vec));
+    TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &vec, &x, unit));
+    TRY(check_input(name, "g", a->g, a->g_n_stride, a->g_t_stride, a->n, a->S, a->g_dtype, &vec, &g, unit));
+    TRY(check_output(name, "y", a->y, a->dtype, &vec, unit));
     if (!a->state && a->pool > 0) return fail(GDP_ERR_INVALID, "%s: state is NULL", name);
-    TRY(check_states(name, "state", a->state, GDP_F32, &vec));
+    TRY(check_states(name, "state", a->state, GDP_F32, &vec, 1));
     return hip_status(gdp::launch_linrec_decode(*a, vec, (hipStream_t)stream), name);
 }
 
@@ -212,13 +212,14 @@ gdp_status gdp_conv_fwd(const gdp_conv_args *a, void *stream) {
     gdp::ShortConv p;
     TRY(check_conv(name, a, &p));
     TRY(check_taps(name, a->w, a->b));
+    const int64_t unit = unit_of(a->dtype);
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x));
-        TRY(check_output(name, "y", a->y, a->dtype, &p.vec));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, unit));
+        TRY(check_output(name, "y", a->y, a->dtype, &p.vec, unit));
         if (a->x == a->y) return fail(GDP_ERR_INVALID, "%s: y may not be x", name);
     }
-    TRY(check_states(name, "h0", a->h0, a->dtype, &p.vec));
-    TRY(check_states(name, "ht", a->ht, a->dtype, &p.vec));
+    TRY(check_states(name, "h0", a->h0, a->dtype, &p.vec, unit));
+    TRY(check_states(name, "ht", a->ht, a->dtype, &p.vec, unit));
     if (a->ht && a->ht == a->h0) return fail(GDP_ERR_INVALID, "%s: ht may not be h0", name);
     p.w = a->w;
     p.b = a->b;
@@ -243,15 +244,16 @@ gdp_status gdp_conv_bwd(const gdp_conv_args *a, const gdp_conv_grads *d, void *w
     TRY(check_conv(name, a, &p));
     if (!d) return fail(GDP_ERR_INVALID, "%s: grads is NULL", name);
     TRY(check_taps(name, a->w, a->b));
+    const int64_t unit = unit_of(a->dtype);
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x));
-        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy));
-        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, unit));
+        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy, unit));
+        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec, unit));
         if (d->dx == a->x || d->dx == d->dy) return fail(GDP_ERR_INVALID, "%s: dx may not be x or dy", name);
     }
-    TRY(check_states(name, "h0", a->h0, a->dtype, &p.vec));
-    TRY(check_states(name, "dht", d->dht, a->dtype, &p.vec));
-    TRY(check_states(name, "dh0", d->dh0, a->dtype, &p.vec));
+    TRY(check_states(name, "h0", a->h0, a->dtype, &p.vec, unit));
+    TRY(check_states(name, "dht", d->dht, a->dtype, &p.vec, unit));
+    TRY(check_states(name, "dh0", d->dh0, a->dtype, &p.vec, unit));
     if (d->dh0 && (d->dh0 == d->dht || d->dh0 == a->h0))
         return fail(GDP_ERR_INVALID, "%s: dh0 may not be dht or h0", name);
     if (((uintptr_t)d->dw | (uintptr_t)d->db) & 3)
@@ -287,10 +289,11 @@ gdp_status gdp_conv_decode(const gdp_conv_decode_args *a, void *stream) {
     TRY(check_decode(name, a->n, a->S, a->C, a->pool, a->slots));
     if (a->n == 0 || a->S == 0) return ok();
     TRY(check_taps(name, a->w, a->b));
-    TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &p.vec, &p.x));
-    TRY(check_output(name, "y", a->y, a->dtype, &p.vec));
+    const int64_t unit = unit_of(a->dtype);
+    TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &p.vec, &p.x, unit));
+    TRY(check_output(name, "y", a->y, a->dtype, &p.vec, unit));
     if (!a->state && a->pool > 0) return fail(GDP_ERR_INVALID, "%s: state is NULL", name);
-    TRY(check_states(name, "state", a->state, a->dtype, &p.vec));
+    TRY(check_states(name, "state", a->state, a->dtype, &p.vec, unit));
     return hip_status(gdp::launch_conv_decode(*a, p.vec, (hipStream_t)stream), name);
 }
 
@@ -313,7 +316,7 @@ gdp_status gdp_rotary(const gdp_rotary_args *a, void *stream) {
         return fail(GDP_ERR_INVALID, "%s: strides of positions must be >= 0", name);
     if (!a->freq || ((uintptr_t)a->freq & 7)) return fail(GDP_ERR_INVALID, "%s: freq is NULL or not 8-byte aligned", name);
     if (p.m.rows == 0 || p.m.nseq == 0) return ok();
-    const int unit = a->dtype == GDP_BF16 ? 8 : 4;
+    const int64_t unit = unit_of(a->dtype);
     p.vec = a->D % unit == 0 && (a->interleaved ? a->R : a->R / 2) % unit == 0;
     const struct {
         const char *in, *out;
@@ -327,8 +330,8 @@ gdp_status gdp_rotary(const gdp_rotary_args *a, void *stream) {
     for (int i = 0; i < 2; ++i) {
         p.H[i] = t[i].heads;
         if (!t[i].heads) continue;
-        TRY(check_input(name, t[i].in, t[i].x, t[i].bs, t[i].ts, a->B, a->T, a->dtype, &p.vec, &p.in[i]));
-        TRY(check_input(name, t[i].out, t[i].y, t[i].ybs, t[i].yts, a->B, a->T, a->dtype, &p.vec, &p.out[i]));
+        TRY(check_input(name, t[i].in, t[i].x, t[i].bs, t[i].ts, a->B, a->T, a->dtype, &p.vec, &p.in[i], unit));
+        TRY(check_input(name, t[i].out, t[i].y, t[i].ybs, t[i].yts, a->B, a->T, a->dtype, &p.vec, &p.out[i], unit));
         const int64_t width = (int64_t)t[i].heads * a->D;
         if ((a->T > 1 && t[i].yts < width) || (a->B > 1 && t[i].ybs < width))
             return fail(GDP_ERR_INVALID, "%s: rows of %s overlap", name, t[i].out);

@@ -15,41 +15,64 @@ namespace gdp {
 namespace {
 
 constexpr int LNT = 256;
+constexpr int RF = 8, RB = 8;
+constexpr int W = 64;  // channels of a block: those that a wave joins, a lane each
 
-// The decay a of a row in one number d, a = 1 + d where d < 0, else a = d:
-// close to one its distance from one is kept, which a rounding of a itself
-// would lose and compound over the rows that a slow channel remembers; a fast
-// channel keeps a.
-__device__ __forceinline__ float decay_log(float g) {
-    // e^g - 1 by its series near zero, where the difference would cancel
-    float p = fmaf(g, 1.0f / 5040.0f, 1.0f / 720.0f);
-    p = fmaf(g, p, 1.0f / 120.0f);
-    p = fmaf(g, p, 1.0f / 24.0f);
-    p = fmaf(g, p, 1.0f / 6.0f);
-    p = fmaf(g, p, 0.5f);
-    p = fmaf(g * g, p, g);
-    return g < 0.f && g >= -0.35f ? p : exp_exact(g);
-}
-__device__ __forceinline__ float decay_sigmoid(float g) {
-    const float r = __builtin_amdgcn_rcpf(1.0f + exp_exact(fabsf(g)));
-    return g > 0.f ? -fmaxf(r, 1.17549435e-38f) : r;  // never -0, which would be a = 0
-}
-template <int N>
+// The decay a of a row and channel in one number, by the type of the rows.
+//
+// float32: d, with a = 1 + d where d < 0, else a = d.  Close to one its
+// distance from one is kept, which a rounding of a itself would lose and
+// compound over the rows that a slow channel remembers; a fast channel keeps a.
+template <typename T> struct Decay {
+    static __device__ __forceinline__ float log(float g) {
+        // e^g - 1 by its series near zero, where the difference would cancel
+        float p = fmaf(g, 1.0f / 5040.0f, 1.0f / 720.0f);
+        p = fmaf(g, p, 1.0f / 120.0f);
+        p = fmaf(g, p, 1.0f / 24.0f);
+        p = fmaf(g, p, 1.0f / 6.0f);
+        p = fmaf(g, p, 0.5f);
+        p = fmaf(g * g, p, g);
+        return g < 0.f && g >= -0.35f ? p : exp_exact(g);
+    }
+    static __device__ __forceinline__ float sigmoid(float g) {
+        const float r = __builtin_amdgcn_rcpf(1.0f + exp_exact(fabsf(g)));
+        return g > 0.f ? -fmaxf(r, 1.17549435e-38f) : r;  // never -0, which would be a = 0
+    }
+    static __device__ __forceinline__ float keep(float d, float h) { return fmaf(d, h, d < 0.f ? h : 0.f); }  // a h
+    static __device__ __forceinline__ float rest(float d) { return d < 0.f ? -d : 1.0f - d; }                 // 1 - a
+    template <bool COMP> static __device__ __forceinline__ float step(float h, float d, float x) {
+        return COMP ? fmaf(rest(d), x, keep(d, h)) : keep(d, h) + x;
+    }
+};
+// bfloat16: s = 1 - a, to a few 2^-24 of itself (of one, where a is small: such
+// a state counts as little beside the 2^-9 of the rows).  Four to six
+// instructions a row fewer, by which the kernels were bound: 32768 x 2048
+// gates, with the form above, 293 us of gradients.
+template <> struct Decay<bf16> {
+    static __device__ __forceinline__ float log(float g) {
+        float p = fmaf(g, 1.0f / 24.0f, 1.0f / 6.0f);
+        p = fmaf(g, p, 0.5f);
+        p = fmaf(g, p, 1.0f);
+        return fabsf(g) <= 0.0625f ? -g * p : 1.0f - __builtin_amdgcn_exp2f(g * 1.44269502f);
+    }
+    static __device__ __forceinline__ float sigmoid(float g) {
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * 1.44269502f));
+    }
+    static __device__ __forceinline__ float keep(float s, float h) { return fmaf(-s, h, h); }
+    static __device__ __forceinline__ float rest(float s) { return s; }
+    template <bool COMP> static __device__ __forceinline__ float step(float h, float s, float x) {
+        return COMP ? fmaf(s, x - h, h) : fmaf(-s, h, h) + x;
+    }
+};
+template <typename T, int N>
 __device__ __forceinline__ void decays(float (&d)[N], bool sigmoid) {
     if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = decay_sigmoid(d[i]);
+        for (int i = 0; i < N; ++i) d[i] = Decay<T>::sigmoid(d[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = decay_log(d[i]);
+        for (int i = 0; i < N; ++i) d[i] = Decay<T>::log(d[i]);
     }
-}
-__device__ __forceinline__ float keep(float d, float h) { return fmaf(d, h, d < 0.f ? h : 0.f); }  // a h
-__device__ __forceinline__ float rest(float d) { return d < 0.f ? -d : 1.0f - d; }                 // 1 - a
-
-template <bool COMP>
-__device__ __forceinline__ float step(float h, float d, float x) {
-    return COMP ? fmaf(rest(d), x, keep(d, h)) : keep(d, h) + x;
 }
 
 // What a run of rows does to the state; A < 0: it ends with B whatever came in
@@ -165,6 +188,7 @@ __device__ __forceinline__ Turn next_turn(const LinRec &p, uint32_t *count, int 
 template <int TT>
 struct Kinds {
     uint32_t in = 0, first = 0, last = 0;
+    bool plain;  // all rows of the wave inside a sequence, none its first or last
     __device__ __forceinline__ Kinds(const uint8_t *code) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
@@ -173,7 +197,14 @@ struct Kinds {
             first |= (uint32_t)row_first(c) << i;
             last |= (uint32_t)row_last(c) << i;
         }
+        plain = !__any(in != (1u << TT) - 1 || first || last);
     }
+    __device__ __forceinline__ bool inside(int i) const { return plain || (in >> i & 1); }
+    __device__ __forceinline__ bool is_first(int i) const { return !plain && (first >> i & 1); }
+    __device__ __forceinline__ bool is_last(int i) const { return !plain && (last >> i & 1); }
+    // nothing from before (or behind) them gets past these rows
+    __device__ __forceinline__ bool cut() const { return in != (1u << TT) - 1 || first; }
+    __device__ __forceinline__ bool cut_back() const { return in != (1u << TT) - 1 || last; }
 };
 
 // A thread's rows from the first to the last: h <- a h + c x
@@ -186,21 +217,24 @@ __device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT],
     for (int i = 0; i < TT; ++i) {
         float x[E];
         xr[i].to(x);
-        if (is.first >> i & 1) {
+        if (is.is_first(i)) {
             float h[E];
             load_state<E>(h, h0, seq[i], C, col);
 #pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
+            for (int e = 0; e < E; ++e) run[e].B = h[e];
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = step<COMP>(run[e].B, d[i][e], x[e]);
-            run[e].A = run[e].A < 0.f ? -1.f : keep(d[i][e], run[e].A);
+            run[e].B = Decay<T>::template step<COMP>(run[e].B, d[i][e], x[e]);
+            run[e].A = Decay<T>::keep(d[i][e], run[e].A);
         }
-        if (!(is.in >> i & 1))
+        if (!is.inside(i))
 #pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
+            for (int e = 0; e < E; ++e) run[e].B = 0.f;
     }
+    if (!is.plain && is.cut())
+#pragma unroll
+        for (int e = 0; e < E; ++e) run[e].A = -1.f;
 }
 // From the last to the first: m <- a (dy + m), the gradient of the state before the row
 template <typename T, int E, int TT>
@@ -212,58 +246,58 @@ __device__ __forceinline__ void walk_back(Run (&run)[E], const Chans<T, E> (&dr)
     for (int i = TT - 1; i >= 0; --i) {
         float dy[E];
         dr[i].to(dy);
-        if (is.last >> i & 1) {
+        if (is.is_last(i)) {
             float h[E];
             load_state<E>(h, dht, seq[i], C, col);
 #pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, h[e]};
+            for (int e = 0; e < E; ++e) run[e].B = h[e];
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = keep(d[i][e], dy[e] + run[e].B);
-            run[e].A = run[e].A < 0.f ? -1.f : keep(d[i][e], run[e].A);
+            run[e].B = Decay<T>::keep(d[i][e], dy[e] + run[e].B);
+            run[e].A = Decay<T>::keep(d[i][e], run[e].A);
         }
-        if (!(is.in >> i & 1))
+        if (!is.inside(i))
 #pragma unroll
-            for (int e = 0; e < E; ++e) run[e] = {-1.f, 0.f};
+            for (int e = 0; e < E; ++e) run[e].B = 0.f;
     }
+    if (!is.plain && is.cut_back())
+#pragma unroll
+        for (int e = 0; e < E; ++e) run[e].A = -1.f;
 }
 
 // The block's runs of every channel, joined in order, a channel a lane: every
 // wave its own runs, then the waves.
 constexpr int LNW = LNT / 64;
-template <bool BACK>
+template <int NY, bool BACK>
 struct Joint {
-    float *ra, *rb;  // [ny][w], the runs; rb becomes the state that enters each
-    int w, per, y0, k;
-    bool mine;
-    Run *part;       // [LNW][64], the waves' runs
-    __device__ __forceinline__ Joint(float *ra, float *rb, Run *part, int w, int ny)
-        : ra(ra), rb(rb), w(w), per(ny / LNW), y0(wave_id() * (ny / LNW)), k(lane_id() < w ? lane_id() : 0),
-          mine(lane_id() < w), part(part) {}
-    __device__ __forceinline__ int row(int i) const { return (y0 + (BACK ? per - 1 - i : i)) * w + k; }
+    static constexpr int PER = NY / LNW;
+    float *ra, *rb;  // [NY][W], the runs; rb becomes the state that enters each
+    Run *part;       // [LNW][W], the waves' runs
+    __device__ __forceinline__ Joint(float *ra, float *rb, Run *part) : ra(ra), rb(rb), part(part) {}
+    __device__ __forceinline__ int row(int i) const { return (wave_id() * PER + (BACK ? PER - 1 - i : i)) * W + lane_id(); }
     __device__ __forceinline__ void own() const {
         Run all{1.f, 0.f};
-        for (int i = 0; i < per; ++i) all = after(all, {ra[row(i)], rb[row(i)]});
-        part[wave_id() * 64 + lane_id()] = all;
+        for (int i = 0; i < PER; ++i) all = after(all, {ra[row(i)], rb[row(i)]});
+        part[wave_id() * W + lane_id()] = all;
     }
     // From the state that enters the tile
     __device__ __forceinline__ void enter_own(float h) const {
 #pragma unroll
         for (int v = 0; v < LNW - 1; ++v) {
             const int u = BACK ? LNW - 1 - v : v;
-            if (BACK ? u > wave_id() : u < wave_id()) h = enter(part[u * 64 + lane_id()], h);
+            if (BACK ? u > wave_id() : u < wave_id()) h = enter(part[u * W + lane_id()], h);
         }
-        for (int i = 0; i < per; ++i) {
+        for (int i = 0; i < PER; ++i) {
             const Run r{ra[row(i)], rb[row(i)]};
-            if (mine) rb[row(i)] = h;
+            rb[row(i)] = h;
             h = enter(r, h);
         }
     }
     __device__ __forceinline__ Run all() const {
         Run r{1.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < LNW; ++v) r = after(r, part[(BACK ? LNW - 1 - v : v) * 64 + lane_id()]);
+        for (int v = 0; v < LNW; ++v) r = after(r, part[(BACK ? LNW - 1 - v : v) * W + lane_id()]);
         return r;
     }
 };
@@ -298,19 +332,20 @@ __device__ __forceinline__ float hand_on(Run all, const Chain &ch, int64_t C, in
 // ROWS: y and the final states; without: only H, the state after every tile.
 template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
 __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int strips) {
-    __shared__ uint8_t code[LNT * TT];
-    __shared__ int seq[LNT * TT];
-    __shared__ float ra[LNT * E], rb[LNT * E], enters[64];
-    __shared__ Run part[LNW * 64];
+    __shared__ uint8_t code[LNT / (W / E) * TT];
+    __shared__ int seq[LNT / (W / E) * TT];
+    __shared__ float ra[LNT * E], rb[LNT * E], enters[W];
+    __shared__ Run part[LNW * W];
     const Turn t = next_turn<false>(p, ch.count, strips);
-    const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
-    const int w = at.nx * E, k0 = at.ty * TT;  // channels of the block, the thread's rows in the tile
+    constexpr int NX = W / E, NY = LNT / NX;  // threads side by side, and one behind the other
+    const Place<NX, NY, E, TT> at(p.C, t.tile, t.strip);
+    const int k0 = at.ty * TT;  // the thread's rows in the tile
 
     Chans<T, E> xr[TT];
     Chans<G, E> gr[TT];
     load_rows<T, E, TT>(xr, p.x, p.m, at.row0, at.col, at.live);
     load_rows<G, E, TT>(gr, p.g, p.m, at.row0, at.col, at.live);
-    find_rows<LNT>(p.m, at.tile0, at.ny * TT, code, seq);
+    find_rows<LNT>(p.m, at.tile0, NY * TT, code, seq);
     __syncthreads();
 
     const Kinds<TT> is(code + k0);
@@ -318,22 +353,22 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         gr[i].to(d[i]);
-        decays<E>(d[i], p.sigmoid);
+        decays<T>(d[i], p.sigmoid);
     }
     Run run[E];
     walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        ra[at.ty * w + at.tx * E + e] = run[e].A;
-        rb[at.ty * w + at.tx * E + e] = run[e].B;
+        ra[at.ty * W + at.tx * E + e] = run[e].A;
+        rb[at.ty * W + at.tx * E + e] = run[e].B;
     }
     __syncthreads();
-    const Joint<false> join(ra, rb, part, w, at.ny);
+    const Joint<NY, false> join(ra, rb, part);
     join.own();
     __syncthreads();
-    const int c = t.strip * w + lane_id();
+    const int c = t.strip * W + lane_id();
     if (wave_id() == 0) {
-        const float h = hand_on<false>(join.all(), ch, p.C, p.tiles, t, c, join.mine && c < p.C,
+        const float h = hand_on<false>(join.all(), ch, p.C, p.tiles, t, c, c < p.C,
                                        row_first(code[0]) || !(code[0] & ROW_IN), [] {});
         enters[lane_id()] = h;
     }
@@ -343,7 +378,7 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     if (!at.live) return;
     float h[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = rb[at.ty * w + at.tx * E + e];
+    for (int e = 0; e < E; ++e) h[e] = rb[at.ty * W + at.tx * E + e];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         xr[i].forget();
@@ -351,16 +386,16 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        if (!(is.in >> i & 1)) continue;
+        if (!is.inside(i)) continue;
         float x[E];
         xr[i].to(x);
-        if (is.first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
+        if (is.is_first(i)) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = step<COMP>(h[e], d[i][e], x[e]);
+        for (int e = 0; e < E; ++e) h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
         Chans<T, E> o;
         o.from(h);
         o.store((T *)p.y + (int64_t)(at.row0 + i) * p.C + at.col);
-        if (p.ht && (is.last >> i & 1)) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
+        if (is.is_last(i) && p.ht) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
     }
     if (p.ht && at.ty == 0)
         for (int q = t.tile; q < p.m.nseq; q += p.tiles)
@@ -375,20 +410,21 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
 // the tiles (gdp_linrec_k without ROWS, in the same tiles).
 template <typename T, typename G, int E, int TT, bool COMP>
 __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
-    __shared__ uint8_t code[LNT * TT];
-    __shared__ int seq[LNT * TT];
-    __shared__ float ra[2][LNT * E], rb[2][LNT * E], enters[64];
-    __shared__ Run part[2][LNW * 64];
+    __shared__ uint8_t code[LNT / (W / E) * TT];
+    __shared__ int seq[LNT / (W / E) * TT];
+    __shared__ float ra[2][LNT * E], rb[2][LNT * E], enters[W];
+    __shared__ Run part[2][LNW * W];
     const Turn t = next_turn<true>(p, ch.count, strips);
-    const Place<LNT, E, TT> at(p.lognx, p.C, t.tile, t.strip);
-    const int w = at.nx * E, k0 = at.ty * TT;
+    constexpr int NX = W / E, NY = LNT / NX;
+    const Place<NX, NY, E, TT> at(p.C, t.tile, t.strip);
+    const int k0 = at.ty * TT;
 
     Chans<T, E> xr[TT], dr[TT];
     Chans<G, E> gr[TT];
     load_rows<T, E, TT>(xr, p.x, p.m, at.row0, at.col, at.live);
     load_rows<G, E, TT>(gr, p.g, p.m, at.row0, at.col, at.live);
     load_rows<T, E, TT>(dr, p.dy, p.m, at.row0, at.col, at.live);
-    find_rows<LNT>(p.m, at.tile0, at.ny * TT, code, seq);
+    find_rows<LNT>(p.m, at.tile0, NY * TT, code, seq);
     __syncthreads();
 
     const Kinds<TT> is(code + k0);
@@ -396,7 +432,7 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         gr[i].to(d[i]);
-        decays<E>(d[i], p.sigmoid);
+        decays<T>(d[i], p.sigmoid);
     }
     Run run[E];
 #pragma unroll
@@ -407,18 +443,18 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
         else walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            ra[z][at.ty * w + at.tx * E + e] = run[e].A;
-            rb[z][at.ty * w + at.tx * E + e] = run[e].B;
+            ra[z][at.ty * W + at.tx * E + e] = run[e].A;
+            rb[z][at.ty * W + at.tx * E + e] = run[e].B;
         }
     }
     __syncthreads();
-    const Joint<false> to(ra[0], rb[0], part[0], w, at.ny);
-    const Joint<true> back(ra[1], rb[1], part[1], w, at.ny);
+    const Joint<NY, false> to(ra[0], rb[0], part[0]);
+    const Joint<NY, true> back(ra[1], rb[1], part[1]);
     to.own();
     back.own();
     __syncthreads();
-    const int c = t.strip * w + lane_id(), n = at.ny * TT;
-    const bool mine = to.mine && c < p.C;
+    const int c = t.strip * W + lane_id(), n = NY * TT;
+    const bool mine = c < p.C;
     auto forwards = [&] {
         to.enter_own(t.tile > 0 && mine ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f);
     };
@@ -433,8 +469,8 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     float h[E], m[E], hp[TT][E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        h[e] = rb[0][at.ty * w + at.tx * E + e];
-        m[e] = rb[1][at.ty * w + at.tx * E + e];
+        h[e] = rb[0][at.ty * W + at.tx * E + e];
+        m[e] = rb[1][at.ty * W + at.tx * E + e];
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
@@ -446,27 +482,27 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     for (int i = 0; i < TT; ++i) {  // hp: what da is l times
         float x[E];
         xr[i].to(x);
-        if (is.first >> i & 1) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
+        if (is.is_first(i)) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             hp[i][e] = COMP ? h[e] - x[e] : h[e];
-            h[e] = step<COMP>(h[e], d[i][e], x[e]);
+            h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
         }
     }
 #pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
-        if (at.row0 + i >= p.m.rows) continue;
+        if (!is.plain && at.row0 + i >= p.m.rows) continue;
         float dy[E], dx[E], dg[E];
         dr[i].to(dy);
-        if (is.last >> i & 1) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
+        if (is.is_last(i)) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float l = dy[e] + m[e], al = keep(d[i][e], l), cl = rest(d[i][e]);
+            const float l = dy[e] + m[e], al = Decay<T>::keep(d[i][e], l), cl = Decay<T>::rest(d[i][e]);
             dx[e] = COMP ? cl * l : l;
             dg[e] = hp[i][e] * (p.sigmoid ? cl * al : al);
             m[e] = al;
         }
-        if (!(is.in >> i & 1))
+        if (!is.inside(i))
 #pragma unroll
             for (int e = 0; e < E; ++e) dx[e] = dg[e] = 0.f;
         Chans<T, E> ox;
@@ -475,7 +511,7 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
         og.from(dg);
         ox.store((T *)p.dx + (int64_t)(at.row0 + i) * p.C + at.col);
         og.store((G *)p.dg + (int64_t)(at.row0 + i) * p.C + at.col);
-        if (p.dh0 && (is.first >> i & 1)) store_state<E>(p.dh0, seq[k0 + i], p.C, at.col, m);
+        if (is.is_first(i) && p.dh0) store_state<E>(p.dh0, seq[k0 + i], p.C, at.col, m);
     }
     if (p.dh0 && at.ty == 0)
         for (int q = t.tile; q < p.m.nseq; q += p.tiles)
@@ -521,9 +557,9 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_decode_k(gdp_linrec_decode_arg
         float x[E], d[E];
         xr.to(x);
         gr.to(d);
-        decays<E>(d, a.decay == GDP_DECAY_SIGMOID);
+        decays<T>(d, a.decay == GDP_DECAY_SIGMOID);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = a.complement ? step<true>(h[e], d[e], x[e]) : step<false>(h[e], d[e], x[e]);
+        for (int e = 0; e < E; ++e) h[e] = a.complement ? Decay<T>::template step<true>(h[e], d[e], x[e]) : Decay<T>::template step<false>(h[e], d[e], x[e]);
         xr.from(h);
         xr.store(y + t * a.C);
     }
@@ -532,23 +568,13 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_decode_k(gdp_linrec_decode_arg
 
 namespace {
 
-// Rows a thread holds: 8 of 16 bytes, 16 single elements; half of it backwards,
-// where three tensors and two states are held.
-constexpr int rows_of(int E, bool back) { return (E == 1 ? 16 : 8) / (back ? 2 : 1); }
-
-int lanes_log(const LinRec &p, gdp_dtype dtype) {
-    const int E = !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4;
-    int l = 0;
-    while ((E << l) < 64 && (E << l) < p.C) ++l;  // at most 64 channels a block: a wave joins them
-    return l;
-}
-int elems_of(const LinRec &p, gdp_dtype dtype) { return !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4; }
-int strips_of(const LinRec &p, gdp_dtype dtype) {
-    const int w = elems_of(p, dtype) << lanes_log(p, dtype);
-    return (p.C + w - 1) / w;
-}
-int64_t tiles_of(const LinRec &p, gdp_dtype dtype, bool back) {
-    const int64_t per = (int64_t)(LNT >> lanes_log(p, dtype)) * rows_of(elems_of(p, dtype), back);
+// Channels and rows that a thread holds.
+int elems_of(const LinRec &p) { return p.vec ? 4 : 1; }
+constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : (back ? RB : RF); }
+int strips_of(const LinRec &p) { return (p.C + W - 1) / W; }
+int64_t tiles_of(const LinRec &p, bool back) {
+    const int E = elems_of(p);
+    const int64_t per = (int64_t)(LNT / (W / E)) * rows_of(E, back);
     return (p.m.rows + per - 1) / per;
 }
 
@@ -563,7 +589,7 @@ Chain chain_at(char *q, int64_t tiles, int64_t strips, int64_t C) {
 
 template <typename T, typename G, int E, bool COMP>
 hipError_t run_linrec(const LinRec &p, bool back, hipStream_t stream) {
-    const int w = E << p.lognx, strips = (p.C + w - 1) / w;
+    const int strips = strips_of(p);
     const int64_t tiles = p.tiles, words = chain_bytes(tiles, strips, p.C);
     const dim3 grid((unsigned)(tiles * strips));
     constexpr int TF = rows_of(E, false), TB = rows_of(E, true);
@@ -587,12 +613,11 @@ hipError_t run_kind(const LinRec &p, bool back, hipStream_t stream) {
     return p.complement ? run_linrec<T, G, E, true>(p, back, stream) : run_linrec<T, G, E, false>(p, back, stream);
 }
 hipError_t run_types(LinRec p, gdp_dtype dtype, bool back, hipStream_t stream) {
-    p.lognx = lanes_log(p, dtype);
-    const int64_t tiles = tiles_of(p, dtype, back);
+    const int64_t tiles = tiles_of(p, back);
     p.tiles = tiles > 1 ? (int)tiles : 1;
     if (dtype == GDP_F32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);
-    if (p.g32) return p.vec ? run_kind<bf16, float, 8>(p, back, stream) : run_kind<bf16, float, 1>(p, back, stream);
-    return p.vec ? run_kind<bf16, bf16, 8>(p, back, stream) : run_kind<bf16, bf16, 1>(p, back, stream);
+    if (p.g32) return p.vec ? run_kind<bf16, float, 4>(p, back, stream) : run_kind<bf16, float, 1>(p, back, stream);
+    return p.vec ? run_kind<bf16, bf16, 4>(p, back, stream) : run_kind<bf16, bf16, 1>(p, back, stream);
 }
 
 template <typename T, typename G, int E>
@@ -604,13 +629,13 @@ hipError_t run_decode(const gdp_linrec_decode_args &a, hipStream_t stream) {
 
 }  // namespace
 
-bool linrec_fits(const LinRec &p, gdp_dtype dtype, bool backward) {
-    const int64_t tiles = tiles_of(p, dtype, backward), strips = strips_of(p, dtype);
+bool linrec_fits(const LinRec &p, bool backward) {
+    const int64_t tiles = tiles_of(p, backward), strips = strips_of(p);
     return tiles * strips * LNT <= 0xffffffffll && 2 * chain_bytes(tiles, strips, p.C) / 16 <= 0xffffff00ll;
 }
-int64_t linrec_space(const LinRec &p, gdp_dtype dtype, bool backward) {
-    const int64_t tiles = tiles_of(p, dtype, backward);
-    return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, strips_of(p, dtype), p.C) : 0;
+int64_t linrec_space(const LinRec &p, bool backward) {
+    const int64_t tiles = tiles_of(p, backward);
+    return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, strips_of(p), p.C) : 0;
 }
 hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
 hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, true, stream); }

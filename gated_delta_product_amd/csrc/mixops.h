@@ -28,14 +28,14 @@ struct LinRec {
     int C;
     bool vec;  // every row of every tensor starts on 16 bytes, C in whole units
     bool g32, sigmoid, complement;
-    int lognx, tiles;  // set at launch
+    int tiles;  // set at launch
     const float *h0, *dht;
     void *y, *dx, *dg;
     float *ht, *dh0;
     void *space;
 };
-int64_t linrec_space(const LinRec &p, gdp_dtype dtype, bool backward);
-bool linrec_fits(const LinRec &p, gdp_dtype dtype, bool backward);
+int64_t linrec_space(const LinRec &p, bool backward);
+bool linrec_fits(const LinRec &p, bool backward);
 hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream);
 hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream);
 hipError_t launch_linrec_decode(const gdp_linrec_decode_args &a, bool vec, hipStream_t stream);

@@ -77,12 +77,12 @@ __device__ __forceinline__ bool seq_empty(const RowMap &m, int i) {
     return b == e;
 }
 
-// E neighbouring channels as they lie in memory (16 bytes, or one element;
+// E neighbouring channels as they lie in memory (8 or 16 bytes, or one element;
 // 8 float32 are two units).
 template <typename T, int E>
 struct Chans {
     static constexpr int N = (int)(E * sizeof(T) + 15) / 16;
-    typedef typename std::conditional<E == 1, T, uint4>::type U;
+    typedef typename std::conditional<E == 1, T, typename std::conditional<E * sizeof(T) == 8, uint2, uint4>::type>::type U;
     U u[N];
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -99,9 +99,12 @@ struct Chans {
     // Makes the compiler forget what it has formed from the contents, which it
     // would otherwise keep in registers for a second walk over them.
     __device__ __forceinline__ void forget() {
-        if constexpr (E > 1)
+        if constexpr (E * sizeof(T) == 8) {
+            asm volatile("" : "+v"(u[0].x), "+v"(u[0].y));
+        } else if constexpr (E > 1) {
 #pragma unroll
             for (int i = 0; i < N; ++i) asm volatile("" : "+v"(u[i].x), "+v"(u[i].y), "+v"(u[i].z), "+v"(u[i].w));
+        }
     }
     __device__ __forceinline__ void to(float *f) const {
         if constexpr (E == 1) {
@@ -114,10 +117,10 @@ struct Chans {
                 for (int k = 0; k < 4; ++k) f[4 * i + k] = v[k];
             }
         } else {
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            const u32x4 v = __builtin_bit_cast(u32x4, u[0]);
+            typedef uint32_t words __attribute__((ext_vector_type(E / 2)));
+            const words v = __builtin_bit_cast(words, u[0]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < E / 2; ++k) {
                 f[2 * k] = __uint_as_float(v[k] << 16);
                 f[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
             }
@@ -130,31 +133,25 @@ struct Chans {
 #pragma unroll
             for (int i = 0; i < N; ++i) u[i] = __builtin_bit_cast(U, f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]});
         } else {
-            bf16x8 v;
+            typedef __bf16 vec __attribute__((ext_vector_type(E)));
+            vec v;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = (bf16)f[k];
+            for (int k = 0; k < E; ++k) v[k] = (bf16)f[k];
             u[0] = __builtin_bit_cast(U, v);
         }
     }
 };
 
-// The place of one of NT threads: channels col .. col + E of the rows row0 ..
-// row0 + TT; 2^lognx threads side by side hold a row of the block.
-template <int NT, int E, int TT>
+// A thread's place in a block of NX threads side by side and NY one behind the
+// other: channels col .. col + E of the rows row0 .. row0 + TT.
+template <int NX, int NY, int E, int TT>
 struct Place {
-    int nx, ny, tx, ty, col;
+    int tx, ty, col;
     uint32_t tile0, row0;
     bool live;
-    __device__ __forceinline__ Place(int lognx, int C, uint32_t tile, uint32_t strip) {
-        nx = 1 << lognx;
-        ny = NT >> lognx;
-        tx = threadIdx.x & (nx - 1);
-        ty = threadIdx.x >> lognx;
-        col = (int)((strip << lognx) + tx) * E;
-        live = col < C;
-        tile0 = tile * (uint32_t)(ny * TT);
-        row0 = tile0 + ty * TT;
-    }
+    __device__ __forceinline__ Place(int C, uint32_t tile, uint32_t strip)
+        : tx(threadIdx.x % NX), ty(threadIdx.x / NX), col((int)(strip * NX + tx) * E), tile0(tile * (NY * TT)),
+          row0(tile0 + ty * TT), live(col < C) {}
 };
 
 // Walks the rows of a strided [B, T, C] one after the other.

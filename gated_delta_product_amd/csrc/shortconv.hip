@@ -14,6 +14,25 @@ namespace {
 constexpr int CNT = 256;
 constexpr int CTT = 16;
 
+// A thread's place: channels col .. col + E of the rows row0 .. row0 + TT;
+// 2^lognx threads side by side hold a row of the block.
+template <int NT, int E, int TT>
+struct Spot {
+    int nx, ny, tx, ty, col;
+    uint32_t tile0, row0;
+    bool live;
+    __device__ __forceinline__ Spot(int lognx, int C, uint32_t tile, uint32_t strip) {
+        nx = 1 << lognx;
+        ny = NT >> lognx;
+        tx = threadIdx.x & (nx - 1);
+        ty = threadIdx.x >> lognx;
+        col = (int)((strip << lognx) + tx) * E;
+        live = col < C;
+        tile0 = tile * (uint32_t)(ny * TT);
+        row0 = tile0 + ty * TT;
+    }
+};
+
 // The W - 1 inputs before a row, oldest first.
 template <typename T, int E, int W>
 struct Window {
@@ -86,7 +105,7 @@ __global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p) {
     constexpr int TT = CTT;
     __shared__ uint8_t code[CNT * TT];
     __shared__ int seq[CNT * TT];
-    const Place<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
+    const Spot<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
     find_rows<CNT>(p.m, at.tile0, at.ny * TT, code, seq);
     __syncthreads();
     if (!at.live) return;
@@ -125,7 +144,7 @@ __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p) {
     __shared__ uint8_t code[CNT * TT + X];
     __shared__ int seq[CNT * TT + X];
     __shared__ float red[CNT * E];
-    const Place<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
+    const Spot<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
     find_rows<CNT>(p.m, at.tile0, at.ny * TT + X, code, seq);
     __syncthreads();
     float dw[W][E], db[E];

@@ -37,7 +37,10 @@ def gates(g, decay):
 
 
 class Rec:
-    """x, g [rows, C], seqs [(first, end)], h0 [nseq, C] or None."""
+    """x, g [rows, C], seqs [(first, end)], h0 [nseq, C] or None.
+
+    Of rows in bfloat16 the kernels keep 1 - a (`short`): off by a few U of itself, by the power's (2 + |g|) U of a (of
+    a (1 - a) behind a sigmoid), and a state that it decays by a U of the state."""
 
     def __init__(self, x, g, seqs, decay, complement, h0=None):
         self.x, self.seqs, self.decay, self.comp = x.double(), seqs, decay, complement
@@ -51,14 +54,18 @@ class Rec:
         self.prev_err = torch.zeros(n, C, dtype=torch.float64)
         self.ht, self.ht_err = torch.zeros_like(self.h0), torch.zeros_like(self.h0)
         s_abs = self.s.abs()
+        short = x.dtype == torch.bfloat16
+        power = ((3 + g.double().abs()) * self.a).nan_to_num(0.0, 0.0, 0.0) * (self.s if decay == "sigmoid" else 1)
+        self.rest_err = U * (12 * s_abs + (power if short else 0))
+        self.keep_err = self.rest_err + (U if short else 0)
         for i, (b, e) in enumerate(seqs):
             h, ha, er = self.h0[i], self.h0[i].abs(), torch.zeros(C, dtype=torch.float64)
             for t in range(b, e):
                 self.prev[t], self.prev_abs[t], self.prev_err[t] = h, ha, er
                 # a rounding of the step, of the products that carry a state over many rows, and of 1 - a (12 U:
                 # exponential, sum and reciprocal)
-                er = self.a[t] * er + U * (8 * (self.a[t] * ha + self.c[t].abs() * self.x[t].abs())
-                                           + 12 * s_abs[t] * (ha + (self.x[t].abs() if complement else 0))) + TINY * ha
+                er = (self.a[t] * er + 8 * U * (self.a[t] * ha + self.c[t].abs() * self.x[t].abs()) + TINY * ha
+                      + self.keep_err[t] * ha + (self.keep_err[t] * self.x[t].abs() if complement else 0))
                 h = self.a[t] * h + self.c[t] * self.x[t]
                 ha = self.a[t] * ha + self.c[t].abs() * self.x[t].abs()
                 self.h[t], self.h_abs[t], self.err[t] = h, ha, er
@@ -82,14 +89,17 @@ class Rec:
                 l, la = dy[t] + m, dy[t].abs() + ma
                 le = me + U * 2 * la
                 dx[t] = self.c[t] * l
-                dxe[t] = self.c[t].abs() * (le + 13 * U * la)
+                dxe[t] = self.c[t].abs() * (le + 13 * U * la) + (self.rest_err[t] * la if self.comp else 0)
                 core = self.prev[t] - (self.x[t] if self.comp else 0)
                 core_abs = self.prev_abs[t] + (self.x[t].abs() if self.comp else 0)
                 slope = a if self.decay == "log" else a * s
                 dg[t] = slope * l * core
                 dge[t] = slope * (le * core_abs + la * (self.prev_err[t] + U * core_abs) + 30 * U * la * core_abs) + TINY * la * core_abs
+                # a and 1 - a as they are kept
+                dge[t] += la * core_abs * (self.keep_err[t] * (s if self.decay == "sigmoid" else 1)
+                                           + (self.rest_err[t] * a if self.decay == "sigmoid" else 0))
                 m, ma = a * l, a * la
-                me = a * le + U * (6 * ma + 12 * s.abs() * la) + TINY * la
+                me = a * le + 6 * U * ma + self.keep_err[t] * la + TINY * la
             dh0[i], dh0e[i] = m, me
         return (dx, dxe), (dg, dge), (dh0, dh0e)
 
