@@ -75,10 +75,11 @@ gdp_status check_linrec(const char *name, const gdp_linrec_args *a, gdp::LinRec 
     const gdp_status st = check_map(name, a->B, a->T, a->cu_seqlens, a->num_seqs, &p->m);
     if (st != GDP_OK) return st;
     p->C = a->C;
+    p->f32 = a->dtype == GDP_F32;
     p->g32 = a->g_dtype == GDP_F32;
     p->sigmoid = a->decay == GDP_DECAY_SIGMOID;
     p->complement = a->complement != 0;
-    p->vec = a->C % 4 == 0;
+    p->vec = a->C % unit_of(a->dtype) == 0;
     return ok();
 }
 // What the tensors' alignment leaves open: the larger workspace of both.
@@ -140,10 +141,11 @@ gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t wor
     const char *name = "gdp_linrec_fwd";
     gdp::LinRec p;
     TRY(check_linrec(name, a, &p));
+    const int64_t unit = unit_of(a->dtype), gunit = unit_of(a->g_dtype);
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, 4));
-        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, 4));
-        TRY(check_output(name, "y", a->y, a->dtype, &p.vec, 4));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, unit));
+        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, gunit));
+        TRY(check_output(name, "y", a->y, a->dtype, &p.vec, unit));
     }
     TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
     TRY(check_states(name, "ht", a->ht, GDP_F32, &p.vec, 1));
@@ -154,7 +156,7 @@ gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t wor
     TRY(check_space(name, workspace, workspace_bytes, largest_space(p, false)));
     p.space = workspace;
     if (p.m.nseq == 0 || (p.m.rows == 0 && !p.ht)) return ok();
-    return hip_status(gdp::launch_linrec(p, a->dtype, (hipStream_t)stream), name);
+    return hip_status(gdp::launch_linrec(p, false, (hipStream_t)stream), name);
 }
 
 gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, void *workspace, int64_t workspace_bytes,
@@ -162,13 +164,14 @@ gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, v
     const char *name = "gdp_linrec_bwd";
     gdp::LinRec p;
     TRY(check_linrec(name, a, &p));
+    const int64_t unit = unit_of(a->dtype), gunit = unit_of(a->g_dtype);
     if (!d) return fail(GDP_ERR_INVALID, "%s: grads is NULL", name);
     if (p.m.rows > 0) {
-        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, 4));
-        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, 4));
-        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy, 4));
-        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec, 4));
-        TRY(check_output(name, "dg", d->dg, a->g_dtype, &p.vec, 4));
+        TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, unit));
+        TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, gunit));
+        TRY(check_input(name, "dy", d->dy, d->dy_b_stride, d->dy_t_stride, a->B, a->T, a->dtype, &p.vec, &p.dy, unit));
+        TRY(check_output(name, "dx", d->dx, a->dtype, &p.vec, unit));
+        TRY(check_output(name, "dg", d->dg, a->g_dtype, &p.vec, gunit));
     }
     TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
     TRY(check_states(name, "dht", d->dht, GDP_F32, &p.vec, 1));
@@ -184,7 +187,7 @@ gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, v
     TRY(check_space(name, workspace, workspace_bytes, largest_space(p, true)));
     p.space = workspace;
     if (p.m.rows == 0 && !p.dh0) return ok();
-    return hip_status(gdp::launch_linrec_bwd(p, a->dtype, (hipStream_t)stream), name);
+    return hip_status(gdp::launch_linrec(p, true, (hipStream_t)stream), name);
 }
 
 gdp_status gdp_linrec_decode(const gdp_linrec_decode_args *a, void *stream) {
@@ -200,7 +203,7 @@ gdp_status gdp_linrec_decode(const gdp_linrec_decode_args *a, void *stream) {
     bool vec = a->C % unit == 0;
     gdp::Strided x, g;
     TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &vec, &x, unit));
-    TRY(check_input(name, "g", a->g, a->g_n_stride, a->g_t_stride, a->n, a->S, a->g_dtype, &vec, &g, unit));
+    TRY(check_input(name, "g", a->g, a->g_n_stride, a->g_t_stride, a->n, a->S, a->g_dtype, &vec, &g, unit_of(a->g_dtype)));
     TRY(check_output(name, "y", a->y, a->dtype, &vec, unit));
     if (!a->state && a->pool > 0) return fail(GDP_ERR_INVALID, "%s: state is NULL", name);
     TRY(check_states(name, "state", a->state, GDP_F32, &vec, 1));

@@ -15,7 +15,6 @@ namespace gdp {
 namespace {
 
 constexpr int LNT = 256;
-constexpr int RF = 8, RB = 8;
 constexpr int W = 64;  // channels of a block: those that a wave joins, a lane each
 
 // The decay a of a row and channel in one number, by the type of the rows.
@@ -340,11 +339,12 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     constexpr int NX = W / E, NY = LNT / NX;  // threads side by side, and one behind the other
     const Place<NX, NY, E, TT> at(p.C, t.tile, t.strip);
     const int k0 = at.ty * TT;  // the thread's rows in the tile
+    const uint32_t n = at.tile0 < p.m.rows ? min(p.m.rows - at.tile0, (uint32_t)(NY * TT)) : 0;
 
     Chans<T, E> xr[TT];
     Chans<G, E> gr[TT];
-    load_rows<T, E, TT>(xr, p.x, p.m, at.row0, at.col, at.live);
-    load_rows<G, E, TT>(gr, p.g, p.m, at.row0, at.col, at.live);
+    load_rows(xr, p.x, p.m, p.flat, at, n, p.C);
+    load_rows(gr, p.g, p.m, p.flat, at, n, p.C);
     find_rows<LNT>(p.m, at.tile0, NY * TT, code, seq);
     __syncthreads();
 
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     __syncthreads();
     join.enter_own(enters[lane_id()]);
     if (!at.live) return;
+    const TileRows<T> y((T *)p.y + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
     float h[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) h[e] = rb[at.ty * W + at.tx * E + e];
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
         for (int e = 0; e < E; ++e) h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
         Chans<T, E> o;
         o.from(h);
-        o.store((T *)p.y + (int64_t)(at.row0 + i) * p.C + at.col);
+        o.store(y.r, y.off + i * y.step);
         if (is.is_last(i) && p.ht) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
     }
     if (p.ht && at.ty == 0)
@@ -418,12 +419,13 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     constexpr int NX = W / E, NY = LNT / NX;
     const Place<NX, NY, E, TT> at(p.C, t.tile, t.strip);
     const int k0 = at.ty * TT;
+    const uint32_t n = at.tile0 < p.m.rows ? min(p.m.rows - at.tile0, (uint32_t)(NY * TT)) : 0;
 
     Chans<T, E> xr[TT], dr[TT];
     Chans<G, E> gr[TT];
-    load_rows<T, E, TT>(xr, p.x, p.m, at.row0, at.col, at.live);
-    load_rows<G, E, TT>(gr, p.g, p.m, at.row0, at.col, at.live);
-    load_rows<T, E, TT>(dr, p.dy, p.m, at.row0, at.col, at.live);
+    load_rows(xr, p.x, p.m, p.flat, at, n, p.C);
+    load_rows(gr, p.g, p.m, p.flat, at, n, p.C);
+    load_rows(dr, p.dy, p.m, p.flat, at, n, p.C);
     find_rows<LNT>(p.m, at.tile0, NY * TT, code, seq);
     __syncthreads();
 
@@ -453,19 +455,21 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     to.own();
     back.own();
     __syncthreads();
-    const int c = t.strip * W + lane_id(), n = NY * TT;
+    const int c = t.strip * W + lane_id(), end = NY * TT - 1;
     const bool mine = c < p.C;
     auto forwards = [&] {
         to.enter_own(t.tile > 0 && mine ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f);
     };
     if (wave_id() == 0)
         enters[lane_id()] = hand_on<true>(back.all(), ch, p.C, p.tiles, t, c, mine,
-                                          row_last(code[n - 1]) || !(code[n - 1] & ROW_IN), forwards);
+                                          row_last(code[end]) || !(code[end] & ROW_IN), forwards);
     else
         forwards();
     __syncthreads();
     back.enter_own(enters[lane_id()]);
     if (!at.live) return;
+    const TileRows<T> rx((T *)p.dx + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
+    const TileRows<G> rg((G *)p.dg + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
     float h[E], m[E], hp[TT][E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -491,7 +495,6 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     }
 #pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
-        if (!is.plain && at.row0 + i >= p.m.rows) continue;
         float dy[E], dx[E], dg[E];
         dr[i].to(dy);
         if (is.is_last(i)) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
@@ -509,8 +512,8 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
         Chans<G, E> og;
         ox.from(dx);
         og.from(dg);
-        ox.store((T *)p.dx + (int64_t)(at.row0 + i) * p.C + at.col);
-        og.store((G *)p.dg + (int64_t)(at.row0 + i) * p.C + at.col);
+        ox.store(rx.r, rx.off + i * rx.step);
+        og.store(rg.r, rg.off + i * rg.step);
         if (is.is_first(i) && p.dh0) store_state<E>(p.dh0, seq[k0 + i], p.C, at.col, m);
     }
     if (p.dh0 && at.ty == 0)
@@ -569,8 +572,8 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_decode_k(gdp_linrec_decode_arg
 namespace {
 
 // Channels and rows that a thread holds.
-int elems_of(const LinRec &p) { return p.vec ? 4 : 1; }
-constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : (back ? RB : RF); }
+int elems_of(const LinRec &p) { return !p.vec ? 1 : p.f32 ? 4 : 8; }
+constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : E == 4 || !back ? 8 : 4; }
 int strips_of(const LinRec &p) { return (p.C + W - 1) / W; }
 int64_t tiles_of(const LinRec &p, bool back) {
     const int E = elems_of(p);
@@ -612,12 +615,17 @@ template <typename T, typename G, int E>
 hipError_t run_kind(const LinRec &p, bool back, hipStream_t stream) {
     return p.complement ? run_linrec<T, G, E, true>(p, back, stream) : run_linrec<T, G, E, false>(p, back, stream);
 }
-hipError_t run_types(LinRec p, gdp_dtype dtype, bool back, hipStream_t stream) {
+// Whether the rows [B*T] of a tensor lie at even distances, a tile's within reach of 31-bit offsets (TileRows).
+bool even(const Strided &s, const RowMap &m) {
+    return (m.T == m.rows || s.bs == (int64_t)m.T * s.ts) && s.ts <= (1 << 20);
+}
+hipError_t run_types(LinRec p, bool back, hipStream_t stream) {
+    p.flat = even(p.x, p.m) && even(p.g, p.m) && (!back || even(p.dy, p.m));
     const int64_t tiles = tiles_of(p, back);
     p.tiles = tiles > 1 ? (int)tiles : 1;
-    if (dtype == GDP_F32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);
-    if (p.g32) return p.vec ? run_kind<bf16, float, 4>(p, back, stream) : run_kind<bf16, float, 1>(p, back, stream);
-    return p.vec ? run_kind<bf16, bf16, 4>(p, back, stream) : run_kind<bf16, bf16, 1>(p, back, stream);
+    if (p.f32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);
+    if (p.g32) return p.vec ? run_kind<bf16, float, 8>(p, back, stream) : run_kind<bf16, float, 1>(p, back, stream);
+    return p.vec ? run_kind<bf16, bf16, 8>(p, back, stream) : run_kind<bf16, bf16, 1>(p, back, stream);
 }
 
 template <typename T, typename G, int E>
@@ -637,8 +645,7 @@ int64_t linrec_space(const LinRec &p, bool backward) {
     const int64_t tiles = tiles_of(p, backward);
     return tiles > 1 ? (backward ? 2 : 1) * chain_bytes(tiles, strips_of(p), p.C) : 0;
 }
-hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
-hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, true, stream); }
+hipError_t launch_linrec(const LinRec &p, bool backward, hipStream_t stream) { return run_types(p, backward, stream); }
 
 hipError_t launch_linrec_decode(const gdp_linrec_decode_args &a, bool vec, hipStream_t stream) {
     if (a.dtype == GDP_F32) return vec ? run_decode<float, float, 4>(a, stream) : run_decode<float, float, 1>(a, stream);

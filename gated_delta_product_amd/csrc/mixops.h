@@ -27,8 +27,9 @@ struct LinRec {
     Strided x, g, dy;
     int C;
     bool vec;  // every row of every tensor starts on 16 bytes, C in whole units
-    bool g32, sigmoid, complement;
-    int tiles;  // set at launch
+    bool f32, g32, sigmoid, complement;  // f32: x, y, dy, dx
+    int tiles;  // set at launch, as is flat: the rows of x, g, dy lie at even distances
+    bool flat;
     const float *h0, *dht;
     void *y, *dx, *dg;
     float *ht, *dh0;
@@ -36,8 +37,7 @@ struct LinRec {
 };
 int64_t linrec_space(const LinRec &p, bool backward);
 bool linrec_fits(const LinRec &p, bool backward);
-hipError_t launch_linrec(LinRec p, gdp_dtype dtype, hipStream_t stream);
-hipError_t launch_linrec_bwd(LinRec p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_linrec(const LinRec &p, bool backward, hipStream_t stream);
 hipError_t launch_linrec_decode(const gdp_linrec_decode_args &a, bool vec, hipStream_t stream);
 
 struct ShortConv {

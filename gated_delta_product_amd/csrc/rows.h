@@ -96,6 +96,24 @@ struct Chans {
 #pragma unroll
         for (int i = 0; i < N; ++i) ((U *)p)[i] = u[i];
     }
+    __device__ __forceinline__ void load(rsrc_t r, uint32_t off) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(U) == 16) u[i] = buf_load16(r, off + 16 * i);
+            else if constexpr (sizeof(U) == 8) u[i] = buf_load8(r, off);
+            else if constexpr (sizeof(U) == 4) u[i] = buf_load_f32(r, off);
+            else u[i] = __builtin_bit_cast(U, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0));
+        }
+    }
+    __device__ __forceinline__ void store(rsrc_t r, uint32_t off) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(U) == 16) buf_store16(r, off + 16 * i, u[i]);
+            else if constexpr (sizeof(U) == 8) buf_store8(r, off, u[i]);
+            else if constexpr (sizeof(U) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, u[i]), r, (int)off, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, u[i]), r, (int)off, 0, 0);
+        }
+    }
     // Makes the compiler forget what it has formed from the contents, which it
     // would otherwise keep in registers for a second walk over them.
     __device__ __forceinline__ void forget() {
@@ -182,16 +200,36 @@ __device__ __forceinline__ void forget(float (&f)[E]) {
     for (int e = 0; e < E; ++e) asm volatile("" : "+v"(f[e]));
 }
 
-// TT raw rows from row0 on; past the last row, or the last channel, zeros.
-template <typename T, int E, int TT>
-__device__ __forceinline__ void load_rows(Chans<T, E> (&u)[TT], const Strided &x, const RowMap &m, uint32_t row0, int col,
-                                          bool live) {
-    RowWalk<T> at(x, m, row0, col);
+// The rows of a tile, n of them, ts elements apart, as a buffer: a row past the
+// last one, or a thread without channels, reads zeros and writes nothing.  The
+// tile's rows lie within 2^31 bytes.
+template <typename T>
+struct TileRows {
+    rsrc_t r;
+    uint32_t off, step;  // of the thread's first row, and from row to row
+    __device__ __forceinline__ TileRows(const T *tile, int64_t ts, uint32_t n, int C, int row, int col, bool live) {
+        step = (uint32_t)ts * sizeof(T);
+        r = make_rsrc((const void *)uniform_i64((int64_t)tile), __builtin_amdgcn_readfirstlane(n ? (n - 1) * step + C * (uint32_t)sizeof(T) : 0));
+        off = live ? row * step + col * sizeof(T) : 0x80000000u;
+    }
+};
+// TT raw rows of a thread; past the last row, or the last channel, zeros.
+// flat: every row ts behind the one before, and a tile's within 2^31 bytes
+template <typename T, int E, int TT, typename P>
+__device__ __forceinline__ void load_rows(Chans<T, E> (&u)[TT], const Strided &x, const RowMap &m, bool flat, const P &at,
+                                          uint32_t n, int C) {
+    if (flat) {
+        const TileRows<T> rows((const T *)x.p + (int64_t)at.tile0 * x.ts, x.ts, n, C, at.ty * TT, at.col, at.live);
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        u[i].zero();
-        if (live && row0 + i < m.rows) u[i].load(at.p);
-        at.next();
+        for (int i = 0; i < TT; ++i) u[i].load(rows.r, rows.off + i * rows.step);
+    } else {
+        RowWalk<T> row(x, m, at.row0, at.col);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            u[i].zero();
+            if (at.live && at.row0 + i < m.rows) u[i].load(row.p);
+            row.next();
+        }
     }
 }
 
