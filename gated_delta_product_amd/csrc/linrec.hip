@@ -88,16 +88,20 @@ __device__ __forceinline__ Run after(Run all, Run r) {
 
 // ---------------------------------------------------------------- tiles in order
 //
-// Tiles of a strip of channels hand the state on through words in the
-// workspace, cleared before the launch: P of a tile is its Run, H the state
-// after it.  A tile publishes P as soon as its rows are joined, takes the
-// nearest H before it whose successors' P are all there, enters those one
-// after the other, and publishes its own H.  Whichever H that is, the same
-// products and sums are formed in the same order, so the bits do not depend on
-// timing.  A value and its being there are one word, so nothing else has to be
-// ordered: a word of zeros is not there yet, and a zero is kept as -0.  What a
-// tile has published is noted in `flag` too, so that one load of a wave looks
-// at 64 tiles; that is only where to look, and comes in any order.
+// The tiles of a strip of channels, in the order of their chain, hand the state
+// on through words in the workspace, cleared before the launch.  A tile
+// publishes its Run P as soon as its rows are joined.  A few tiles in a row are
+// a group: its last tile publishes the Run G of them all, and, entering G from
+// the state H after the group before, the state after the group.  The state
+// that enters a tile is the H before its group with the P of the group's
+// earlier tiles entered one by one; that H is the nearest one there is with the
+// G since then entered.  So the same products and sums are formed in the same
+// order whatever is found, and the bits do not depend on timing.
+//
+// A value and its being there are one word, so nothing else has to be ordered:
+// a word of zeros is not there yet, and a zero is kept as -0.  What has been
+// published is noted in flags too, so that one load of a wave looks at all that
+// a tile may wait for; they only tell where to look, and come in any order.
 //
 // The tiles of a strip are numbered by a counter in the order in which its
 // blocks start, so every tile before one that waits belongs to a block that runs
@@ -106,10 +110,18 @@ __device__ __forceinline__ Run after(Run all, Run r) {
 typedef unsigned long long u64;
 struct Chain {
     uint32_t *count;  // [strips], COUNT_STEP apart: blocks that have started
-    uint32_t *flag;   // [strips][tiles] 0, 1: P, 2: H
-    u64 *P;           // [tiles][C]
-    uint32_t *H;      // [tiles][C]
+    uint32_t *flag;   // [strips][tiles] 1: P
+    uint32_t *gflag;  // [strips][groups] 1: G, 2: H
+    u64 *P, *G;       // [tiles][C], [groups][C]
+    uint32_t *H;      // [groups][C]
+    int tiles, group, groups;
 };
+// Tiles of a group.  Entered one by one from the nearest state, with some 24
+// tiles of a strip under way, the words a tile reads hold up the rest (128 rows a
+// tile of 32768 x 2048: 84 us for the states, 62 in groups of 8, 64 of 4; the
+// gradients 162 and 157).  A short chain goes without: a step less to wait for
+// (2 x 1024 x 1024 backwards 25 -> 19 us).
+__host__ __device__ inline int group_of(int64_t tiles) { return tiles <= 16 ? 16 : 8; }
 constexpr int COUNT_STEP = 64;     // counters in lines of their own
 constexpr int PATIENCE = 1 << 22;  // looks (seconds) before a tile gives up, with NaN
 
@@ -121,44 +133,118 @@ template <typename T> __device__ __forceinline__ void show(T *p, T x) {
 }
 __device__ __forceinline__ uint32_t not_zero(float x) { return x == 0.f ? 0x80000000u : __float_as_uint(x); }
 __device__ __forceinline__ u64 word(Run r) { return (u64)__float_as_uint(r.B) << 32 | not_zero(r.A); }
-__device__ __forceinline__ Run run_of(u64 w) {
-    return {__uint_as_float((uint32_t)w) + 0.f, __uint_as_float((uint32_t)(w >> 32))};
+__device__ __forceinline__ Run run_of(u64 w) {  // of no word: NaN
+    return w ? Run{__uint_as_float((uint32_t)w) + 0.f, __uint_as_float((uint32_t)(w >> 32))} : Run{-1.f, __builtin_nanf("")};
 }
 
-// The state that enters the pos-th tile of its chain, a channel a lane, by one
-// wave.  P, H and flag are the tile's own words; those of the tile before lie
-// `back` and `step` further.
-__device__ __forceinline__ float entering(const u64 *P, const uint32_t *H, int64_t back, const uint32_t *flag, int step,
-                                          int pos, bool mine) {
-    const int lane = lane_id();
+// Enters the n Runs at `at` (one every C words) into h, the first eight as they
+// were asked for before; one that is not there yet is asked for again.
+__device__ __forceinline__ float enter_words(const u64 *at, int64_t C, int n, u64 (&w)[8], float h, bool mine, int &patience) {
+    for (int k = 0; k < n; k += 8) {
+        if (k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = k + i < n && mine ? look(at + (k + i) * C) : 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < n) {
+                while (!w[i] && --patience > 0) w[i] = look(at + (k + i) * C);
+                h = enter(run_of(w[i]), h);
+            }
+    }
+    return h;
+}
+__device__ __forceinline__ void ask(const u64 *at, int64_t C, int n, u64 (&w)[8], bool mine) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < n && mine ? look(at + i * C) : 1;
+}
+
+// Publishes the Run of tile pos and returns the state that enters it, for the
+// channel c of every lane (mine: it has one), by one wave.  Where that is not
+// wanted, or nothing enters the tile whatever comes before (alone), only the
+// last tile of a group waits.  `meanwhile` is done once P is out.
+template <typename F>
+__device__ __forceinline__ float hand_on(Run own, const Chain &ch, int64_t C, int strip, int pos, int c, bool mine, bool alone,
+                                         bool wanted, F meanwhile) {
+    const int lane = lane_id(), g = pos / ch.group, r = pos - g * ch.group;
+    u64 *P = ch.P + (int64_t)(pos - r) * C + c, *G = ch.G + (int64_t)g * C + c;
+    uint32_t *H = ch.H + (int64_t)g * C + c, *flag = ch.flag + (int64_t)strip * ch.tiles + pos - r,
+             *gflag = ch.gflag + (int64_t)strip * ch.groups + g;
+    const bool more = pos + 1 < ch.tiles, ends = more && r == ch.group - 1;
+    if (more && !ends) {
+        if (mine) show(P + r * C, word(own));
+        if (lane == 0) show(flag + r, 1u);
+    }
+    meanwhile();
+    if ((alone || !wanted) && !ends) return 0.f;
     int patience = PATIENCE, near = -1;
+    bool have = false;
+    u64 w[8], q[8];
+    Run all{1.f, 0.f};
     do {
-        // lane l: the tile l + 1 before; before the first one the state is there, and zero
-        const uint32_t f = lane < pos ? look(flag + (lane + 1) * step) : 2u;
-        const uint64_t some = __ballot(f >= 1), all = __ballot(f == 2);
-        if (all) {
-            const int k = __builtin_ctzll(all);
+        // lanes 0 to 47: the groups before, nearest first (before the first one the state is there, and zero); from 48 on:
+        // the group's earlier tiles
+        const uint32_t f = lane < 48 ? (lane < g ? look(gflag - 1 - lane) : 2u) : lane - 48 < r ? look(flag + lane - 48) : 1u;
+        const uint64_t some = __ballot(f >= 1), done = __ballot(f == 2) & ((1ull << 48) - 1);
+        if (!have && some >> 48 == 0xffff) {
+            have = true;
+            if (ends) {
+                for (int k = 0; k < r; k += 8) {
+                    ask(P + k * C, C, r - k, q, mine);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (k + i < r) {
+                            while (!q[i] && --patience > 0) q[i] = look(P + (k + i) * C);
+                            all = after(all, run_of(q[i]));
+                        }
+                }
+                all = after(all, own);
+                const bool cut = __all(!mine || all.A < 0.f);  // nothing gets past the group
+                if (mine) {
+                    if (cut) show(H, not_zero(all.B));
+                    else show(G, word(all));
+                }
+                if (lane == 0) show(gflag, cut ? 2u : 1u);
+                if (cut && (alone || !wanted)) return 0.f;
+            }
+        }
+        if (have && done) {
+            const int k = __builtin_ctzll(done);
             if (!(~some & ((1ull << k) - 1))) near = k;
         }
         if (near < 0) __builtin_amdgcn_s_sleep(1);
     } while (near < 0 && --patience > 0);
-    if (near < 0) return __builtin_nanf("");
     float h = 0.f;
-    if (near < pos && mine) {
-        uint32_t w;
-        while (!(w = look(H + (near + 1) * back)) && --patience > 0) {}
-        h = w ? __uint_as_float(w) + 0.f : __builtin_nanf("");
+    if (near < 0) {
+        near = 0;
+        patience = 1;
+        h = __builtin_nanf("");
+    } else {
+        // all asked for at once
+        uint32_t first = near < g && mine ? look(H - (near + 1) * C) : 1u;
+        ask(G - near * C, C, near, w, mine);
+        ask(P, C, r, q, mine);
+        while (!first && --patience > 0) first = look(H - (near + 1) * C);
+        h = near == g ? 0.f : first ? __uint_as_float(first) + 0.f : __builtin_nanf("");
+        h = enter_words(G - near * C, C, near, w, h, mine, patience);
     }
-    for (int k = near; k > 0; k -= 8) {
-        u64 w[8];
+    if (ends) {
+        if (mine) show(H, not_zero(enter(all, h)));
+        if (lane == 0) show(gflag, 2u);
+    }
+    return wanted && have ? enter_words(P, C, r, q, h, mine, patience) : h;
+}
+// The state that enters tile pos of a chain that has ended, for a channel.
+__device__ __forceinline__ float handed_on(const Chain &ch, int64_t C, int pos, int c) {
+    const int g = pos / ch.group, r = pos - g * ch.group;
+    const u64 *P = ch.P + (int64_t)(pos - r) * C + c;
+    float h = g > 0 ? __uint_as_float(ch.H[(int64_t)(g - 1) * C + c]) + 0.f : 0.f;
+    for (int k = 0; k < r; k += 8) {
+        u64 q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = k - i > 0 && mine ? look(P + (k - i) * back) : 1;
+        for (int i = 0; i < 8; ++i) q[i] = k + i < r ? P[(k + i) * C] : 1;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (k - i > 0 && mine) {
-                while (!w[i] && --patience > 0) w[i] = look(P + (k - i) * back);
-                h = enter(w[i] ? run_of(w[i]) : Run{-1.f, __builtin_nanf("")}, h);
-            }
+            if (k + i < r) h = enter(run_of(q[i]), h);
     }
     return h;
 }
@@ -207,15 +293,16 @@ struct Kinds {
 };
 
 // A thread's rows from the first to the last: h <- a h + c x
-template <bool COMP, typename T, int E, int TT>
-__device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT], const float (&d)[TT][E], const Kinds<TT> &is,
-                                     const int *seq, const float *h0, int C, int col) {
+template <bool COMP, typename T, int E, int TT, typename F>
+__device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT], F decay, const Kinds<TT> &is, const int *seq,
+                                     const float *h0, int C, int col) {
 #pragma unroll
     for (int e = 0; e < E; ++e) run[e] = {1.f, 0.f};
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        float x[E];
+        float x[E], d[E];
         xr[i].to(x);
+        decay(d, i);
         if (is.is_first(i)) {
             float h[E];
             load_state<E>(h, h0, seq[i], C, col);
@@ -224,8 +311,8 @@ __device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT],
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = Decay<T>::template step<COMP>(run[e].B, d[i][e], x[e]);
-            run[e].A = Decay<T>::keep(d[i][e], run[e].A);
+            run[e].B = Decay<T>::template step<COMP>(run[e].B, d[e], x[e]);
+            run[e].A = Decay<T>::keep(d[e], run[e].A);
         }
         if (!is.inside(i))
 #pragma unroll
@@ -301,36 +388,11 @@ struct Joint {
     }
 };
 
-// The tile's Run goes out, and the state that enters the tile comes back, to
-// the lane of every channel (first wave only); `wait` is done in between.
-template <bool BACK, typename F>
-__device__ __forceinline__ float hand_on(Run all, const Chain &ch, int64_t C, int tiles, const Turn &t, int c, bool mine,
-                                         bool alone, F wait) {
-    float h = 0.f;
-    u64 *P = ch.P + (int64_t)t.tile * C + c;
-    uint32_t *H = ch.H + (int64_t)t.tile * C + c, *flag = ch.flag + (int64_t)t.strip * tiles + t.tile;
-    if (alone || tiles == 1) {  // nothing enters
-        if (tiles > 1) {
-            if (mine) show(H, not_zero(enter(all, h)));
-            if (lane_id() == 0) show(flag, 2u);
-        }
-        wait();
-        return h;
-    }
-    if (mine) show(P, word(all));
-    if (lane_id() == 0) show(flag, 1u);
-    wait();
-    h = entering(P, H, BACK ? C : -C, flag, BACK ? 1 : -1, t.pos, mine);
-    if (mine) show(H, not_zero(enter(all, h)));
-    if (lane_id() == 0) show(flag, 2u);
-    return h;
-}
-
 }  // namespace
 
 // ROWS: y and the final states; without: only H, the state after every tile.
 template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
-__global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int strips) {
+__global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
     __shared__ int seq[LNT / (W / E) * TT];
     __shared__ float ra[LNT * E], rb[LNT * E], enters[W];
@@ -349,14 +411,16 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     __syncthreads();
 
     const Kinds<TT> is(code + k0);
-    float d[TT][E];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        gr[i].to(d[i]);
-        decays<T>(d[i], p.sigmoid);
-    }
+    float d[ROWS ? TT : 1][E];
     Run run[E];
-    walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
+    const auto decay = [&](float (&s)[E], int i) {  // kept for the rows, or formed as they are walked
+        gr[i].to(s);
+        decays<T>(s, p.sigmoid);
+        if constexpr (ROWS)
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[i][e] = s[e];
+    };
+    walk<COMP>(run, xr, decay, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         ra[at.ty * W + at.tx * E + e] = run[e].A;
@@ -368,43 +432,43 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_k(LinRec p, Chain ch, int stri
     __syncthreads();
     const int c = t.strip * W + lane_id();
     if (wave_id() == 0) {
-        const float h = hand_on<false>(join.all(), ch, p.C, p.tiles, t, c, c < p.C,
-                                       row_first(code[0]) || !(code[0] & ROW_IN), [] {});
-        enters[lane_id()] = h;
+        const bool alone = row_first(code[0]) || !(code[0] & ROW_IN);
+        enters[lane_id()] = p.tiles > 1 ? hand_on(join.all(), ch, p.C, t.strip, t.pos, c, c < p.C, alone, ROWS, [] {}) : 0.f;
     }
-    if constexpr (!ROWS) return;
-    __syncthreads();
-    join.enter_own(enters[lane_id()]);
-    if (!at.live) return;
-    const TileRows<T> y((T *)p.y + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
-    float h[E];
+    if constexpr (ROWS) {
+        __syncthreads();
+        join.enter_own(enters[lane_id()]);
+        if (!at.live) return;
+        const TileRows<T> y((T *)p.y + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
+        float h[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = rb[at.ty * W + at.tx * E + e];
+        for (int e = 0; e < E; ++e) h[e] = rb[at.ty * W + at.tx * E + e];
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        xr[i].forget();
-        forget(d[i]);
+        for (int i = 0; i < TT; ++i) {
+            xr[i].forget();
+            forget(d[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            if (!is.inside(i)) continue;
+            float x[E];
+            xr[i].to(x);
+            if (is.is_first(i)) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
+            Chans<T, E> o;
+            o.from(h);
+            o.store(y.r, y.off + i * y.step);
+            if (is.is_last(i) && p.ht) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
+        }
+        if (p.ht && at.ty == 0)
+            for (int q = t.tile; q < p.m.nseq; q += p.tiles)
+                if (seq_empty(p.m, q)) {
+                    float z[E];
+                    load_state<E>(z, p.h0, q, p.C, at.col);
+                    store_state<E>(p.ht, q, p.C, at.col, z);
+                }
     }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-        if (!is.inside(i)) continue;
-        float x[E];
-        xr[i].to(x);
-        if (is.is_first(i)) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
-#pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
-        Chans<T, E> o;
-        o.from(h);
-        o.store(y.r, y.off + i * y.step);
-        if (is.is_last(i) && p.ht) store_state<E>(p.ht, seq[k0 + i], p.C, at.col, h);
-    }
-    if (p.ht && at.ty == 0)
-        for (int q = t.tile; q < p.m.nseq; q += p.tiles)
-            if (seq_empty(p.m, q)) {
-                float z[E];
-                load_state<E>(z, p.h0, q, p.C, at.col);
-                store_state<E>(p.ht, q, p.C, at.col, z);
-            }
 }
 
 // The gradients, tiles from the last to the first; fwd holds the states after
@@ -437,12 +501,16 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
         decays<T>(d[i], p.sigmoid);
     }
     Run run[E];
+    const auto kept = [&](float (&s)[E], int i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] = d[i][e];
+    };
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) forget(d[i]);
         if (z) walk_back(run, dr, d, is, seq + k0, at.live ? p.dht : nullptr, p.C, at.col);
-        else walk<COMP>(run, xr, d, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
+        else walk<COMP>(run, xr, kept, is, seq + k0, at.live ? p.h0 : nullptr, p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             ra[z][at.ty * W + at.tx * E + e] = run[e].A;
@@ -457,14 +525,14 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Cha
     __syncthreads();
     const int c = t.strip * W + lane_id(), end = NY * TT - 1;
     const bool mine = c < p.C;
-    auto forwards = [&] {
-        to.enter_own(t.tile > 0 && mine ? __uint_as_float(fwd.H[(int64_t)(t.tile - 1) * p.C + c]) + 0.f : 0.f);
-    };
-    if (wave_id() == 0)
-        enters[lane_id()] = hand_on<true>(back.all(), ch, p.C, p.tiles, t, c, mine,
-                                          row_last(code[end]) || !(code[end] & ROW_IN), forwards);
-    else
+    const auto forwards = [&] { to.enter_own(p.tiles > 1 && mine ? handed_on(fwd, p.C, t.tile, c) : 0.f); };
+    if (wave_id() == 0 && p.tiles > 1) {
+        const bool alone = row_last(code[end]) || !(code[end] & ROW_IN);
+        enters[lane_id()] = hand_on(back.all(), ch, p.C, t.strip, t.pos, c, mine, alone, true, forwards);
+    } else {
         forwards();
+        if (wave_id() == 0) enters[lane_id()] = 0.f;
+    }
     __syncthreads();
     back.enter_own(enters[lane_id()]);
     if (!at.live) return;
@@ -581,13 +649,22 @@ int64_t tiles_of(const LinRec &p, bool back) {
     return (p.m.rows + per - 1) / per;
 }
 
-// The words of a chain, in whole units of 256 bytes: counters and flags, P, H.
+// The words of a chain, in whole units of 256 bytes: counters and flags, P, G, H.
 int64_t units(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-int64_t flag_bytes(int64_t tiles, int64_t strips) { return units(4 * strips * (COUNT_STEP + tiles)); }
-int64_t chain_bytes(int64_t tiles, int64_t strips, int64_t C) { return flag_bytes(tiles, strips) + units(tiles * C * 12); }
-Chain chain_at(char *q, int64_t tiles, int64_t strips, int64_t C) {
-    char *r = q + flag_bytes(tiles, strips);
-    return Chain{(uint32_t *)q, (uint32_t *)q + strips * COUNT_STEP, (u64 *)r, (uint32_t *)(r + tiles * C * 8)};
+int64_t chain_bytes(int64_t tiles, int64_t strips, int64_t C, char *q = nullptr, Chain *ch = nullptr) {
+    const int64_t group = group_of(tiles), groups = (tiles + group - 1) / group, marks = units(4 * strips * (COUNT_STEP + tiles + groups));
+    if (ch) {
+        ch->count = (uint32_t *)q;
+        ch->flag = ch->count + strips * COUNT_STEP;
+        ch->gflag = ch->flag + strips * tiles;
+        ch->P = (u64 *)(q + marks);
+        ch->G = ch->P + tiles * C;
+        ch->H = (uint32_t *)(ch->G + groups * C);
+        ch->tiles = (int)tiles;
+        ch->group = (int)group;
+        ch->groups = (int)groups;
+    }
+    return marks + units((tiles * 8 + groups * 12) * C);
 }
 
 template <typename T, typename G, int E, bool COMP>
@@ -598,8 +675,8 @@ hipError_t run_linrec(const LinRec &p, bool back, hipStream_t stream) {
     constexpr int TF = rows_of(E, false), TB = rows_of(E, true);
     Chain one{}, two{};
     if (tiles > 1) {
-        one = chain_at((char *)p.space, tiles, strips, p.C);
-        if (back) two = chain_at((char *)p.space + words, tiles, strips, p.C);
+        chain_bytes(tiles, strips, p.C, (char *)p.space, &one);
+        if (back) chain_bytes(tiles, strips, p.C, (char *)p.space + words, &two);
         const int64_t n = (back ? 2 : 1) * words / 16;
         hipLaunchKernelGGL(gdp_linrec_clear_k, dim3((unsigned)((n + LNT - 1) / LNT)), dim3(LNT), 0, stream, (uint4 *)p.space, n);
     }
