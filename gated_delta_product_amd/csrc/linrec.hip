@@ -692,12 +692,8 @@ template <typename T, typename G, int E>
 hipError_t run_kind(const LinRec &p, bool back, hipStream_t stream) {
     return p.complement ? run_linrec<T, G, E, true>(p, back, stream) : run_linrec<T, G, E, false>(p, back, stream);
 }
-// Whether the rows [B*T] of a tensor lie at even distances, a tile's within reach of 31-bit offsets (TileRows).
-bool even(const Strided &s, const RowMap &m) {
-    return (m.T == m.rows || s.bs == (int64_t)m.T * s.ts) && s.ts <= (1 << 20);
-}
 hipError_t run_types(LinRec p, bool back, hipStream_t stream) {
-    p.flat = even(p.x, p.m) && even(p.g, p.m) && (!back || even(p.dy, p.m));
+    p.flat = even_rows(p.x, p.m) && even_rows(p.g, p.m) && (!back || even_rows(p.dy, p.m));
     const int64_t tiles = tiles_of(p, back);
     p.tiles = tiles > 1 ? (int)tiles : 1;
     if (p.f32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);

@@ -22,6 +22,12 @@ struct Strided {
     int64_t bs, ts;
 };
 
+// Whether the rows [B*T] of a tensor lie at even distances, those of a tile
+// within reach of 30-bit offsets.
+inline bool even_rows(const Strided &s, const RowMap &m) {
+    return (m.T == m.rows || s.bs == (int64_t)m.T * s.ts) && s.ts <= (1 << 20);
+}
+
 struct LinRec {
     RowMap m;
     Strided x, g, dy;
@@ -44,8 +50,7 @@ struct ShortConv {
     RowMap m;
     Strided x, dy;
     int C, W, act;
-    bool vec;
-    int lognx, tiles;  // set at launch
+    bool vec, flat;  // flat: the rows of x and dy lie at even distances (set at launch)
     const float *w, *b;
     const void *h0, *dht;  // [nseq, W - 1, C]
     void *y, *ht, *dx, *dh0;
@@ -53,8 +58,8 @@ struct ShortConv {
 };
 int64_t conv_space(const ShortConv &p, gdp_dtype dtype);
 bool conv_fits(const ShortConv &p, gdp_dtype dtype, bool backward);
-hipError_t launch_conv(ShortConv p, gdp_dtype dtype, hipStream_t stream);
-hipError_t launch_conv_bwd(ShortConv p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_conv(const ShortConv &p, gdp_dtype dtype, hipStream_t stream);
+hipError_t launch_conv_bwd(const ShortConv &p, gdp_dtype dtype, hipStream_t stream);
 hipError_t launch_conv_decode(const gdp_conv_decode_args &a, bool vec, hipStream_t stream);
 
 struct Rotary {

@@ -258,15 +258,5 @@ __device__ __forceinline__ float exp_exact(float g) {
     return fabsf(g) < 88.0f ? fmaf(v, l * 0.693147182f, v) : v;
 }
 __device__ __forceinline__ float sigmoid_exact(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_exact(-x)); }
-__device__ __forceinline__ float act_exact(int kind, float x) {
-    if (kind == GDP_ACT_NONE) return x;
-    const float s = sigmoid_exact(x);
-    return kind == GDP_ACT_SILU ? x * s : s;
-}
-__device__ __forceinline__ float act_slope_exact(int kind, float x) {
-    if (kind == GDP_ACT_NONE) return 1.0f;
-    const float s = sigmoid_exact(x), r = sigmoid_exact(-x);
-    return kind == GDP_ACT_SILU ? s * fmaf(x, r, 1.0f) : s * r;
-}
 
 }  // namespace gdp

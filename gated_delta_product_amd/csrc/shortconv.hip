@@ -4,7 +4,8 @@
 // before it (oldest first), and with du = dy act'(u):
 //   dx_s = sum_j w_j du_{s+W-1-j},  dw_j = sum_t du_t x_{t-W+1+j},  db = sum du
 //
-// A thread walks TT rows of E channels with the last W - 1 rows in registers.
+// A thread walks a run of rows of E channels with the last W - 1 rows (and
+// backwards the last W du) in registers, a few rows' loads ahead.
 #include "rows.h"
 
 namespace gdp {
@@ -12,24 +13,56 @@ namespace gdp {
 namespace {
 
 constexpr int CNT = 256;
-constexpr int CTT = 16;
+constexpr int CHUNK = 4;  // rows whose loads are under way together
+// Rows of a thread: forwards 16; backwards so many that with the W - 1 rows
+// behind them, whose du it forms too, they are whole chunks.
+constexpr int run_of(bool back, int W) { return back ? 16 * CHUNK - (W - 1) : 4 * CHUNK; }
 
-// A thread's place: channels col .. col + E of the rows row0 .. row0 + TT;
-// 2^lognx threads side by side hold a row of the block.
-template <int NT, int E, int TT>
-struct Spot {
-    int nx, ny, tx, ty, col;
-    uint32_t tile0, row0;
-    bool live;
-    __device__ __forceinline__ Spot(int lognx, int C, uint32_t tile, uint32_t strip) {
-        nx = 1 << lognx;
-        ny = NT >> lognx;
-        tx = threadIdx.x & (nx - 1);
-        ty = threadIdx.x >> lognx;
-        col = (int)((strip << lognx) + tx) * E;
-        live = col < C;
-        tile0 = tile * (uint32_t)(ny * TT);
-        row0 = tile0 + ty * TT;
+// 1 / (1 + e^-u).  bfloat16: to (2 + |u|) 2^-24, far within the rows' own 2^-9.
+template <typename T> __device__ __forceinline__ float sigmoid_of(float u) {
+    if constexpr (std::is_same<T, float>::value) return sigmoid_exact(u);
+    else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269502f));
+}
+template <typename T> __device__ __forceinline__ float act_of(int kind, float u) {
+    if (kind == GDP_ACT_NONE) return u;
+    const float s = sigmoid_of<T>(u);
+    return kind == GDP_ACT_SILU ? u * s : s;
+}
+template <typename T> __device__ __forceinline__ float act_slope_of(int kind, float u) {
+    if (kind == GDP_ACT_NONE) return 1.0f;
+    const float s = sigmoid_of<T>(u), r = fmaf(-s, s, s);  // s (1 - s)
+    return kind == GDP_ACT_SILU ? fmaf(u, r, s) : r;
+}
+
+// Rows of a strided tensor by their distance from a thread's first one, also
+// in front of it and behind its tile; zeros past the ends of the tensor.
+template <typename T, int E>
+struct Reader {
+    TileRows<T> rows;
+    const Strided &x;
+    const RowMap &m;
+    bool flat, live;
+    uint32_t row0;
+    int col;
+    template <typename P>
+    __device__ __forceinline__ Reader(const Strided &x, const RowMap &m, bool flat, const P &at, int run, int tile_rows, int C)
+        : rows(start(x, m, flat, at, run, tile_rows, C)), x(x), m(m), flat(flat), live(at.live), row0(at.row0), col(at.col) {}
+    // the tile with three rows in front of it and three behind, as far as there are
+    template <typename P>
+    static __device__ __forceinline__ TileRows<T> start(const Strided &x, const RowMap &m, bool flat, const P &at, int run,
+                                                        int tile_rows, int C) {
+        const uint32_t front = at.tile0 < 3 ? at.tile0 : 3, first = at.tile0 - front;
+        const uint32_t n = flat && first < m.rows ? min(m.rows - first, front + tile_rows + 3) : 0;
+        return TileRows<T>((const T *)x.p + (int64_t)first * x.ts, x.ts, n, C, (int)front + at.ty * run, at.col, at.live);
+    }
+    __device__ __forceinline__ void load(Chans<T, E> &u, int i) const {
+        if (flat) {
+            u.load(rows.r, rows.off + (uint32_t)i * rows.step);
+        } else {
+            const int64_t r = (int64_t)row0 + i;
+            u.zero();
+            if (live && r >= 0 && r < m.rows) u.load(RowWalk<T>(x, m, (uint32_t)r, col).p);
+        }
     }
 };
 
@@ -37,19 +70,27 @@ struct Spot {
 template <typename T, int E, int W>
 struct Window {
     float v[W - 1][E];
-    // of the row with this code, in sequence seq (anything where it is in none)
-    __device__ __forceinline__ void start(const ShortConv &p, uint32_t row, uint32_t code, int seq, int col) {
+    // of a sequence's first row
+    __device__ __forceinline__ void start(const ShortConv &p, int seq, int col) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            Chans<T, E> r;
+            r.zero();
+            if (p.h0) r.load((const T *)p.h0 + ((int64_t)seq * (W - 1) + k) * p.C + col);
+            r.to(v[k]);
+        }
+    }
+    // of a thread's first row, with this code, in sequence seq (anything where it is in none)
+    __device__ __forceinline__ void start(const ShortConv &p, const Reader<T, E> &in, uint32_t code, int seq, int col) {
         const int before = (int)rows_before(code);
 #pragma unroll
         for (int k = 1; k < W; ++k) {
             Chans<T, E> r;
-            r.zero();
-            if (!(code & ROW_IN)) {
-            } else if (k <= before) {
-                const RowWalk<T> at(p.x, p.m, row - k, col);
-                r.load(at.p);
-            } else if (p.h0) {
-                r.load((const T *)p.h0 + ((int64_t)seq * (W - 1) + (W - 1 - k + before)) * p.C + col);
+            if (!(code & ROW_IN)) r.zero();
+            else if (k <= before) in.load(r, -k);
+            else {
+                r.zero();
+                if (p.h0) r.load((const T *)p.h0 + ((int64_t)seq * (W - 1) + (W - 1 - k + before)) * p.C + col);
             }
             r.to(v[W - 1 - k]);
         }
@@ -86,8 +127,8 @@ struct Taps {
 
 // Final states (or dh0 from dht) of the empty sequences: those before them.
 template <typename T, int E, int W>
-__device__ __forceinline__ void empty_states(const RowMap &m, const void *from, void *to, int C, int col) {
-    for (int q = blockIdx.x; q < m.nseq; q += gridDim.x)
+__device__ __forceinline__ void empty_states(const RowMap &m, const void *from, void *to, int C, int col, int tile, int tiles) {
+    for (int q = tile; q < m.nseq; q += tiles)
         if (seq_empty(m, q))
             for (int k = 0; k < W - 1; ++k) {
                 Chans<T, E> r;
@@ -98,54 +139,86 @@ __device__ __forceinline__ void empty_states(const RowMap &m, const void *from, 
             }
 }
 
-}  // namespace
-
-template <typename T, int E, int W>
-__global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p) {
-    constexpr int TT = CTT;
-    __shared__ uint8_t code[CNT * TT];
-    __shared__ int seq[CNT * TT];
-    const Spot<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
-    find_rows<CNT>(p.m, at.tile0, at.ny * TT, code, seq);
-    __syncthreads();
-    if (!at.live) return;
-    Taps<E, W> f;
-    f.load(p.w, p.b, at.col);
-    const int k0 = at.ty * TT;
-    Window<T, E, W> win;
-    win.start(p, at.row0, code[k0], seq[k0], at.col);
-    RowWalk<T> in(p.x, p.m, at.row0, at.col);
-    for (int i = 0; i < TT; ++i, in.next()) {
-        const uint32_t c = code[k0 + i];
-        if (!(c & ROW_IN)) continue;
-        if (row_first(c)) win.start(p, at.row0 + i, c, seq[k0 + i], at.col);
-        Chans<T, E> r;
-        float x[E], y[E];
-        r.load(in.p);
-        r.to(x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = act_exact(p.act, f.at(win, x, e));
-        win.push(x);
-        r.from(y);
-        r.store((T *)p.y + (int64_t)(at.row0 + i) * p.C + at.col);
-        if (p.ht && row_last(c))
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-                r.from(win.v[k]);
-                r.store((T *)p.ht + ((int64_t)seq[k0 + i] * (W - 1) + k) * p.C + at.col);
-            }
-    }
-    if (p.ht && at.ty == 0) empty_states<T, E, W>(p.m, p.h0, p.ht, p.C, at.col);
+// Whether none of the wave's rows is outside the sequences or within three of
+// an end: nothing has to be asked row by row then.
+__device__ __forceinline__ bool plain_rows(const uint8_t *code, int n) {
+    bool odd = false;
+    for (int i = 0; i < n; ++i) odd = odd || code[i] != (ROW_IN | 3 << 1 | 3 << 3);
+    return !__any(odd);
 }
 
-template <typename T, int E, int W>
-__global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p) {
-    constexpr int TT = CTT, X = W - 1;
-    __shared__ uint8_t code[CNT * TT + X];
-    __shared__ int seq[CNT * TT + X];
+}  // namespace
+
+template <typename T, int E, int W, int NX>
+__global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p, int strips, int tiles) {
+    constexpr int NY = CNT / NX, TT = run_of(false, W);
+    __shared__ uint8_t code[NY * TT];
+    __shared__ int seq[NY * TT];
+    const uint32_t tile = blockIdx.x / (uint32_t)strips, strip = blockIdx.x - tile * strips;
+    const Place<NX, NY, E, TT> at(p.C, tile, strip);
+    const Reader<T, E> in(p.x, p.m, p.flat, at, TT, NY * TT, p.C);
+    Chans<T, E> next[CHUNK];
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) in.load(next[i], i);
+    find_rows<CNT>(p.m, at.tile0, NY * TT, code, seq);
+    __syncthreads();
+    if (!at.live) return;
+    const int k0 = at.ty * TT;
+    Taps<E, W> f;
+    f.load(p.w, p.b, at.col);
+    Window<T, E, W> win;
+    win.start(p, in, code[k0], seq[k0], at.col);
+    const bool plain = plain_rows(code + k0, TT);
+    const uint32_t n = at.tile0 < p.m.rows ? min(p.m.rows - at.tile0, (uint32_t)(NY * TT)) : 0;
+    const TileRows<T> y((T *)p.y + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
+#pragma unroll
+    for (int i0 = 0; i0 < TT; i0 += CHUNK) {
+        Chans<T, E> raw[CHUNK];
+#pragma unroll
+        for (int i = 0; i < CHUNK; ++i) raw[i] = next[i];
+        if (i0 + CHUNK < TT)
+#pragma unroll
+            for (int i = 0; i < CHUNK; ++i) in.load(next[i], i0 + CHUNK + i);
+#pragma unroll
+        for (int i = 0; i < CHUNK; ++i) {
+            const int k = k0 + i0 + i;
+            const uint32_t c = plain ? 0u : code[k];
+            if (!plain && !(c & ROW_IN)) continue;
+            if (!plain && row_first(c)) win.start(p, seq[k], at.col);
+            float x[E], o[E];
+            raw[i].to(x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = act_of<T>(p.act, f.at(win, x, e));
+            win.push(x);
+            raw[i].from(o);
+            raw[i].store(y.r, y.off + (i0 + i) * y.step);
+            if (!plain && row_last(c) && p.ht)
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    raw[i].from(win.v[j]);
+                    raw[i].store((T *)p.ht + ((int64_t)seq[k] * (W - 1) + j) * p.C + at.col);
+                }
+        }
+    }
+    if (p.ht && at.ty == 0) empty_states<T, E, W>(p.m, p.h0, p.ht, p.C, at.col, tile, tiles);
+}
+
+template <typename T, int E, int W, int NX>
+__global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p, int strips, int tiles) {
+    constexpr int NY = CNT / NX, TT = run_of(true, W), X = W - 1, CW = NX * E;
+    __shared__ uint8_t code[NY * TT + X];
+    __shared__ int seq[NY * TT + X];
     __shared__ float red[CNT * E];
-    const Spot<CNT, E, TT> at(p.lognx, p.C, blockIdx.x, blockIdx.y);
-    find_rows<CNT>(p.m, at.tile0, at.ny * TT + X, code, seq);
+    const uint32_t tile = blockIdx.x / (uint32_t)strips, strip = blockIdx.x - tile * strips;
+    const Place<NX, NY, E, TT> at(p.C, tile, strip);
+    const Reader<T, E> in(p.x, p.m, p.flat, at, TT, NY * TT, p.C), dn(p.dy, p.m, p.flat, at, TT, NY * TT, p.C);
+    Chans<T, E> nx[CHUNK], nd[CHUNK];
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) {
+        in.load(nx[i], i);
+        dn.load(nd[i], i);
+    }
+    find_rows<CNT>(p.m, at.tile0, NY * TT + X, code, seq);
     __syncthreads();
     float dw[W][E], db[E];
 #pragma unroll
@@ -159,100 +232,121 @@ __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p) {
         f.load(p.w, p.b, at.col);
         const int k0 = at.ty * TT;
         Window<T, E, W> win;
-        win.start(p, at.row0, code[k0], seq[k0], at.col);
-        RowWalk<T> in(p.x, p.m, at.row0, at.col), dn(p.dy, p.m, at.row0, at.col);
-        float du[W][E];  // of the rows r - X .. r
+        win.start(p, in, code[k0], seq[k0], at.col);
+        const bool plain = plain_rows(code + k0, TT + X);
+        const uint32_t n = at.tile0 < p.m.rows ? min(p.m.rows - at.tile0, (uint32_t)(NY * TT)) : 0;
+        const TileRows<T> out((T *)p.dx + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
+        float du[W][E];  // of the rows i - X .. i
 #pragma unroll
         for (int j = 0; j < W; ++j)
 #pragma unroll
             for (int e = 0; e < E; ++e) du[j][e] = 0.f;
-        for (int i = 0; i < TT + X; ++i, in.next(), dn.next()) {
-            const uint32_t c = code[k0 + i];
+#pragma unroll 1
+        for (int i0 = 0; i0 < TT + X; i0 += CHUNK) {
+            Chans<T, E> rx[CHUNK], rd[CHUNK];
 #pragma unroll
-            for (int j = 0; j < X; ++j)
-#pragma unroll
-                for (int e = 0; e < E; ++e) du[j][e] = du[j + 1][e];
-            if (c & ROW_IN) {
-                if (row_first(c)) win.start(p, at.row0 + i, c, seq[k0 + i], at.col);
-                Chans<T, E> r;
-                float x[E], d[E];
-                r.load(in.p);
-                r.to(x);
-                r.load(dn.p);
-                r.to(d);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float u = d[e] * act_slope_exact(p.act, f.at(win, x, e));
-                    du[X][e] = u;
-                    if (i < TT) {
-                        db[e] += u;
-#pragma unroll
-                        for (int j = 0; j < X; ++j) dw[j][e] = fmaf(u, win.v[j][e], dw[j][e]);
-                        dw[X][e] = fmaf(u, x[e], dw[X][e]);
-                    }
-                }
-                win.push(x);
+            for (int i = 0; i < CHUNK; ++i) {
+                rx[i] = nx[i];
+                rd[i] = nd[i];
             }
-            if (i < X) continue;
-            // row s = r - X: its du and those of the rows behind it are du[0 .. X]
-            const uint32_t s = at.row0 + i - X, cs = code[k0 + i - X];
-            if (s >= p.m.rows) continue;
-            const int behind = (int)rows_behind(cs), q = seq[k0 + i - X];
-            Chans<T, E> r;
-            float dx[E];
+            if (i0 + CHUNK < TT + X)
 #pragma unroll
-            for (int e = 0; e < E; ++e) dx[e] = 0.f;
-            if (cs & ROW_IN) {
+                for (int i = 0; i < CHUNK; ++i) {
+                    in.load(nx[i], i0 + CHUNK + i);
+                    dn.load(nd[i], i0 + CHUNK + i);
+                }
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (j <= behind)
+            for (int i = 0; i < CHUNK; ++i) {
+                const int k = i0 + i;
+                const uint32_t c = plain ? ROW_IN : code[k0 + k];
+#pragma unroll
+                for (int j = 0; j < X; ++j)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) du[j][e] = du[j + 1][e];
+                if (plain || (c & ROW_IN)) {
+                    if (!plain && row_first(c)) win.start(p, seq[k0 + k], at.col);
+                    float x[E], d[E];
+                    rx[i].to(x);
+                    rd[i].to(d);
+                    const bool own = k < TT;  // the rows behind are another thread's for the sums
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float u = d[e] * act_slope_of<T>(p.act, f.at(win, x, e)), s = own ? u : 0.f;
+                        du[X][e] = u;
+                        db[e] += s;
+                        if (own) {
+#pragma unroll
+                            for (int j = 0; j < X; ++j) dw[j][e] = fmaf(s, win.v[j][e], dw[j][e]);
+                            dw[X][e] = fmaf(s, x[e], dw[X][e]);
+                        }
+                    }
+                    win.push(x);
+                }
+                if (k < X) continue;
+                // row s = k - X: its du and those of the rows behind it are du[0 .. X]
+                const int s = k - X;
+                Chans<T, E> r;
+                float dx[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) dx[e] = 0.f;
+                if (plain) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
 #pragma unroll
                         for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
-                if (p.dht && behind < X) {
-                    float z[E];
-                    r.load((const T *)p.dht + ((int64_t)q * X + X - 1 - behind) * p.C + at.col);
-                    r.to(z);
+                } else if (const uint32_t cs = code[k0 + s]; cs & ROW_IN) {
+                    const int behind = (int)rows_behind(cs), q = seq[k0 + s];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) dx[e] += z[e];
-                }
-                if (p.dh0 && row_first(cs))
+                    for (int j = 0; j < W; ++j)
+                        if (j <= behind)
 #pragma unroll
-                    for (int k = 0; k < X; ++k) {  // state row k: read by the taps k - d of the rows d behind the first
+                            for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
+                    if (p.dht && behind < X) {
                         float z[E];
+                        r.load((const T *)p.dht + ((int64_t)q * X + X - 1 - behind) * p.C + at.col);
+                        r.to(z);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) z[e] = 0.f;
-                        if (p.dht && k > behind) {  // a sequence so short that its final state still holds the row
-                            r.load((const T *)p.dht + ((int64_t)q * X + k - 1 - behind) * p.C + at.col);
-                            r.to(z);
-                        }
-#pragma unroll
-                        for (int d = 0; d <= k; ++d)
-                            if (d <= behind)
-#pragma unroll
-                                for (int e = 0; e < E; ++e) z[e] = fmaf(f.w[e][k - d], du[d][e], z[e]);
-                        r.from(z);
-                        r.store((T *)p.dh0 + ((int64_t)q * X + k) * p.C + at.col);
+                        for (int e = 0; e < E; ++e) dx[e] += z[e];
                     }
+                    if (p.dh0 && row_first(cs))
+#pragma unroll
+                        for (int t = 0; t < X; ++t) {  // state row t: read by the taps t - d of the rows d behind the first
+                            float z[E];
+#pragma unroll
+                            for (int e = 0; e < E; ++e) z[e] = 0.f;
+                            if (p.dht && t > behind) {  // a sequence so short that its final state still holds the row
+                                r.load((const T *)p.dht + ((int64_t)q * X + t - 1 - behind) * p.C + at.col);
+                                r.to(z);
+                            }
+#pragma unroll
+                            for (int d = 0; d <= t; ++d)
+                                if (d <= behind)
+#pragma unroll
+                                    for (int e = 0; e < E; ++e) z[e] = fmaf(f.w[e][t - d], du[d][e], z[e]);
+                            r.from(z);
+                            r.store((T *)p.dh0 + ((int64_t)q * X + t) * p.C + at.col);
+                        }
+                }
+                r.from(dx);
+                r.store(out.r, out.off + s * out.step);
             }
-            r.from(dx);
-            r.store((T *)p.dx + (int64_t)s * p.C + at.col);
         }
-        if (p.dh0 && at.ty == 0) empty_states<T, E, W>(p.m, p.dht, p.dh0, p.C, at.col);
+        if (p.dh0 && at.ty == 0) empty_states<T, E, W>(p.m, p.dht, p.dh0, p.C, at.col, tile, tiles);
     }
     if (!p.part) return;
     // the block's rows: [tiles][W + 1][C]
-    const int w = at.nx * E, c = (int)(blockIdx.y * w) + (int)threadIdx.x;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) red[at.ty * w + at.tx * E + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        for (int e = 0; e < E; ++e) red[at.ty * CW + at.tx * E + e] = j < W ? dw[j < W ? j : 0][e] : db[e];
         __syncthreads();
-        for (int k = threadIdx.x; k < w; k += CNT) {
+        for (int k = threadIdx.x; k < CW; k += CNT) {
             float t = 0.f;
-            for (int y = 0; y < at.ny; ++y) t += red[y * w + k];
-            if (c - (int)threadIdx.x + k < p.C)
-                p.part[((int64_t)blockIdx.x * (W + 1) + j) * p.C + c - threadIdx.x + k] = t;
+#pragma unroll
+            for (int y = 0; y < NY; ++y) t += red[y * CW + k];
+            const int c = (int)strip * CW + k;
+            if (c < p.C) p.part[((int64_t)tile * (W + 1) + j) * p.C + c] = t;
         }
     }
 }
@@ -319,7 +413,7 @@ __global__ void __launch_bounds__(CNT) gdp_conv_decode_k(gdp_conv_decode_args a)
         r.load(xp + t * a.x_t_stride);
         r.to(x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = act_exact(a.activation, f.at(win, x, e));
+        for (int e = 0; e < E; ++e) u[e] = act_of<T>(a.activation, f.at(win, x, e));
         win.push(x);
         r.from(u);
         r.store(y + t * a.C);
@@ -333,40 +427,47 @@ __global__ void __launch_bounds__(CNT) gdp_conv_decode_k(gdp_conv_decode_args a)
 
 namespace {
 
-int elems_of(const ShortConv &p, gdp_dtype dtype) { return !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4; }
-int lanes_log(const ShortConv &p, gdp_dtype dtype) {
-    const int E = elems_of(p, dtype);
-    int l = 0;
-    while (l < 6 && (E << l) < p.C) ++l;
-    return l;
-}
-int64_t tiles_of(const ShortConv &p, gdp_dtype dtype) {
-    const int64_t per = (int64_t)(CNT >> lanes_log(p, dtype)) * CTT;
-    return (p.m.rows + per - 1) / per;
+// Channels of a thread: units of 16 bytes, backwards of 8 in bfloat16 (its
+// sums take the registers).  Narrow rows are walked by fewer threads side by
+// side.
+int elems_of(const ShortConv &p, gdp_dtype dtype, bool back) { return !p.vec ? 1 : dtype == GDP_BF16 && !back ? 8 : 4; }
+int lanes_of(const ShortConv &p, gdp_dtype dtype, bool back) { return p.C > 16 * elems_of(p, dtype, back) ? 64 : 16; }
+int64_t tiles_of(const ShortConv &p, gdp_dtype dtype, bool back) {
+    const int64_t per = (int64_t)(CNT / lanes_of(p, dtype, back)) * run_of(back, p.W), n = (p.m.rows + per - 1) / per;
+    return n > 0 ? n : 1;
 }
 
-template <typename T, int E, int W>
-hipError_t run_conv(const ShortConv &p, bool back, hipStream_t stream) {
-    const int w = E << p.lognx;
-    const dim3 grid((unsigned)(p.tiles > 0 ? p.tiles : 1), (unsigned)((p.C + w - 1) / w));
-    if (back) hipLaunchKernelGGL((gdp_conv_bwd_k<T, E, W>), grid, dim3(CNT), 0, stream, p);
-    else hipLaunchKernelGGL((gdp_conv_k<T, E, W>), grid, dim3(CNT), 0, stream, p);
+template <typename T, int E, int W, int NX>
+hipError_t run_lanes(const ShortConv &p, int64_t tiles, bool back, hipStream_t stream) {
+    const int strips = (p.C + NX * E - 1) / (NX * E);
+    const dim3 grid((unsigned)(tiles * strips));  // a tile's strips side by side: whole rows are under way at once
+    // forwards and backwards differ in E: each is built for its own
+    if constexpr (E != 8) {
+        if (back) hipLaunchKernelGGL((gdp_conv_bwd_k<T, E, W, NX>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+    }
+    if constexpr (!(E == 4 && std::is_same<T, bf16>::value)) {
+        if (!back) hipLaunchKernelGGL((gdp_conv_k<T, E, W, NX>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+    }
     return hipGetLastError();
 }
 template <typename T, int E>
-hipError_t run_width(const ShortConv &p, bool back, hipStream_t stream) {
+hipError_t run_width(const ShortConv &p, gdp_dtype dtype, bool back, hipStream_t stream) {
+    const int64_t tiles = tiles_of(p, dtype, back);
+    const bool wide = lanes_of(p, dtype, back) == 64;
     switch (p.W) {
-    case 2: return run_conv<T, E, 2>(p, back, stream);
-    case 3: return run_conv<T, E, 3>(p, back, stream);
-    case 4: return run_conv<T, E, 4>(p, back, stream);
+    case 2: return wide ? run_lanes<T, E, 2, 64>(p, tiles, back, stream) : run_lanes<T, E, 2, 16>(p, tiles, back, stream);
+    case 3: return wide ? run_lanes<T, E, 3, 64>(p, tiles, back, stream) : run_lanes<T, E, 3, 16>(p, tiles, back, stream);
+    case 4: return wide ? run_lanes<T, E, 4, 64>(p, tiles, back, stream) : run_lanes<T, E, 4, 16>(p, tiles, back, stream);
     }
     return hipErrorInvalidValue;
 }
 hipError_t run_types(ShortConv p, gdp_dtype dtype, bool back, hipStream_t stream) {
-    p.lognx = lanes_log(p, dtype);
-    p.tiles = (int)tiles_of(p, dtype);
-    if (dtype == GDP_BF16) return p.vec ? run_width<bf16, 8>(p, back, stream) : run_width<bf16, 1>(p, back, stream);
-    return p.vec ? run_width<float, 4>(p, back, stream) : run_width<float, 1>(p, back, stream);
+    p.flat = even_rows(p.x, p.m) && (!back || even_rows(p.dy, p.m));
+    switch (elems_of(p, dtype, back)) {
+    case 8: return run_width<bf16, 8>(p, dtype, back, stream);
+    case 4: return dtype == GDP_BF16 ? run_width<bf16, 4>(p, dtype, back, stream) : run_width<float, 4>(p, dtype, back, stream);
+    default: return dtype == GDP_BF16 ? run_width<bf16, 1>(p, dtype, back, stream) : run_width<float, 1>(p, dtype, back, stream);
+    }
 }
 
 template <typename T, int E>
@@ -384,18 +485,19 @@ hipError_t run_decode(const gdp_conv_decode_args &a, hipStream_t stream) {
 
 }  // namespace
 
-bool conv_fits(const ShortConv &p, gdp_dtype dtype, bool) { return tiles_of(p, dtype) * CNT <= 0xffffffffll; }
-int64_t conv_space(const ShortConv &p, gdp_dtype dtype) {
-    const int64_t tiles = tiles_of(p, dtype);
-    return (tiles > 0 ? tiles : 1) * (p.W + 1) * p.C * (int64_t)sizeof(float);
+bool conv_fits(const ShortConv &p, gdp_dtype dtype, bool backward) {
+    const int64_t w = lanes_of(p, dtype, backward) * elems_of(p, dtype, backward);
+    return tiles_of(p, dtype, backward) * ((p.C + w - 1) / w) * CNT <= 0xffffffffll;
 }
-hipError_t launch_conv(ShortConv p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
-hipError_t launch_conv_bwd(ShortConv p, gdp_dtype dtype, hipStream_t stream) {
+int64_t conv_space(const ShortConv &p, gdp_dtype dtype) {
+    return tiles_of(p, dtype, true) * (p.W + 1) * p.C * (int64_t)sizeof(float);
+}
+hipError_t launch_conv(const ShortConv &p, gdp_dtype dtype, hipStream_t stream) { return run_types(p, dtype, false, stream); }
+hipError_t launch_conv_bwd(const ShortConv &p, gdp_dtype dtype, hipStream_t stream) {
     const hipError_t e = run_types(p, dtype, true, stream);
     if (e != hipSuccess || !p.part) return e;
-    const int64_t tiles = tiles_of(p, dtype);
     hipLaunchKernelGGL(gdp_conv_sum_k, dim3((unsigned)((p.C + 63) / 64), (unsigned)(p.W + 1)), dim3(64 * CSW), 0, stream,
-                       p.part, tiles > 0 ? tiles : 1, (int64_t)p.C, p.W, p.dw, p.db);
+                       p.part, tiles_of(p, dtype, true), (int64_t)p.C, p.W, p.dw, p.db);
     return hipGetLastError();
 }
 hipError_t launch_conv_decode(const gdp_conv_decode_args &a, bool vec, hipStream_t stream) {
