@@ -13,17 +13,60 @@
 namespace gdp {
 
 namespace {
+
 constexpr int RNT = 256;
 constexpr int MAX_TOK = 64;
-constexpr int MAX_CS = 4096;  // cosine and sine pairs in LDS: 32 KB
+constexpr int MAX_CS = 4096;  // cosine and sine pairs of a block: 32 KB of LDS
+
+// What a thread turns of a head: E elements of both halves, or E elements of
+// neighbouring pairs (a pair where E is 1); or it copies E that are not turned.
+template <typename T, int E, bool INTER>
+struct Piece {
+    Chans<T, E> a, c;
+    __device__ __forceinline__ void load(const T *p, int second) {
+        a.load(p);
+        if (second) c.load(p + second);
+    }
+    __device__ __forceinline__ void store(T *p, int second) const {
+        a.store(p);
+        if (second) c.store(p + second);
+    }
+    __device__ __forceinline__ void turn(const float2 *cs) {
+        float x[E], y[E];
+        a.to(x);
+        if constexpr (INTER && E > 1) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 z = cs[e / 2];
+                const float v = x[e];
+                x[e] = v * z.x - x[e + 1] * z.y;
+                x[e + 1] = v * z.y + x[e + 1] * z.x;
+            }
+            a.from(x);
+        } else {
+            c.to(y);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float2 z = cs[e];
+                const float v = x[e];
+                x[e] = v * z.x - y[e] * z.y;
+                y[e] = v * z.y + y[e] * z.x;
+            }
+            a.from(x);
+            c.from(y);
+        }
+    }
+};
+
 }  // namespace
 
-template <typename T, int E>
-__global__ void __launch_bounds__(RNT) gdp_rotary_k(Rotary p, int ntok) {
+// lanes: threads side by side on the pieces of a token (a power of two)
+template <typename T, int E, bool INTER>
+__global__ void __launch_bounds__(RNT) gdp_rotary_k(Rotary p, int ntok, int lanes_log) {
     __shared__ uint8_t code[MAX_TOK];
     __shared__ int seq[MAX_TOK];
     __shared__ double pos[MAX_TOK];
-    __shared__ float2 cs[MAX_CS];
+    extern __shared__ float2 cs[];  // [ntok][R / 2]
     const uint32_t r0 = blockIdx.x * (uint32_t)ntok;
     const int half = p.R / 2;
     find_rows<RNT>(p.m, r0, ntok, code, seq);
@@ -48,87 +91,70 @@ __global__ void __launch_bounds__(RNT) gdp_rotary_k(Rotary p, int ntok) {
         cs[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
     }
     __syncthreads();
-    // units of a head: E elements of each of the two halves, or E elements of
-    // pairs; then what is not rotated
-    const int turn = p.interleaved ? p.R / E : half / E, rest = (p.D - p.R) / E, per = turn + rest;
-    const int heads = p.H[0] + p.H[1], items = heads * per;
-    for (int it = threadIdx.x; it < ntok * items; it += RNT) {
-        const int tok = it / items, w = it - tok * items, head = w / per, u = w - head * per;
-        if (!(code[tok] & ROW_IN)) continue;
-        const int which = head >= p.H[0];
-        const int64_t col = (int64_t)(head - (which ? p.H[0] : 0)) * p.D;
-        const uint32_t r = r0 + tok, b = p.m.cu ? 0 : (uint32_t)seq[tok], t = r - b * (p.m.cu ? 0 : p.m.T);
+    constexpr int STEP = INTER && E == 1 ? 2 : E;  // elements from one turned piece to the next
+    const int turned = INTER ? p.R / STEP : half / E, per = turned + (p.D - p.R) / E;
+    const int pieces = (p.H[0] + p.H[1]) * per, lanes = 1 << lanes_log, rows = RNT >> lanes_log;
+    for (int w = threadIdx.x & (lanes - 1); w < pieces; w += lanes) {
+        const int head = w / per, u = w - head * per, which = head >= p.H[0];
+        const bool turn = u < turned;
+        const int at = turn ? u * STEP : p.R + (u - turned) * E, second = !turn || (INTER && E > 1) ? 0 : INTER ? 1 : half;
+        const int64_t col = (int64_t)(head - (which ? p.H[0] : 0)) * p.D + at;
+        const int f = INTER ? at / 2 : at;  // first frequency of the piece
         const Strided &si = p.in[which], &so = p.out[which];
-        const T *in = (const T *)si.p + b * si.bs + t * si.ts + col;
-        T *out = (T *)so.p + b * so.bs + t * so.ts + col;
-        Chans<T, E> a, c;
-        if (u >= turn) {
-            a.load(in + p.R + (u - turn) * E);
-            a.store(out + p.R + (u - turn) * E);
-            continue;
-        }
-        float x[E], y[E];
-        if (!p.interleaved) {
-            a.load(in + u * E);
-            c.load(in + half + u * E);
-            a.to(x);
-            c.to(y);
+        if (!turn && si.p == so.p) continue;  // already there
+        const auto place = [&](const Strided &s, int tok) {
+            const uint32_t r = r0 + tok, b = p.m.cu ? 0 : (uint32_t)seq[tok], t = r - b * (p.m.cu ? 0 : p.m.T);
+            return (T *)s.p + b * s.bs + t * s.ts + col;
+        };
+        // a few tokens' loads under way together (32768 x 32 heads interleaved, of 2 / 4 / 8 tokens 100 / 98 / 114 us;
+        // halves are two loads: 15151 x 20 heads, 1 / 2 / 4 pairs of loads 29 / 27 / 31)
+        constexpr int N = INTER && E > 1 ? 4 : 2;
+        for (int t0 = threadIdx.x >> lanes_log; t0 < ntok; t0 += N * rows) {
+            Piece<T, E, INTER> x[N];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 z = cs[tok * half + u * E + e];
-                const float v = x[e];
-                x[e] = v * z.x - y[e] * z.y;
-                y[e] = v * z.y + y[e] * z.x;
+            for (int j = 0; j < N; ++j) {
+                const int tok = t0 + j * rows;
+                if (tok < ntok && (code[tok] & ROW_IN)) x[j].load(place(si, tok), second);
             }
-            a.from(x);
-            c.from(y);
-            a.store(out + u * E);
-            c.store(out + half + u * E);
-        } else if constexpr (E > 1) {
-            a.load(in + u * E);
-            a.to(x);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 z = cs[tok * half + (u * E + e) / 2];
-                const float v = x[e];
-                x[e] = v * z.x - x[e + 1] * z.y;
-                x[e + 1] = v * z.y + x[e + 1] * z.x;
+            for (int j = 0; j < N; ++j) {
+                const int tok = t0 + j * rows;
+                if (tok < ntok && (code[tok] & ROW_IN)) {
+                    if (turn) x[j].turn(cs + tok * half + f);
+                    x[j].store(place(so, tok), second);
+                }
             }
-            a.from(x);
-            a.store(out + u * E);
-        } else if (u % 2 == 0) {  // a pair by its first element
-            a.load(in + u);
-            c.load(in + u + 1);
-            a.to(x);
-            c.to(y);
-            const float2 z = cs[tok * half + u / 2];
-            const float v = x[0];
-            x[0] = v * z.x - y[0] * z.y;
-            y[0] = v * z.y + y[0] * z.x;
-            a.from(x);
-            c.from(y);
-            a.store(out + u);
-            c.store(out + u + 1);
         }
     }
 }
 
-hipError_t launch_rotary(const Rotary &p, gdp_dtype dtype, hipStream_t stream) {
-    const int half = p.R / 2;
-    int ntok = half > 0 ? MAX_CS / half : MAX_TOK;
-    ntok = ntok > 8 ? 8 : ntok;
-    const int64_t blocks = ((int64_t)p.m.rows + ntok - 1) / ntok;
-    if (blocks == 0) return hipSuccess;
-    if (blocks * RNT > 0xffffffffll) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks);
-    if (dtype == GDP_BF16) {
-        if (p.vec) hipLaunchKernelGGL((gdp_rotary_k<bf16, 8>), grid, dim3(RNT), 0, stream, p, ntok);
-        else hipLaunchKernelGGL((gdp_rotary_k<bf16, 1>), grid, dim3(RNT), 0, stream, p, ntok);
-    } else {
-        if (p.vec) hipLaunchKernelGGL((gdp_rotary_k<float, 4>), grid, dim3(RNT), 0, stream, p, ntok);
-        else hipLaunchKernelGGL((gdp_rotary_k<float, 1>), grid, dim3(RNT), 0, stream, p, ntok);
-    }
+namespace {
+template <typename T, int E>
+hipError_t run_rotary(const Rotary &p, int ntok, int lanes_log, hipStream_t stream) {
+    const dim3 grid((unsigned)(((int64_t)p.m.rows + ntok - 1) / ntok));
+    const size_t lds = (size_t)ntok * (p.R / 2) * sizeof(float2);
+    if (p.interleaved) hipLaunchKernelGGL((gdp_rotary_k<T, E, true>), grid, dim3(RNT), lds, stream, p, ntok, lanes_log);
+    else hipLaunchKernelGGL((gdp_rotary_k<T, E, false>), grid, dim3(RNT), lds, stream, p, ntok, lanes_log);
     return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_rotary(const Rotary &p, gdp_dtype dtype, hipStream_t stream) {
+    if (p.m.rows == 0) return hipSuccess;
+    const int E = !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4, half = p.R / 2;
+    const int turned = p.interleaved ? p.R / (E == 1 ? 2 : E) : half / E;
+    const int64_t pieces = (int64_t)(p.H[0] + p.H[1]) * (turned + (p.D - p.R) / E);
+    int lanes_log = 0;
+    while (lanes_log < 8 && (1 << lanes_log) < pieces) ++lanes_log;
+    // Tokens of a block: four or eight for every thread, few enough for 1024
+    // blocks (one alone: a step of a few tokens is all latency) and for LDS.
+    int ntok = 8 * (RNT >> lanes_log);
+    while (ntok > 1 && p.m.rows / ntok < 1024) ntok /= 2;
+    ntok = ntok > MAX_TOK ? MAX_TOK : ntok;
+    ntok = ntok > MAX_CS / half ? MAX_CS / half : ntok;
+    if (((int64_t)p.m.rows + ntok - 1) / ntok * RNT > 0xffffffffll) return hipErrorInvalidValue;
+    if (dtype == GDP_BF16) return E == 8 ? run_rotary<bf16, 8>(p, ntok, lanes_log, stream) : run_rotary<bf16, 1>(p, ntok, lanes_log, stream);
+    return E == 4 ? run_rotary<float, 4>(p, ntok, lanes_log, stream) : run_rotary<float, 1>(p, ntok, lanes_log, stream);
 }
 
 }  // namespace gdp

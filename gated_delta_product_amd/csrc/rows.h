@@ -238,8 +238,17 @@ template <int E>
 __device__ __forceinline__ void load_state(float (&h)[E], const float *s, int64_t seq, int C, int col) {
     if (s) {
         const float *q = s + seq * C + col;
+        if (E > 1 && !((uintptr_t)s & 15)) {  // C and col are whole units of four
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = q[e];
+            for (int i = 0; i < E / 4; ++i) {
+                const f32x4 v = ((const f32x4 *)q)[i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[4 * i + k] = v[k];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = q[e];
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) h[e] = 0.f;
@@ -248,8 +257,13 @@ __device__ __forceinline__ void load_state(float (&h)[E], const float *s, int64_
 template <int E>
 __device__ __forceinline__ void store_state(float *s, int64_t seq, int C, int col, const float (&h)[E]) {
     float *q = s + seq * C + col;
+    if (E > 1 && !((uintptr_t)s & 15)) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = h[e];
+        for (int i = 0; i < E / 4; ++i) ((f32x4 *)q)[i] = f32x4{h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[e] = h[e];
+    }
 }
 
 // e^g to about an ulp: 2^(g log2 e) with the product's rounding put back

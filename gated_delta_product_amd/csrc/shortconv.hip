@@ -109,11 +109,34 @@ template <int E, int W>
 struct Taps {
     float w[E][W], b[E];
     __device__ __forceinline__ void load(const float *pw, const float *pb, int col) {
+        const float *q = pw + (int64_t)col * W;
+        if (E > 1 && !((uintptr_t)pw & 15)) {  // E W of them in a row: a thread's first is on 16 bytes, as E is 4 or 8
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+            for (int i = 0; i < E * W / 4; ++i) {
+                const f32x4 v = ((const f32x4 *)q)[i];
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[e][j] = pw[(int64_t)(col + e) * W + j];
-            b[e] = pb ? pb[col + e] : 0.f;
+                for (int k = 0; k < 4; ++k) w[(4 * i + k) / W][(4 * i + k) % W] = v[k];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[e][j] = q[e * W + j];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) b[e] = 0.f;
+        if (pb) {
+            if (E > 1 && !((uintptr_t)pb & 15)) {
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    const f32x4 v = ((const f32x4 *)(pb + col))[i];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) b[4 * i + k] = v[k];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) b[e] = pb[col + e];
+            }
         }
     }
     template <typename T>
