@@ -972,6 +972,15 @@ def _channels(t, name, shape, dtypes):
     return s[0], s[1]
 
 
+def _new_like(t, dev):
+    """A contiguous tensor of t's shape and dtype (empty_like takes half of empty's time on the host)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=dev)
+
+
+def _out_like(y, name, t, dev):
+    return _new_like(t, dev) if y is None else _output(y, name, t.shape, t.dtype, dev)
+
+
 def _sequences(cu_seqlens, B):
     if cu_seqlens is None:
         return B
@@ -1023,7 +1032,7 @@ def linrec_fwd(x, g, decay="log", complement=False, cu_seqlens=None, initial_sta
     come from linrec_bwd."""
     dev = _need_cuda(x, g, cu_seqlens, initial_state, y)
     nseq, a = _rec_args(x, g, decay, complement, cu_seqlens, initial_state)
-    y = _output(y, "y", x.shape, x.dtype, dev)
+    y = _out_like(y, "y", x, dev)
     a.y = y.data_ptr()
     ht = None
     if output_final_state:
@@ -1044,8 +1053,8 @@ def linrec_bwd(dy, x, g, decay="log", complement=False, cu_seqlens=None, initial
     nseq, a = _rec_args(x, g, decay, complement, cu_seqlens, initial_state)
     ds = _channels(dy, "dy", x.shape, (x.dtype,))
     _state_of(dht, "dht", (nseq, a.C), torch.float32)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    dx = _new_like(x, dev)
+    dg = _new_like(g, dev)
     dh0 = None if initial_state is None else torch.empty_like(initial_state)
     d = LinrecGrads(dy.data_ptr(), ds[0], ds[1], _at(dht), dx.data_ptr(), dg.data_ptr(), _at(dh0))
     L, pa = lib(), ctypes.byref(a)
@@ -1065,7 +1074,7 @@ def linrec_decode(x, g, state, decay="log", complement=False, slots=None, y=None
     pool = state.shape[0] if state.dim() else 0
     _state_of(state, "state", (pool, C), torch.float32)
     _slots_of(slots, n)
-    y = _output(y, "y", x.shape, x.dtype, dev)
+    y = _out_like(y, "y", x, dev)
     a = LinrecDecodeArgs(n, S, C, code, _dtype_code(g.dtype), DECAYS[decay], 1 if complement else 0, pool, x.data_ptr(),
                          xs[0], xs[1], g.data_ptr(), gs[0], gs[1], state.data_ptr(), _at(slots), y.data_ptr())
     _call(dev, lib().gdp_linrec_decode, ctypes.byref(a))
@@ -1113,7 +1122,7 @@ def conv_fwd(x, weight, bias=None, activation="silu", cu_seqlens=None, initial_s
     y outside every request are not written.  Nothing is recorded for autograd; the gradients come from conv_bwd."""
     dev = _need_cuda(x, weight, bias, cu_seqlens, initial_state, y)
     nseq, a = _conv_args(x, weight, bias, activation, cu_seqlens, initial_state)
-    y = _output(y, "y", x.shape, x.dtype, dev)
+    y = _out_like(y, "y", x, dev)
     a.y = y.data_ptr()
     ht = None
     if output_final_state:
@@ -1131,7 +1140,7 @@ def conv_bwd(dy, x, weight, bias=None, activation="silu", cu_seqlens=None, initi
     nseq, a = _conv_args(x, weight, bias, activation, cu_seqlens, initial_state)
     ds = _channels(dy, "dy", x.shape, (x.dtype,))
     _state_of(dht, "dht", (nseq, a.W - 1, a.C), x.dtype)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dx = _new_like(x, dev)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
     dh0 = None if initial_state is None else torch.empty_like(initial_state)
@@ -1156,7 +1165,7 @@ def conv_decode(x, state, weight, bias=None, activation="silu", slots=None, y=No
     pool = state.shape[0] if state.dim() else 0
     _state_of(state, "state", (pool, W - 1, C), x.dtype)
     _slots_of(slots, n)
-    y = _output(y, "y", x.shape, x.dtype, dev)
+    y = _out_like(y, "y", x, dev)
     a = ConvDecodeArgs(n, S, C, W, _dtype_code(x.dtype), act, pool, x.data_ptr(), xs[0], xs[1], weight.data_ptr(),
                        _at(bias), state.data_ptr(), _at(slots), y.data_ptr())
     _call(dev, lib().gdp_conv_decode, ctypes.byref(a))
@@ -1232,8 +1241,8 @@ def rotary(q, k, freq, positions=None, offsets=None, cu_seqlens=None, interleave
     if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (nseq,) or not offsets.is_contiguous()):
         raise ValueError("offsets must be a contiguous int32 [nseq]")
     if out is None:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        ko = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+        qo = _new_like(q, dev)
+        ko = None if k is None else _new_like(k, dev)
     else:
         qo, ko = out
         if (k is None) != (ko is None):

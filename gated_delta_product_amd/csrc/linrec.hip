@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chai
 // The gradients, tiles from the last to the first; fwd holds the states after
 // the tiles (gdp_linrec_k without ROWS, in the same tiles).
 template <typename T, typename G, int E, int TT, bool COMP>
-__global__ void __launch_bounds__(LNT) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
+__global__ void __launch_bounds__(LNT, E == 8 ? 4 : 1) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
     __shared__ int seq[LNT / (W / E) * TT];
     __shared__ float ra[2][LNT * E], rb[2][LNT * E], enters[W];
