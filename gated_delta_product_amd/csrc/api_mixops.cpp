@@ -38,7 +38,8 @@ gdp_status check_input(const char *name, const char *what, const void *p, int64_
     if ((B > 1 && bs < 0) || (T > 1 && ts < 0)) return fail(GDP_ERR_INVALID, "%s: strides of %s must be >= 0", name, what);
     if ((uintptr_t)p % dsize(dtype)) return fail(GDP_ERR_INVALID, "%s: %s is not aligned to its type", name, what);
     if ((uintptr_t)p % (unit * dsize(dtype)) || (B > 1 && bs % unit) || (T > 1 && ts % unit)) *vec = false;
-    *out = gdp::Strided{p, B > 1 ? bs : 0, T > 1 ? ts : 0};
+    // rows of one token lie a batch stride apart
+    *out = gdp::Strided{p, B > 1 ? bs : 0, T > 1 ? ts : B > 1 ? bs : 0};
     return ok();
 }
 // A contiguous array of states, or NULL.
@@ -149,6 +150,8 @@ gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t wor
     }
     TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
     TRY(check_states(name, "ht", a->ht, GDP_F32, &p.vec, 1));
+    // a first row reads its h0 again where the last row of its sequence may have left ht already
+    if (a->ht && a->ht == a->h0) return fail(GDP_ERR_INVALID, "%s: ht may not be h0", name);
     p.h0 = a->h0;
     p.y = a->y;
     p.ht = a->ht;

@@ -643,11 +643,8 @@ namespace {
 int elems_of(const LinRec &p) { return !p.vec ? 1 : p.f32 ? 4 : 8; }
 constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : E == 4 || !back ? 8 : 4; }
 int strips_of(const LinRec &p) { return (p.C + W - 1) / W; }
-int64_t tiles_of(const LinRec &p, bool back) {
-    const int E = elems_of(p);
-    const int64_t per = (int64_t)(LNT / (W / E)) * rows_of(E, back);
-    return (p.m.rows + per - 1) / per;
-}
+int64_t tile_rows(const LinRec &p, bool back) { return (int64_t)(LNT / (W / elems_of(p))) * rows_of(elems_of(p), back); }
+int64_t tiles_of(const LinRec &p, bool back) { return (p.m.rows + tile_rows(p, back) - 1) / tile_rows(p, back); }
 
 // The words of a chain, in whole units of 256 bytes: counters and flags, P, G, H.
 int64_t units(int64_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -693,7 +690,8 @@ hipError_t run_kind(const LinRec &p, bool back, hipStream_t stream) {
     return p.complement ? run_linrec<T, G, E, true>(p, back, stream) : run_linrec<T, G, E, false>(p, back, stream);
 }
 hipError_t run_types(LinRec p, bool back, hipStream_t stream) {
-    p.flat = even_rows(p.x, p.m) && even_rows(p.g, p.m) && (!back || even_rows(p.dy, p.m));
+    const int64_t rows = tile_rows(p, back);
+    p.flat = even_rows(p.x, p.m, rows) && even_rows(p.g, p.m, rows) && (!back || even_rows(p.dy, p.m, rows));
     const int64_t tiles = tiles_of(p, back);
     p.tiles = tiles > 1 ? (int)tiles : 1;
     if (p.f32) return p.vec ? run_kind<float, float, 4>(p, back, stream) : run_kind<float, float, 1>(p, back, stream);

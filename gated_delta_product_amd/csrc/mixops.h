@@ -22,10 +22,10 @@ struct Strided {
     int64_t bs, ts;
 };
 
-// Whether the rows [B*T] of a tensor lie at even distances, those of a tile
-// within reach of 30-bit offsets.
-inline bool even_rows(const Strided &s, const RowMap &m) {
-    return (m.T == m.rows || s.bs == (int64_t)m.T * s.ts) && s.ts <= (1 << 20);
+// Whether the rows [B*T] of a tensor lie at even distances, those of a tile of
+// `rows` within 2^30 bytes of 4-byte elements.
+inline bool even_rows(const Strided &s, const RowMap &m, int64_t rows) {
+    return (m.T == m.rows || s.bs == (int64_t)m.T * s.ts) && s.ts <= (1 << 28) / rows;
 }
 
 struct LinRec {

@@ -455,8 +455,11 @@ namespace {
 // side.
 int elems_of(const ShortConv &p, gdp_dtype dtype, bool back) { return !p.vec ? 1 : dtype == GDP_BF16 && !back ? 8 : 4; }
 int lanes_of(const ShortConv &p, gdp_dtype dtype, bool back) { return p.C > 16 * elems_of(p, dtype, back) ? 64 : 16; }
+int64_t tile_rows(const ShortConv &p, gdp_dtype dtype, bool back) {
+    return (int64_t)(CNT / lanes_of(p, dtype, back)) * run_of(back, p.W);
+}
 int64_t tiles_of(const ShortConv &p, gdp_dtype dtype, bool back) {
-    const int64_t per = (int64_t)(CNT / lanes_of(p, dtype, back)) * run_of(back, p.W), n = (p.m.rows + per - 1) / per;
+    const int64_t per = tile_rows(p, dtype, back), n = (p.m.rows + per - 1) / per;
     return n > 0 ? n : 1;
 }
 
@@ -485,7 +488,8 @@ hipError_t run_width(const ShortConv &p, gdp_dtype dtype, bool back, hipStream_t
     return hipErrorInvalidValue;
 }
 hipError_t run_types(ShortConv p, gdp_dtype dtype, bool back, hipStream_t stream) {
-    p.flat = even_rows(p.x, p.m) && (!back || even_rows(p.dy, p.m));
+    const int64_t rows = tile_rows(p, dtype, back) + 6;  // and three on either side
+    p.flat = even_rows(p.x, p.m, rows) && (!back || even_rows(p.dy, p.m, rows));
     switch (elems_of(p, dtype, back)) {
     case 8: return run_width<bf16, 8>(p, dtype, back, stream);
     case 4: return dtype == GDP_BF16 ? run_width<bf16, 4>(p, dtype, back, stream) : run_width<float, 4>(p, dtype, back, stream);

@@ -749,7 +749,7 @@ gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm
  *          as they were.  May be x, or g of that dtype, where those are
  *          contiguous too.
  *   ht     [nseq, C] float32 state after each sequence, or NULL (h0, or zero,
- *          for an empty one).  May be h0.
+ *          for an empty one).  It may not overlap h0.
  * States are float32 and y is rounded once; 1 - a is formed without
  * cancellation.  Inputs must be finite but for a log decay of -inf; others
  * reach only later rows of their channel and sequence.

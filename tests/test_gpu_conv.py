@@ -118,6 +118,22 @@ def test_strides(dtype):
     assert torch.equal(G.conv_fwd(one, gpu(w), gpu(b))[0], G.conv_fwd(one.contiguous(), gpu(w), gpu(b))[0])
 
 
+def test_rows_far_apart_and_taps_off_16_bytes():
+    T, C = 1100, 64
+    x, dy, w, b, s0, dht = draw(1, T, C, 4, BF16, 1, 23)
+    how = dict(initial_state=gpu(s0))
+    want = G.conv_fwd(gpu(x), gpu(w), gpu(b), output_final_state=True, **how) + G.conv_bwd(gpu(dy), gpu(x), gpu(w), gpu(b), **how)
+    wide = torch.zeros(1, T, 280000, dtype=BF16, device=DEV)
+    xs = wide[..., 64:64 + C]
+    xs.copy_(gpu(x))
+    wo = torch.zeros(4 * C + 1, device=DEV)[1:].view(C, 4)
+    bo = torch.zeros(C + 1, device=DEV)[1:]
+    wo.copy_(gpu(w))
+    bo.copy_(gpu(b))
+    got = G.conv_fwd(xs, wo, bo, output_final_state=True, **how) + G.conv_bwd(gpu(dy), xs, wo, bo, **how)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
 def test_nothing_of_other_requests_and_gaps():
     T, C, cu = 400, 40, [10, 140, 150, 390]
     x, dy, w, b, s0, dht = draw(1, T, C, 4, F32, 3, 9)

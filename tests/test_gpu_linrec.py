@@ -134,8 +134,8 @@ def test_strides_and_in_place(dtype):
         assert torch.equal(pair[i], want)
 
 
-def test_state_in_place_continues():
-    """ht over h0, and a row cut in two: bit for bit the states of the parts, and the whole to its bound."""
+def test_a_row_cut_in_two():
+    """The states of the first part continue in the second: the whole, to its bound."""
     T, C = 700, 72
     x, g, _, s0, _ = draw(1, T, C, BF16, BF16, "log", 1, 8, slow=True)
     ref = Rec(x[0], g[0], [(0, T)], "log", False, s0)
@@ -143,16 +143,32 @@ def test_state_in_place_continues():
     b, h2 = G.linrec_fwd(gpu(x)[:, 333:], gpu(g)[:, 333:], initial_state=h, output_final_state=True)
     check("y", torch.cat([a, b], 1)[0], ref.h, ref.err)
     check("ht", h2, ref.ht, 2 * ref.ht_err)
-    import ctypes
-    state = gpu(s0).clone()
-    xs, gs = gpu(x)[:, :333].contiguous(), gpu(g)[:, :333].contiguous()
-    y = torch.empty_like(xs)
-    args = G.LinrecArgs(1, 333, C, G.GDP_BF16, G.GDP_BF16, 0, 0, None, 1, xs.data_ptr(), 333 * C, C, gs.data_ptr(),
-                        333 * C, C, state.data_ptr(), y.data_ptr(), state.data_ptr())
-    need = G.lib().gdp_linrec_workspace_bytes(ctypes.byref(args), 0)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
-    G._check(G.lib().gdp_linrec_fwd(ctypes.byref(args), ws.data_ptr(), need, G._stream(xs.device)))
-    assert torch.equal(state, h) and torch.equal(y, a)
+
+
+def test_rows_far_apart():
+    """A narrow slice of very wide rows, rows of one token each, and states off 16 bytes."""
+    T, C = 300, 64
+    x, g, dy, s0, dht = draw(1, T, C, BF16, BF16, "sigmoid", 1, 22)
+    how = dict(decay="sigmoid", initial_state=gpu(s0))
+    want = G.linrec_fwd(gpu(x), gpu(g), output_final_state=True, **how) + G.linrec_bwd(gpu(dy), gpu(x), gpu(g), **how)
+    wide = torch.zeros(1, T, (1 << 20) + 1000 * C, dtype=BF16, device=DEV)
+    xs = wide[..., 64:64 + C]
+    xs.copy_(gpu(x))
+    got = G.linrec_fwd(xs, gpu(g), output_final_state=True, **how) + G.linrec_bwd(gpu(dy), xs, gpu(g), **how)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    off = torch.zeros(C + 1, device=DEV)[1:].view(1, C)
+    off.copy_(gpu(s0))
+    got = G.linrec_fwd(gpu(x), gpu(g), decay="sigmoid", initial_state=off, output_final_state=True)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    many = torch.zeros(T, 2, C, dtype=BF16, device=DEV)[:, :1]  # T batch rows of a token, two tokens apart
+    many.copy_(gpu(x).view(T, 1, C))
+    s = torch.randn(T, C, device=DEV)
+    gs = gpu(g).view(T, 1, C)
+    a = G.linrec_fwd(many, gs, decay="sigmoid", initial_state=s, output_final_state=True)
+    b = G.linrec_fwd(many.contiguous(), gs, decay="sigmoid", initial_state=s, output_final_state=True)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    d = G.linrec_decode(many, gs, s, decay="sigmoid")
+    assert torch.equal(a[0], d) and torch.equal(a[1], s)
 
 
 def test_nothing_of_other_requests_and_gaps():

@@ -63,12 +63,10 @@ def test_linrec_rejects(name, kw, status):
     a = rec(**kw)
     d = B.LinrecGrads(dy=0x60000, dy_b_stride=6400, dy_t_stride=64, dx=0x70000, dg=0x80000)
     L = B.lib()
-    # fewer lanes walk a tile backwards, so that direction's launch is the larger one
     assert L.gdp_linrec_bwd(ctypes.byref(a), ctypes.byref(d), 0x1000000, BIG, None) == status
     assert L.gdp_last_error()
-    if name != "threads":
-        assert L.gdp_linrec_fwd(ctypes.byref(a), 0x1000000, BIG, None) == status
-        assert L.gdp_last_error()
+    assert L.gdp_linrec_fwd(ctypes.byref(a), 0x1000000, BIG, None) == status
+    assert L.gdp_last_error()
 
 
 def test_linrec_rejects_outputs_and_workspaces():
@@ -76,7 +74,7 @@ def test_linrec_rejects_outputs_and_workspaces():
     ok = rec(T=5000)
     need = L.gdp_linrec_workspace_bytes(ctypes.byref(ok), 0)
     assert need > 0
-    for a, ws, n in ((rec(y=None), 0, 0), (rec(y=0x40001), 0, 0), (rec(ht=0x50002), 0, 0), (ok, 0, need),
+    for a, ws, n in ((rec(y=None), 0, 0), (rec(y=0x40001), 0, 0), (rec(ht=0x50002), 0, 0), (rec(ht=0x30000), 0, 0), (ok, 0, need),
                      (ok, 0x1000000, need - 1), (ok, 0x1000010, need)):
         assert L.gdp_linrec_fwd(ctypes.byref(a), ws, n, None) == INV
     assert L.gdp_linrec_fwd(None, None, 0, None) == INV
@@ -157,7 +155,8 @@ def conv(**kw):
 
 @pytest.mark.parametrize("name,kw,status", SHARED_BAD + [
     ("W=1", dict(W=1), UNS), ("W=5", dict(W=5), UNS), ("W=0", dict(W=0), INV), ("activation", dict(activation=3), INV),
-    ("w NULL", dict(w=None), INV), ("w alignment", dict(w=0x20002), INV)], ids=lambda v: v if isinstance(v, str) else "")
+    ("w NULL", dict(w=None), INV), ("w alignment", dict(w=0x20002), INV),
+    ("threads", dict(B=1, T=(1 << 31) - 1, C=65, x_t_stride=65), UNS)], ids=lambda v: v if isinstance(v, str) else "")
 def test_conv_rejects(name, kw, status):
     L = B.lib()
     a = conv(**kw)
