@@ -35,28 +35,28 @@ template <typename T> __device__ __forceinline__ float act_slope_of(int kind, fl
 }
 
 // Rows of a strided tensor by their distance from a thread's first one, also
-// in front of it and behind its tile; zeros past the ends of the tensor.
-template <typename T, int E>
+// in front of it and behind its tile; zeros past the ends of the tensor.  FLAT:
+// they lie at even distances.
+template <typename T, int E, bool FLAT>
 struct Reader {
     TileRows<T> rows;
     const Strided &x;
     const RowMap &m;
-    bool flat, live;
+    bool live;
     uint32_t row0;
     int col;
     template <typename P>
-    __device__ __forceinline__ Reader(const Strided &x, const RowMap &m, bool flat, const P &at, int run, int tile_rows, int C)
-        : rows(start(x, m, flat, at, run, tile_rows, C)), x(x), m(m), flat(flat), live(at.live), row0(at.row0), col(at.col) {}
+    __device__ __forceinline__ Reader(const Strided &x, const RowMap &m, const P &at, int run, int tile_rows, int C)
+        : rows(start(x, m, at, run, tile_rows, C)), x(x), m(m), live(at.live), row0(at.row0), col(at.col) {}
     // the tile with three rows in front of it and three behind, as far as there are
     template <typename P>
-    static __device__ __forceinline__ TileRows<T> start(const Strided &x, const RowMap &m, bool flat, const P &at, int run,
-                                                        int tile_rows, int C) {
+    static __device__ __forceinline__ TileRows<T> start(const Strided &x, const RowMap &m, const P &at, int run, int tile_rows, int C) {
         const uint32_t front = at.tile0 < 3 ? at.tile0 : 3, first = at.tile0 - front;
-        const uint32_t n = flat && first < m.rows ? min(m.rows - first, front + tile_rows + 3) : 0;
+        const uint32_t n = FLAT && first < m.rows ? min(m.rows - first, front + tile_rows + 3) : 0;
         return TileRows<T>((const T *)x.p + (int64_t)first * x.ts, x.ts, n, C, (int)front + at.ty * run, at.col, at.live);
     }
     __device__ __forceinline__ void load(Chans<T, E> &u, int i) const {
-        if (flat) {
+        if constexpr (FLAT) {
             u.load(rows.r, rows.off + (uint32_t)i * rows.step);
         } else {
             const int64_t r = (int64_t)row0 + i;
@@ -81,7 +81,8 @@ struct Window {
         }
     }
     // of a thread's first row, with this code, in sequence seq (anything where it is in none)
-    __device__ __forceinline__ void start(const ShortConv &p, const Reader<T, E> &in, uint32_t code, int seq, int col) {
+    template <bool FLAT>
+    __device__ __forceinline__ void start(const ShortConv &p, const Reader<T, E, FLAT> &in, uint32_t code, int seq, int col) {
         const int before = (int)rows_before(code);
 #pragma unroll
         for (int k = 1; k < W; ++k) {
@@ -172,14 +173,14 @@ __device__ __forceinline__ bool plain_rows(const uint8_t *code, int n) {
 
 }  // namespace
 
-template <typename T, int E, int W, int NX>
+template <typename T, int E, int W, int NX, bool FLAT>
 __global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p, int strips, int tiles) {
     constexpr int NY = CNT / NX, TT = run_of(false, W);
     __shared__ uint8_t code[NY * TT];
     __shared__ int seq[NY * TT];
     const uint32_t tile = blockIdx.x / (uint32_t)strips, strip = blockIdx.x - tile * strips;
     const Place<NX, NY, E, TT> at(p.C, tile, strip);
-    const Reader<T, E> in(p.x, p.m, p.flat, at, TT, NY * TT, p.C);
+    const Reader<T, E, FLAT> in(p.x, p.m, at, TT, NY * TT, p.C);
     Chans<T, E> next[CHUNK];
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i) in.load(next[i], i);
@@ -194,6 +195,26 @@ __global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p, int strips, int t
     const bool plain = plain_rows(code + k0, TT);
     const uint32_t n = at.tile0 < p.m.rows ? min(p.m.rows - at.tile0, (uint32_t)(NY * TT)) : 0;
     const TileRows<T> y((T *)p.y + (int64_t)at.tile0 * p.C, p.C, n, p.C, k0, at.col, true);
+    const auto row = [&](auto is_plain, Chans<T, E> &raw, int i) {
+        constexpr bool PLAIN = decltype(is_plain)::value;
+        const int k = k0 + i;
+        const uint32_t c = PLAIN ? 0u : code[k];
+        if (!PLAIN && !(c & ROW_IN)) return;
+        if (!PLAIN && row_first(c)) win.start(p, seq[k], at.col);
+        float x[E], o[E];
+        raw.to(x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = act_of<T>(p.act, f.at(win, x, e));
+        win.push(x);
+        raw.from(o);
+        raw.store(y.r, y.off + i * y.step);
+        if (!PLAIN && row_last(c) && p.ht)
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                raw.from(win.v[j]);
+                raw.store((T *)p.ht + ((int64_t)seq[k] * (W - 1) + j) * p.C + at.col);
+            }
+    };
 #pragma unroll
     for (int i0 = 0; i0 < TT; i0 += CHUNK) {
         Chans<T, E> raw[CHUNK];
@@ -202,31 +223,19 @@ __global__ void __launch_bounds__(CNT) gdp_conv_k(ShortConv p, int strips, int t
         if (i0 + CHUNK < TT)
 #pragma unroll
             for (int i = 0; i < CHUNK; ++i) in.load(next[i], i0 + CHUNK + i);
+        // one block of code for the chunk where nothing has to be asked
+        if (plain) {
 #pragma unroll
-        for (int i = 0; i < CHUNK; ++i) {
-            const int k = k0 + i0 + i;
-            const uint32_t c = plain ? 0u : code[k];
-            if (!plain && !(c & ROW_IN)) continue;
-            if (!plain && row_first(c)) win.start(p, seq[k], at.col);
-            float x[E], o[E];
-            raw[i].to(x);
+            for (int i = 0; i < CHUNK; ++i) row(std::true_type{}, raw[i], i0 + i);
+        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = act_of<T>(p.act, f.at(win, x, e));
-            win.push(x);
-            raw[i].from(o);
-            raw[i].store(y.r, y.off + (i0 + i) * y.step);
-            if (!plain && row_last(c) && p.ht)
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    raw[i].from(win.v[j]);
-                    raw[i].store((T *)p.ht + ((int64_t)seq[k] * (W - 1) + j) * p.C + at.col);
-                }
+            for (int i = 0; i < CHUNK; ++i) row(std::false_type{}, raw[i], i0 + i);
         }
     }
     if (p.ht && at.ty == 0) empty_states<T, E, W>(p.m, p.h0, p.ht, p.C, at.col, tile, tiles);
 }
 
-template <typename T, int E, int W, int NX>
+template <typename T, int E, int W, int NX, bool FLAT>
 __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p, int strips, int tiles) {
     constexpr int NY = CNT / NX, TT = run_of(true, W), X = W - 1, CW = NX * E;
     __shared__ uint8_t code[NY * TT + X];
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p, int strips, i
     __shared__ float red[CNT * E];
     const uint32_t tile = blockIdx.x / (uint32_t)strips, strip = blockIdx.x - tile * strips;
     const Place<NX, NY, E, TT> at(p.C, tile, strip);
-    const Reader<T, E> in(p.x, p.m, p.flat, at, TT, NY * TT, p.C), dn(p.dy, p.m, p.flat, at, TT, NY * TT, p.C);
+    const Reader<T, E, FLAT> in(p.x, p.m, at, TT, NY * TT, p.C), dn(p.dy, p.m, at, TT, NY * TT, p.C);
     Chans<T, E> nx[CHUNK], nd[CHUNK];
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i) {
@@ -264,6 +273,80 @@ __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p, int strips, i
         for (int j = 0; j < W; ++j)
 #pragma unroll
             for (int e = 0; e < E; ++e) du[j][e] = 0.f;
+        // (asking row by row: code of their own for plain chunks takes 182 registers for 128, 135 us for 130)
+        const auto row = [&](const Chans<T, E> &rx, const Chans<T, E> &rd, int k) {
+            const uint32_t c = plain ? ROW_IN : code[k0 + k];
+#pragma unroll
+            for (int j = 0; j < X; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) du[j][e] = du[j + 1][e];
+            if (plain || (c & ROW_IN)) {
+                if (!plain && row_first(c)) win.start(p, seq[k0 + k], at.col);
+                float x[E], d[E];
+                rx.to(x);
+                rd.to(d);
+                const bool own = k < TT;  // the rows behind are another thread's for the sums
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float u = d[e] * act_slope_of<T>(p.act, f.at(win, x, e)), s = own ? u : 0.f;
+                    du[X][e] = u;
+                    db[e] += s;
+                    if (own) {
+#pragma unroll
+                        for (int j = 0; j < X; ++j) dw[j][e] = fmaf(s, win.v[j][e], dw[j][e]);
+                        dw[X][e] = fmaf(s, x[e], dw[X][e]);
+                    }
+                }
+                win.push(x);
+            }
+            if (k < X) return;
+            // row s = k - X: its du and those of the rows behind it are du[0 .. X]
+            const int s = k - X;
+            Chans<T, E> r;
+            float dx[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) dx[e] = 0.f;
+            if (plain) {
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
+            } else if (const uint32_t cs = code[k0 + s]; cs & ROW_IN) {
+                const int behind = (int)rows_behind(cs), q = seq[k0 + s];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (j <= behind)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
+                if (p.dht && behind < X) {
+                    float z[E];
+                    r.load((const T *)p.dht + ((int64_t)q * X + X - 1 - behind) * p.C + at.col);
+                    r.to(z);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) dx[e] += z[e];
+                }
+                if (p.dh0 && row_first(cs))
+#pragma unroll
+                    for (int t = 0; t < X; ++t) {  // state row t: read by the taps t - d of the rows d behind the first
+                        float z[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) z[e] = 0.f;
+                        if (p.dht && t > behind) {  // a sequence so short that its final state still holds the row
+                            r.load((const T *)p.dht + ((int64_t)q * X + t - 1 - behind) * p.C + at.col);
+                            r.to(z);
+                        }
+#pragma unroll
+                        for (int d = 0; d <= t; ++d)
+                            if (d <= behind)
+#pragma unroll
+                                for (int e = 0; e < E; ++e) z[e] = fmaf(f.w[e][t - d], du[d][e], z[e]);
+                        r.from(z);
+                        r.store((T *)p.dh0 + ((int64_t)q * X + t) * p.C + at.col);
+                    }
+            }
+            r.from(dx);
+            r.store(out.r, out.off + s * out.step);
+        };
 #pragma unroll 1
         for (int i0 = 0; i0 < TT + X; i0 += CHUNK) {
             Chans<T, E> rx[CHUNK], rd[CHUNK];
@@ -279,80 +362,7 @@ __global__ void __launch_bounds__(CNT) gdp_conv_bwd_k(ShortConv p, int strips, i
                     dn.load(nd[i], i0 + CHUNK + i);
                 }
 #pragma unroll
-            for (int i = 0; i < CHUNK; ++i) {
-                const int k = i0 + i;
-                const uint32_t c = plain ? ROW_IN : code[k0 + k];
-#pragma unroll
-                for (int j = 0; j < X; ++j)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) du[j][e] = du[j + 1][e];
-                if (plain || (c & ROW_IN)) {
-                    if (!plain && row_first(c)) win.start(p, seq[k0 + k], at.col);
-                    float x[E], d[E];
-                    rx[i].to(x);
-                    rd[i].to(d);
-                    const bool own = k < TT;  // the rows behind are another thread's for the sums
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float u = d[e] * act_slope_of<T>(p.act, f.at(win, x, e)), s = own ? u : 0.f;
-                        du[X][e] = u;
-                        db[e] += s;
-                        if (own) {
-#pragma unroll
-                            for (int j = 0; j < X; ++j) dw[j][e] = fmaf(s, win.v[j][e], dw[j][e]);
-                            dw[X][e] = fmaf(s, x[e], dw[X][e]);
-                        }
-                    }
-                    win.push(x);
-                }
-                if (k < X) continue;
-                // row s = k - X: its du and those of the rows behind it are du[0 .. X]
-                const int s = k - X;
-                Chans<T, E> r;
-                float dx[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) dx[e] = 0.f;
-                if (plain) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-#pragma unroll
-                        for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
-                } else if (const uint32_t cs = code[k0 + s]; cs & ROW_IN) {
-                    const int behind = (int)rows_behind(cs), q = seq[k0 + s];
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        if (j <= behind)
-#pragma unroll
-                            for (int e = 0; e < E; ++e) dx[e] = fmaf(f.w[e][X - j], du[j][e], dx[e]);
-                    if (p.dht && behind < X) {
-                        float z[E];
-                        r.load((const T *)p.dht + ((int64_t)q * X + X - 1 - behind) * p.C + at.col);
-                        r.to(z);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) dx[e] += z[e];
-                    }
-                    if (p.dh0 && row_first(cs))
-#pragma unroll
-                        for (int t = 0; t < X; ++t) {  // state row t: read by the taps t - d of the rows d behind the first
-                            float z[E];
-#pragma unroll
-                            for (int e = 0; e < E; ++e) z[e] = 0.f;
-                            if (p.dht && t > behind) {  // a sequence so short that its final state still holds the row
-                                r.load((const T *)p.dht + ((int64_t)q * X + t - 1 - behind) * p.C + at.col);
-                                r.to(z);
-                            }
-#pragma unroll
-                            for (int d = 0; d <= t; ++d)
-                                if (d <= behind)
-#pragma unroll
-                                    for (int e = 0; e < E; ++e) z[e] = fmaf(f.w[e][t - d], du[d][e], z[e]);
-                            r.from(z);
-                            r.store((T *)p.dh0 + ((int64_t)q * X + t) * p.C + at.col);
-                        }
-                }
-                r.from(dx);
-                r.store(out.r, out.off + s * out.step);
-            }
+            for (int i = 0; i < CHUNK; ++i) row(rx[i], rd[i], i0 + i);
         }
         if (p.dh0 && at.ty == 0) empty_states<T, E, W>(p.m, p.dht, p.dh0, p.C, at.col, tile, tiles);
     }
@@ -469,10 +479,12 @@ hipError_t run_lanes(const ShortConv &p, int64_t tiles, bool back, hipStream_t s
     const dim3 grid((unsigned)(tiles * strips));  // a tile's strips side by side: whole rows are under way at once
     // forwards and backwards differ in E: each is built for its own
     if constexpr (E != 8) {
-        if (back) hipLaunchKernelGGL((gdp_conv_bwd_k<T, E, W, NX>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+        if (back && p.flat) hipLaunchKernelGGL((gdp_conv_bwd_k<T, E, W, NX, true>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+        else if (back) hipLaunchKernelGGL((gdp_conv_bwd_k<T, E, W, NX, false>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
     }
     if constexpr (!(E == 4 && std::is_same<T, bf16>::value)) {
-        if (!back) hipLaunchKernelGGL((gdp_conv_k<T, E, W, NX>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+        if (!back && p.flat) hipLaunchKernelGGL((gdp_conv_k<T, E, W, NX, true>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
+        else if (!back) hipLaunchKernelGGL((gdp_conv_k<T, E, W, NX, false>), grid, dim3(CNT), 0, stream, p, strips, (int)tiles);
     }
     return hipGetLastError();
 }
