@@ -74,7 +74,8 @@ template <> struct Decay<bf16> {
     static __device__ __forceinline__ float keep(float s, float h) { return fmaf(-s, h, h); }
     static __device__ __forceinline__ float rest(float s) { return s; }
     template <bool COMP> static __device__ __forceinline__ float step(float h, float s, float x) {
-        return COMP ? fmaf(s, x - h, h) : fmaf(-s, h, h) + x;
+        // (h + s (x - h) is an operation less, but at s = 1 a rounding of x - h stays)
+        return COMP ? fmaf(s, x, keep(s, h)) : keep(s, h) + x;
     }
 };
 template <typename T, int N>
