@@ -33,10 +33,14 @@ constexpr int W = 64;  // channels of a block: those that a wave joins, a lane e
 
 // The decay a of a row and channel in one number, by the type of the rows.
 //
-// float32: d, with a = 1 + d where d < 0, else a = d.  Close to one its
-// distance from one is kept, which a rounding of a itself would lose and
-// compound over the rows that a slow channel remembers; a fast channel keeps a.
+// float32: near one its distance a - 1, whose rounding a slow channel does not
+// compound over the rows that it remembers as it would one of a; elsewhere a.
+// The number's last bit says which, so that both a and 1 - a are known to a few
+// 2^-24 of themselves for every a, above one too.
 template <typename T> struct Decay {
+    static __device__ __forceinline__ float near(float m) { return __uint_as_float(__float_as_uint(m) | 1u); }
+    static __device__ __forceinline__ float far(float a) { return __uint_as_float(__float_as_uint(a) & ~1u); }
+    static __device__ __forceinline__ uint32_t is_near(float d) { return (uint32_t)__builtin_amdgcn_sbfe((int)__float_as_uint(d), 0, 1); }
     static __device__ __forceinline__ float log(float g) {
         // e^g - 1 by its series near zero, where the difference would cancel
         float p = fmaf(g, 1.0f / 5040.0f, 1.0f / 720.0f);
@@ -45,16 +49,22 @@ template <typename T> struct Decay {
         p = fmaf(g, p, 1.0f / 6.0f);
         p = fmaf(g, p, 0.5f);
         p = fmaf(g * g, p, g);
-        return g < 0.f && g >= -0.35f ? p : exp_exact(g);
+        return fabsf(g) <= 0.35f ? near(p) : far(exp_exact(g));
     }
     static __device__ __forceinline__ float sigmoid(float g) {
-        const float r = __builtin_amdgcn_rcpf(1.0f + exp_exact(fabsf(g)));
-        return g > 0.f ? -fmaxf(r, 1.17549435e-38f) : r;  // never -0, which would be a = 0
+        const float r = __builtin_amdgcn_rcpf(1.0f + exp_exact(fabsf(g)));  // the smaller one of a and 1 - a
+        return g > 0.f ? near(-r) : far(r);
     }
-    static __device__ __forceinline__ float keep(float d, float h) { return fmaf(d, h, d < 0.f ? h : 0.f); }  // a h
-    static __device__ __forceinline__ float rest(float d) { return d < 0.f ? -d : 1.0f - d; }                 // 1 - a
+    static __device__ __forceinline__ float keep(float d, float h) {  // a h
+        return fmaf(d, h, __uint_as_float(is_near(d) & __float_as_uint(h)));
+    }
+    static __device__ __forceinline__ float rest(float d) {  // 1 - a
+        return __uint_as_float(~is_near(d) & 0x3f800000u) - d;
+    }
+    // a h + (1 - a) x as h + (a - 1) (h - x) or x + a (h - x): no product is larger than what it decays
     template <bool COMP> static __device__ __forceinline__ float step(float h, float d, float x) {
-        return COMP ? fmaf(rest(d), x, keep(d, h)) : keep(d, h) + x;
+        const uint32_t n = is_near(d);
+        return COMP ? fmaf(d, h - x, __uint_as_float((n & __float_as_uint(h)) | (~n & __float_as_uint(x)))) : keep(d, h) + x;
     }
 };
 // bfloat16: s = 1 - a, to a few 2^-24 of itself (of one, where a is small: such
