@@ -31,71 +31,58 @@ namespace {
 constexpr int LNT = 256;
 constexpr int W = 64;  // channels of a block: those that a wave joins, a lane each
 
-// The decay a of a row and channel in one number, by the type of the rows.
-//
-// float32: near one its distance a - 1, whose rounding a slow channel does not
-// compound over the rows that it remembers as it would one of a; elsewhere a.
-// The number's last bit says which, so that both a and 1 - a are known to a few
-// 2^-24 of themselves for every a, above one too.
-template <typename T> struct Decay {
-    static __device__ __forceinline__ float near(float m) { return __uint_as_float(__float_as_uint(m) | 1u); }
-    static __device__ __forceinline__ float far(float a) { return __uint_as_float(__float_as_uint(a) & ~1u); }
-    static __device__ __forceinline__ uint32_t is_near(float d) { return (uint32_t)__builtin_amdgcn_sbfe((int)__float_as_uint(d), 0, 1); }
-    static __device__ __forceinline__ float log(float g) {
-        // e^g - 1 by its series near zero, where the difference would cancel
-        float p = fmaf(g, 1.0f / 5040.0f, 1.0f / 720.0f);
-        p = fmaf(g, p, 1.0f / 120.0f);
-        p = fmaf(g, p, 1.0f / 24.0f);
-        p = fmaf(g, p, 1.0f / 6.0f);
-        p = fmaf(g, p, 0.5f);
-        p = fmaf(g * g, p, g);
-        return fabsf(g) <= 0.35f ? near(p) : far(exp_exact(g));
-    }
-    static __device__ __forceinline__ float sigmoid(float g) {
-        const float r = __builtin_amdgcn_rcpf(1.0f + exp_exact(fabsf(g)));  // the smaller one of a and 1 - a
-        return g > 0.f ? near(-r) : far(r);
-    }
-    static __device__ __forceinline__ float keep(float d, float h) {  // a h
-        return fmaf(d, h, __uint_as_float(is_near(d) & __float_as_uint(h)));
-    }
-    static __device__ __forceinline__ float rest(float d) {  // 1 - a
-        return __uint_as_float(~is_near(d) & 0x3f800000u) - d;
-    }
-    // a h + (1 - a) x as h + (a - 1) (h - x) or x + a (h - x): no product is larger than what it decays
-    template <bool COMP> static __device__ __forceinline__ float step(float h, float d, float x) {
-        const uint32_t n = is_near(d);
-        return COMP ? fmaf(d, h - x, __uint_as_float((n & __float_as_uint(h)) | (~n & __float_as_uint(x)))) : keep(d, h) + x;
-    }
-};
-// bfloat16: s = 1 - a, to a few 2^-24 of itself (of one, where a is small: such
-// a state counts as little beside the 2^-9 of the rows).  The kernels were bound
-// by their instructions, of which it takes half: gradients of 32768 x 2048 gates
-// 293 us with the form above, 269 with this one.
-template <> struct Decay<bf16> {
-    static __device__ __forceinline__ float log(float g) {
-        float p = fmaf(g, 1.0f / 24.0f, 1.0f / 6.0f);
-        p = fmaf(g, p, 0.5f);
-        p = fmaf(g, p, 1.0f);
-        return fabsf(g) <= 0.0625f ? -g * p : 1.0f - __builtin_amdgcn_exp2f(g * 1.44269502f);
-    }
-    static __device__ __forceinline__ float sigmoid(float g) {
-        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * 1.44269502f));
-    }
-    static __device__ __forceinline__ float keep(float s, float h) { return fmaf(-s, h, h); }
-    static __device__ __forceinline__ float rest(float s) { return s; }
-    template <bool COMP> static __device__ __forceinline__ float step(float h, float s, float x) {
-        // (h + s (x - h) is an operation less, but at s = 1 a rounding of x - h stays)
-        return COMP ? fmaf(s, x, keep(s, h)) : keep(s, h) + x;
-    }
-};
+// The decay a of a row and channel in one number.  Near one it is the distance
+// a - 1, whose rounding a slow channel does not compound over the rows that it
+// remembers as it would one of a; elsewhere a, so that what little a fast
+// channel keeps is as exact.  The number's last bit says which: both a and 1 - a
+// are known to a few 2^-24 of themselves for every a, above one too.  Rows in
+// bfloat16 take the hardware's power of a rounded product, (2 + |g|) 2^-24 off.
+namespace decay {
+constexpr float LOG2E = 1.44269502f;
+template <typename T> __device__ __forceinline__ float log(float g) {
+    // e^g - 1 by its series near zero, where the difference would cancel
+    constexpr bool LONG = std::is_same<T, float>::value;
+    float p = LONG ? fmaf(g, 1.0f / 5040.0f, 1.0f / 720.0f) : 1.0f / 720.0f;
+    p = fmaf(g, p, 1.0f / 120.0f);
+    p = fmaf(g, p, 1.0f / 24.0f);
+    p = fmaf(g, p, 1.0f / 6.0f);
+    p = fmaf(g, p, 0.5f);
+    p = fmaf(g * g, p, g);
+    const bool near = fabsf(g) <= (LONG ? 0.35f : 0.25f);
+    const float v = near ? p : LONG ? exp_exact(g) : __builtin_amdgcn_exp2f(g * LOG2E);
+    return __uint_as_float((__float_as_uint(v) & ~1u) | (near ? 1u : 0u));
+}
+template <typename T> __device__ __forceinline__ float sigmoid(float g) {
+    // r: the smaller one of a and 1 - a, which are kept as r, and as -r with the last bit set: where q is negative
+    const float q = g * -LOG2E;
+    const float e = std::is_same<T, float>::value ? exp_exact(fabsf(g)) : __builtin_amdgcn_exp2f(fabsf(q));
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const uint32_t n = (uint32_t)((int)__float_as_uint(q) >> 31), m = 0x80000001u;
+    return __uint_as_float((n & m) | (__float_as_uint(r) & ~m));
+}
+// Whether d is a - 1: all bits or none
+__device__ __forceinline__ uint32_t is_near(float d) {
+    return (uint32_t)__builtin_amdgcn_sbfe((int)__float_as_uint(d), 0, 1);
+}
+// a h
+__device__ __forceinline__ float keep(float d, uint32_t n, float h) {
+    return fmaf(d, h, __uint_as_float(n & __float_as_uint(h)));
+}
+// 1 - a
+__device__ __forceinline__ float rest(float d, uint32_t n) { return __uint_as_float(~n & 0x3f800000u) - d; }
+// a h + (1 - a) x as h + (a - 1) (h - x) or x + a (h - x): exact at a = 0, and no product is larger than what it decays
+template <bool COMP> __device__ __forceinline__ float step(float h, float d, uint32_t n, float x) {
+    return COMP ? fmaf(d, h - x, __uint_as_float((n & __float_as_uint(h)) | (~n & __float_as_uint(x)))) : keep(d, n, h) + x;
+}
+}  // namespace decay
 template <typename T, int N>
 __device__ __forceinline__ void decays(float (&d)[N], bool sigmoid) {
     if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = Decay<T>::sigmoid(d[i]);
+        for (int i = 0; i < N; ++i) d[i] = decay::sigmoid<T>(d[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = Decay<T>::log(d[i]);
+        for (int i = 0; i < N; ++i) d[i] = decay::log<T>(d[i]);
     }
 }
 
@@ -103,6 +90,9 @@ __device__ __forceinline__ void decays(float (&d)[N], bool sigmoid) {
 // (a sequence begins inside), so that nothing of another one is multiplied.
 struct Run {
     float A, B;
+    // Makes the compiler form A here.  Put off to where the walk ends, which it would do, it takes the kinds of all the
+    // decays there, two scalar registers each: 113 spilled (15151 x 2048 55.6 -> 52.7 us with this and the sign of q).
+    __device__ __forceinline__ void A_now() { asm volatile("" : "+v"(A)); }
 };
 // Zeros come out as +0.
 __device__ __forceinline__ float enter(Run r, float h) { return (r.A < 0.f ? r.B : fmaf(r.A, h, r.B)) + 0.f; }
@@ -335,8 +325,10 @@ __device__ __forceinline__ void walk(Run (&run)[E], const Chans<T, E> (&xr)[TT],
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = Decay<T>::template step<COMP>(run[e].B, d[e], x[e]);
-            run[e].A = Decay<T>::keep(d[e], run[e].A);
+            const uint32_t near = decay::is_near(d[e]);
+            run[e].B = decay::step<COMP>(run[e].B, d[e], near, x[e]);
+            run[e].A = decay::keep(d[e], near, run[e].A);
+            run[e].A_now();
         }
         if (!is.inside(i))
 #pragma unroll
@@ -364,8 +356,10 @@ __device__ __forceinline__ void walk_back(Run (&run)[E], const Chans<T, E> (&dr)
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            run[e].B = Decay<T>::keep(d[i][e], dy[e] + run[e].B);
-            run[e].A = Decay<T>::keep(d[i][e], run[e].A);
+            const uint32_t near = decay::is_near(d[i][e]);
+            run[e].B = decay::keep(d[i][e], near, dy[e] + run[e].B);
+            run[e].A = decay::keep(d[i][e], near, run[e].A);
+            run[e].A_now();
         }
         if (!is.inside(i))
 #pragma unroll
@@ -482,7 +476,7 @@ __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chai
             xr[i].to(x);
             if (is.is_first(i)) load_state<E>(h, p.h0, seq[k0 + i], p.C, at.col);
 #pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
+            for (int e = 0; e < E; ++e) h[e] = decay::step<COMP>(h[e], d[i][e], decay::is_near(d[i][e]), x[e]);
             Chans<T, E> o;
             o.from(h);
             o.store(y.r, y.off + i * y.step);
@@ -586,8 +580,9 @@ __global__ void __launch_bounds__(LNT, E == 8 ? 4 : 1) gdp_linrec_bwd_k(LinRec p
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             hp[i][e] = COMP ? h[e] - x[e] : h[e];
-            h[e] = Decay<T>::template step<COMP>(h[e], d[i][e], x[e]);
+            h[e] = decay::step<COMP>(h[e], d[i][e], decay::is_near(d[i][e]), x[e]);
         }
+        forget(h);  // row by row (the complement's gradients of 32768 x 2048: 230 us without, 227)
     }
 #pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
@@ -596,7 +591,8 @@ __global__ void __launch_bounds__(LNT, E == 8 ? 4 : 1) gdp_linrec_bwd_k(LinRec p
         if (is.is_last(i)) load_state<E>(m, p.dht, seq[k0 + i], p.C, at.col);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float l = dy[e] + m[e], al = Decay<T>::keep(d[i][e], l), cl = Decay<T>::rest(d[i][e]);
+            const uint32_t near = decay::is_near(d[i][e]);
+            const float l = dy[e] + m[e], al = decay::keep(d[i][e], near, l), cl = decay::rest(d[i][e], near);
             dx[e] = COMP ? cl * l : l;
             dg[e] = hp[i][e] * (p.sigmoid ? cl * al : al);
             m[e] = al;
@@ -658,7 +654,8 @@ __global__ void __launch_bounds__(LNT) gdp_linrec_decode_k(gdp_linrec_decode_arg
         gr.to(d);
         decays<T>(d, a.decay == GDP_DECAY_SIGMOID);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = a.complement ? Decay<T>::template step<true>(h[e], d[e], x[e]) : Decay<T>::template step<false>(h[e], d[e], x[e]);
+        for (int e = 0; e < E; ++e) h[e] = a.complement ? decay::step<true>(h[e], d[e], decay::is_near(d[e]), x[e])
+                                                       : decay::step<false>(h[e], d[e], decay::is_near(d[e]), x[e]);
         xr.from(h);
         xr.store(y + t * a.C);
     }

@@ -753,8 +753,10 @@ gdp_status gdp_group_norm_bwd(const gdp_group_norm_args *a, const gdp_group_norm
  *          contiguous too.
  *   ht     [nseq, C] float32 state after each sequence, or NULL (h0, or zero,
  *          for an empty one).  It may not overlap h0.
- * States are float32 and y is rounded once; 1 - a is formed without
- * cancellation (with bfloat16 rows a itself to 2^-24 of one).  Inputs must be finite but for a log decay of -inf; others
+ * States are float32 and y is rounded once.  a and 1 - a are known to a few
+ * 2^-24 of themselves, however small they are, and above a = 1 too; with
+ * bfloat16 rows the power behind them is (2 + |g|) 2^-24 off.  a = 0 drops the
+ * state exactly.  Inputs must be finite but for a log decay of -inf; others
  * reach only later rows of their channel and sequence.
  * Sizes: C <= 2^20, B*T < 2^31; a call that would launch 2^32 threads at once
  * is GDP_ERR_UNSUPPORTED.
