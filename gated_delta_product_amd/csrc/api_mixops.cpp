@@ -354,6 +354,7 @@ gdp_status gdp_rotary(const gdp_rotary_args *a, void *stream) {
     p.pos_ts = a->pos_t_stride;
     p.offsets = a->offsets;
     p.freq = a->freq;
+    if (!gdp::rotary_fits(p, a->dtype)) return too_large(name);
     return hip_status(gdp::launch_rotary(p, a->dtype, (hipStream_t)stream), name);
 }
 

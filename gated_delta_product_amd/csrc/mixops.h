@@ -72,6 +72,7 @@ struct Rotary {
     int64_t pos_bs, pos_ts;
     const double *freq;
 };
+bool rotary_fits(const Rotary &p, gdp_dtype dtype);
 hipError_t launch_rotary(const Rotary &p, gdp_dtype dtype, hipStream_t stream);
 
 }  // namespace gdp

@@ -139,24 +139,33 @@ hipError_t run_rotary(const Rotary &p, int ntok, int lanes_log, hipStream_t stre
     else hipLaunchKernelGGL((gdp_rotary_k<T, E, false>), grid, dim3(RNT), lds, stream, p, ntok, lanes_log);
     return hipGetLastError();
 }
+// Elements of a piece, threads side by side on a token's, and tokens of a block:
+// four or eight for every thread, few enough for 1024 blocks (one alone: a step
+// of a few tokens is all latency) and for LDS.
+struct Shape {
+    int E, lanes_log, ntok;
+    Shape(const Rotary &p, gdp_dtype dtype) : E(!p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4), lanes_log(0) {
+        const int half = p.R / 2, turned = p.interleaved ? p.R / (E == 1 ? 2 : E) : half / E;
+        const int64_t pieces = (int64_t)(p.H[0] + p.H[1]) * (turned + (p.D - p.R) / E);
+        while (lanes_log < 8 && (1 << lanes_log) < pieces) ++lanes_log;
+        ntok = 8 * (RNT >> lanes_log);
+        while (ntok > 1 && p.m.rows / ntok < 1024) ntok /= 2;
+        ntok = ntok > MAX_TOK ? MAX_TOK : ntok;
+        ntok = ntok > MAX_CS / half ? MAX_CS / half : ntok;
+    }
+};
 }  // namespace
 
+bool rotary_fits(const Rotary &p, gdp_dtype dtype) {
+    const int ntok = Shape(p, dtype).ntok;
+    return ((int64_t)p.m.rows + ntok - 1) / ntok * RNT <= 0xffffffffll;
+}
 hipError_t launch_rotary(const Rotary &p, gdp_dtype dtype, hipStream_t stream) {
     if (p.m.rows == 0) return hipSuccess;
-    const int E = !p.vec ? 1 : dtype == GDP_BF16 ? 8 : 4, half = p.R / 2;
-    const int turned = p.interleaved ? p.R / (E == 1 ? 2 : E) : half / E;
-    const int64_t pieces = (int64_t)(p.H[0] + p.H[1]) * (turned + (p.D - p.R) / E);
-    int lanes_log = 0;
-    while (lanes_log < 8 && (1 << lanes_log) < pieces) ++lanes_log;
-    // Tokens of a block: four or eight for every thread, few enough for 1024
-    // blocks (one alone: a step of a few tokens is all latency) and for LDS.
-    int ntok = 8 * (RNT >> lanes_log);
-    while (ntok > 1 && p.m.rows / ntok < 1024) ntok /= 2;
-    ntok = ntok > MAX_TOK ? MAX_TOK : ntok;
-    ntok = ntok > MAX_CS / half ? MAX_CS / half : ntok;
-    if (((int64_t)p.m.rows + ntok - 1) / ntok * RNT > 0xffffffffll) return hipErrorInvalidValue;
-    if (dtype == GDP_BF16) return E == 8 ? run_rotary<bf16, 8>(p, ntok, lanes_log, stream) : run_rotary<bf16, 1>(p, ntok, lanes_log, stream);
-    return E == 4 ? run_rotary<float, 4>(p, ntok, lanes_log, stream) : run_rotary<float, 1>(p, ntok, lanes_log, stream);
+    const Shape s(p, dtype);
+    if (dtype == GDP_BF16)
+        return s.E == 8 ? run_rotary<bf16, 8>(p, s.ntok, s.lanes_log, stream) : run_rotary<bf16, 1>(p, s.ntok, s.lanes_log, stream);
+    return s.E == 4 ? run_rotary<float, 4>(p, s.ntok, s.lanes_log, stream) : run_rotary<float, 1>(p, s.ntok, s.lanes_log, stream);
 }
 
 }  // namespace gdp

@@ -961,7 +961,8 @@ gdp_status gdp_conv_decode(const gdp_conv_decode_args *a, void *stream);
  * Tokens outside every request are left as they were.  Angles are formed in 64
  * bits, so any position an int32 holds keeps float32 accuracy; outputs are
  * rounded once.
- * Sizes: 2 <= R <= D <= 4096, R even, (H + HK) D <= 2^24, B*T < 2^31.
+ * Sizes: 2 <= R <= D <= 4096, R even, (H + HK) D <= 2^24, B*T < 2^31, and no
+ * launch of 2^32 threads, as above (of 2 to 64 tokens a block of 256).
  */
 typedef struct gdp_rotary_args {
     int64_t B;
