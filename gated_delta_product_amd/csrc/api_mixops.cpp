@@ -52,6 +52,22 @@ gdp_status check_output(const char *name, const char *what, const void *p, gdp_d
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
     return check_states(name, what, p, dtype, vec, unit);
 }
+// Whether two of the rows of `width` elements at b*bs + t*ts share one.
+bool rows_overlap(int64_t B, int64_t T, int64_t bs, int64_t ts, int64_t width) {
+    if (B > T) {
+        const int64_t n = B, s = bs;
+        B = T, bs = ts, T = n, ts = s;
+    }
+    if ((B > 1 && bs < width) || (T > 1 && ts < width)) return true;
+    const auto reach = [&](int64_t n, int64_t s) { return (__int128)(n - 1) * s + width; };
+    if (B <= 1 || bs >= reach(T, ts) || ts >= reach(B, bs)) return false;
+    for (int64_t b = 1; b < B; ++b) {  // the rows next to row (b, 0); B^2 <= B*T < 2^31
+        const __int128 at = (__int128)b * bs, t = at / ts, r = at % ts;
+        if (t >= T) break;
+        if (r < width || (t + 1 < T && ts - r < width)) return true;
+    }
+    return false;
+}
 // Elements of 16 bytes
 int64_t unit_of(gdp_dtype d) { return 16 / (int64_t)dsize(d); }
 
@@ -339,11 +355,13 @@ gdp_status gdp_rotary(const gdp_rotary_args *a, void *stream) {
         TRY(check_input(name, t[i].in, t[i].x, t[i].bs, t[i].ts, a->B, a->T, a->dtype, &p.vec, &p.in[i], unit));
         TRY(check_input(name, t[i].out, t[i].y, t[i].ybs, t[i].yts, a->B, a->T, a->dtype, &p.vec, &p.out[i], unit));
         const int64_t width = (int64_t)t[i].heads * a->D;
-        if ((a->T > 1 && t[i].yts < width) || (a->B > 1 && t[i].ybs < width))
+        if (rows_overlap(a->B, a->T, t[i].ybs, t[i].yts, width))
             return fail(GDP_ERR_INVALID, "%s: rows of %s overlap", name, t[i].out);
         if (t[i].x == t[i].y && (p.in[i].bs != p.out[i].bs || p.in[i].ts != p.out[i].ts))
             return fail(GDP_ERR_INVALID, "%s: %s is %s with other strides", name, t[i].out, t[i].in);
     }
+    if (a->H && a->HK && (a->qo == a->ko || a->qo == a->k || a->ko == a->q))
+        return fail(GDP_ERR_INVALID, "%s: an output lies on another tensor", name);
     p.D = a->D;
     p.R = a->R;
     p.interleaved = a->interleaved != 0;

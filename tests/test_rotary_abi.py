@@ -25,3 +25,23 @@ def rot(**kw):
 def test_too_many_threads_for_one_launch(kw):
     assert B.lib().gdp_rotary(ctypes.byref(rot(**kw)), None) == UNS
     assert b"too large" in B.lib().gdp_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=2, q_b_stride=160, qo_b_stride=160),                      # row 1 is row 0 one token on
+    dict(B=2, q_b_stride=1600 - 160, qo_b_stride=1600 - 160),        # its first token is row 0's last
+    dict(B=3, q_b_stride=80 + 1600, qo_b_stride=80 + 1600, q_t_stride=320, qo_t_stride=320),  # between tokens, and into one
+    dict(B=9, T=9, q_b_stride=7 * 160, qo_b_stride=7 * 160),
+    dict(B=2, T=1, q_b_stride=100, qo_b_stride=100),
+], ids=["same", "last", "between", "seven", "one token"])
+def test_rows_of_an_output_that_overlap(kw):
+    assert B.lib().gdp_rotary(ctypes.byref(rot(**kw)), None) == INV
+    assert b"overlap" in B.lib().gdp_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(qo=0x40000, ko=0x10000), dict(ko=0x10000), dict(qo=0x40000), dict(qo=0x50000, ko=0x50000)],
+                         ids=["swapped", "k' on q", "q' on k", "k' on q'"])
+def test_an_output_on_another_tensor(kw):
+    both = dict(HK=2, k=0x40000, k_b_stride=1600, k_t_stride=160, ko=0x60000, ko_b_stride=1600, ko_t_stride=160)
+    assert B.lib().gdp_rotary(ctypes.byref(rot(**{**both, **kw})), None) == INV
+    assert B.lib().gdp_last_error()
