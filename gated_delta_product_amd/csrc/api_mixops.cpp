@@ -52,6 +52,13 @@ gdp_status check_output(const char *name, const char *what, const void *p, gdp_d
     if (!p) return fail(GDP_ERR_INVALID, "%s: %s is NULL", name, what);
     return check_states(name, what, p, dtype, vec, unit);
 }
+// An output of contiguous [B, T, C] on top of an input: only where that one's elements are the output's.
+gdp_status check_on_top(const char *name, const char *what, const void *y, gdp_dtype dtype, const void *x, gdp_dtype x_dtype,
+                        int64_t bs, int64_t ts, int64_t B, int64_t T, int64_t C) {
+    if (y == x && (dtype != x_dtype || (B > 1 && bs != T * C) || (T > 1 && ts != C)))
+        return fail(GDP_ERR_INVALID, "%s: y is %s, of other strides or another type", name, what);
+    return ok();
+}
 // Whether two of the rows of `width` elements at b*bs + t*ts share one.
 bool rows_overlap(int64_t B, int64_t T, int64_t bs, int64_t ts, int64_t width) {
     if (B > T) {
@@ -163,6 +170,8 @@ gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t wor
         TRY(check_input(name, "x", a->x, a->x_b_stride, a->x_t_stride, a->B, a->T, a->dtype, &p.vec, &p.x, unit));
         TRY(check_input(name, "g", a->g, a->g_b_stride, a->g_t_stride, a->B, a->T, a->g_dtype, &p.vec, &p.g, gunit));
         TRY(check_output(name, "y", a->y, a->dtype, &p.vec, unit));
+        TRY(check_on_top(name, "x", a->y, a->dtype, a->x, a->dtype, a->x_b_stride, a->x_t_stride, a->B, a->T, a->C));
+        TRY(check_on_top(name, "g", a->y, a->dtype, a->g, a->g_dtype, a->g_b_stride, a->g_t_stride, a->B, a->T, a->C));
     }
     TRY(check_states(name, "h0", a->h0, GDP_F32, &p.vec, 1));
     TRY(check_states(name, "ht", a->ht, GDP_F32, &p.vec, 1));
@@ -224,6 +233,8 @@ gdp_status gdp_linrec_decode(const gdp_linrec_decode_args *a, void *stream) {
     TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &vec, &x, unit));
     TRY(check_input(name, "g", a->g, a->g_n_stride, a->g_t_stride, a->n, a->S, a->g_dtype, &vec, &g, unit_of(a->g_dtype)));
     TRY(check_output(name, "y", a->y, a->dtype, &vec, unit));
+    TRY(check_on_top(name, "x", a->y, a->dtype, a->x, a->dtype, a->x_n_stride, a->x_t_stride, a->n, a->S, a->C));
+    TRY(check_on_top(name, "g", a->y, a->dtype, a->g, a->g_dtype, a->g_n_stride, a->g_t_stride, a->n, a->S, a->C));
     if (!a->state && a->pool > 0) return fail(GDP_ERR_INVALID, "%s: state is NULL", name);
     TRY(check_states(name, "state", a->state, GDP_F32, &vec, 1));
     return hip_status(gdp::launch_linrec_decode(*a, vec, (hipStream_t)stream), name);
@@ -314,6 +325,7 @@ gdp_status gdp_conv_decode(const gdp_conv_decode_args *a, void *stream) {
     const int64_t unit = unit_of(a->dtype);
     TRY(check_input(name, "x", a->x, a->x_n_stride, a->x_t_stride, a->n, a->S, a->dtype, &p.vec, &p.x, unit));
     TRY(check_output(name, "y", a->y, a->dtype, &p.vec, unit));
+    TRY(check_on_top(name, "x", a->y, a->dtype, a->x, a->dtype, a->x_n_stride, a->x_t_stride, a->n, a->S, a->C));
     if (!a->state && a->pool > 0) return fail(GDP_ERR_INVALID, "%s: state is NULL", name);
     TRY(check_states(name, "state", a->state, a->dtype, &p.vec, unit));
     return hip_status(gdp::launch_conv_decode(*a, p.vec, (hipStream_t)stream), name);

@@ -824,7 +824,7 @@ gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, v
  *          for request i).  A slot outside [0, pool) -- e.g. -1 for a padding
  *          entry -- skips the request: no state is touched and its y rows are
  *          zero.  Slots of one call must be distinct.
- *   y      [n, S, C] dtype, contiguous
+ *   y      [n, S, C] dtype, contiguous (may be x or g, as there)
  * Sizes: C <= 2^20, S <= 4096, n*C < 2^32.
  */
 typedef struct gdp_linrec_decode_args {
