@@ -14,14 +14,14 @@
 // its neighbours.
 //
 // Measured, with inputs that are not in the caches: 32768 x 2048 rows in
-// bfloat16 with float32 log decays 122 us (537 MB, 4.4 TB/s, a large copy
-// reaching 5.1), a ragged pack of 15151 x 2048 gates 61 (186 MB); gradients of
-// 32768 x 2048 gates 230: 6 for clearing the words, 63 for the states (268 MB),
-// 161 for the rows (671 MB).  Left over is what a block waits: for its number,
+// bfloat16 with float32 log decays 120 us (537 MB, 4.5 TB/s, a large copy
+// reaching 5.1), a ragged pack of 15151 x 2048 gates 65 (186 MB); gradients of
+// 32768 x 2048 gates 233: 6 for clearing the words, 64 for the states (268 MB),
+// 163 for the rows (671 MB).  Left over is what a block waits: for its number,
 // its rows, and the state, some 12 us of which the other two or three blocks of
-// its compute unit hide the most.  Rows that do not start on 16 bytes go by
-// single elements (16384 x 1999 bfloat16: 101 and 220 us, 16384 x 2000: 59 and
-// 138).
+// its compute unit hide the most.  float32 rows of 16384 x 2000 take 99 and 207
+// us (floors 78 and 129).  Rows that do not start on 16 bytes go by single
+// elements (16384 x 1999 bfloat16: 101 and 221 us, 16384 x 2000: 62 and 137).
 #include "rows.h"
 
 namespace gdp {
@@ -410,8 +410,7 @@ struct Joint {
 }  // namespace
 
 // ROWS: y and the final states; without: only the chain, for the gradients.
-// Three blocks to a compute unit (168 registers; 12 bytes of a few variants
-// spill): two of 173 registers take 3% longer.
+// Three blocks to a compute unit with rows in bfloat16 (165 registers).
 template <typename T, typename G, int E, int TT, bool COMP, bool ROWS>
 __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
@@ -494,7 +493,8 @@ __global__ void __launch_bounds__(LNT, ROWS ? 3 : 1) gdp_linrec_k(LinRec p, Chai
 
 // The gradients, tiles from the last to the first; fwd is the chain that
 // gdp_linrec_k without ROWS leaves, of the same tiles.  Four blocks to a compute
-// unit (128 registers) instead of three: 226 -> 222 us.
+// unit with rows in bfloat16 (128 registers, two or three more spill) instead of
+// three (136): 235 -> 226 us for 32768 x 2048.  float32 rows take 165.
 template <typename T, typename G, int E, int TT, bool COMP>
 __global__ void __launch_bounds__(LNT, E == 8 ? 4 : 1) gdp_linrec_bwd_k(LinRec p, Chain fwd, Chain ch, int strips) {
     __shared__ uint8_t code[LNT / (W / E) * TT];
@@ -666,9 +666,8 @@ namespace {
 
 // Channels and rows that a thread holds: 16 bytes of a row, and about as many
 // registers of rows as let three or four blocks share a compute unit
-// (bfloat16, 4 / 8 rows forwards: 15151 x 2048 54 / 50 us, 32768 x 2048 123 /
-// 120; 16 rows of 8 bytes 77 and 196.  Backwards 4 / 8: 238 / 228, but 2 x 1024 x
-// 1024 19.5 / 23).
+// (bfloat16, inputs in the caches, 4 / 8 rows forwards: 15151 x 2048 56 / 53 us,
+// 32768 x 2048 127 / 120.  Backwards 4 / 8: 226 / 254, 2 x 1024 x 1024 20 / 25).
 int elems_of(const LinRec &p) { return !p.vec ? 1 : p.f32 ? 4 : 8; }
 constexpr int rows_of(int E, bool back) { return E == 1 ? (back ? 8 : 16) : E == 4 || !back ? 8 : 4; }
 int strips_of(const LinRec &p) { return (p.C + W - 1) / W; }

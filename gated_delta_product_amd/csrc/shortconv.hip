@@ -10,8 +10,11 @@
 // caches, and that bounds the forward pass: 32768 x 10240 bfloat16, W = 4, 244 us
 // (1342 MB, 5.5 TB/s; a large copy reaches 5.1).  The gradients form 36
 // instructions an element, which take as long as two thirds of the time and are
-// not all hidden: 15151 x 5632 125 us (513 MB, 4.1 TB/s), 6 of them the sums of the
-// runs' partial dw and db.  256 steps of 10240 channels take 10 us (the floor is 8).
+// not all hidden, and before them a thread asks what its 64 rows are, one after
+// the other (plain_rows): 15151 x 5632 125 us (513 MB, 4.1 TB/s), 6 of them the
+// sums of the runs' partial dw and db.  256 steps of 10240 channels take 11 us (the
+// floor is 8): a thread's taps come first, then its state and its rows, and five
+// waves a SIMD (94 registers) hide little of the one round that they are.
 // Rows that do not start on 16 bytes go by single elements (16384 x 4999
 // bfloat16: 107 and 173 us, 16384 x 5000: 71 and 140).
 #include "rows.h"
@@ -27,7 +30,9 @@ constexpr int CHUNK = 4;  // rows whose loads are under way together, the next o
 // / 125 rows: 141 / 133 / 130 / 137 us; chunks of 2 / 4 / 8: 142 / 130 / 150).
 constexpr int run_of(bool back, int W) { return back ? 16 * CHUNK - (W - 1) : 4 * CHUNK; }
 
-// 1 / (1 + e^-u).  bfloat16: to (2 + |u|) 2^-24, far within the rows' own 2^-9.
+// 1 / (1 + e^-u).  bfloat16: to (2 + |u|) 2^-24, far within the rows' own 2^-9; the
+// float32 dw and db sum such terms, and their own roundings hide it (15151 x 512:
+// both 1.6e-7 off, as with an exact power, which takes 7 us more at 5632).
 template <typename T> __device__ __forceinline__ float sigmoid_of(float u) {
     if constexpr (std::is_same<T, float>::value) return sigmoid_exact(u);
     else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269502f));
