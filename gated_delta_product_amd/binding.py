@@ -1067,7 +1067,7 @@ def linrec_bwd(dy, x, g, decay="log", complement=False, cu_seqlens=None, initial
 def linrec_decode(x, g, state, decay="log", complement=False, slots=None, y=None):
     """gdp_linrec_decode: S new tokens of each request through the recurrence of linrec_fwd.  x, g [n, S, C] (strided
     as there); state [pool, C] float32, updated in place; slots int32 [n] (outside [0, pool): skipped, its y rows zero)
-    or None.  Returns y [n, S, C].  It has no gradients."""
+    or None.  Returns y [n, S, C] (``y`` may be x or g, as there).  It has no gradients."""
     dev = _need_cuda(x, g, state, slots, y)
     code, xs, gs = _rec_input(x, g, decay)
     n, S, C = x.shape
@@ -1221,8 +1221,8 @@ def rotary(q, k, freq, positions=None, offsets=None, cu_seqlens=None, interleave
     interleaved, (2i, 2i + 1), and pair i turns by position * freq[i] (freq float64, radians; see rotary_freq), times
     scale.  A token's position is positions[b, t] (int32), or its place in its row or request of cu_seqlens plus
     offsets[sequence] (int32 [nseq], or None: 0).  inverse=True turns back: given the gradients of the outputs it
-    returns those of q and k.  ``out`` may be (q', k') to write to, strided likewise, also (q, k) themselves.  Returns
-    (q', k'); rows outside every request are not written."""
+    returns those of q and k.  ``out`` may be (q', k') to write to, strided likewise without rows that overlap, also
+    (q, k) themselves.  Returns (q', k'); rows outside every request are not written."""
     dev = _need_cuda(q, k, freq, positions, offsets, cu_seqlens, *(out or ()))
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must be 4-D")

@@ -809,7 +809,8 @@ typedef struct gdp_linrec_grads {
 int64_t gdp_linrec_workspace_bytes(const gdp_linrec_args *a, int32_t backward);
 /* workspace: gdp_linrec_workspace_bytes bytes, 256-byte aligned, caller-owned;
  * its contents do not matter and are not kept.  Calls that may overlap in time
- * need one each. */
+ * need one each.  (States are handed on through it inside the launch; a part of
+ * it that is kept waiting for seconds gives up, and its rows become NaN.) */
 gdp_status gdp_linrec_fwd(const gdp_linrec_args *a, void *workspace, int64_t workspace_bytes, void *stream);
 /* y, ht and the output pointers of a are not used. */
 gdp_status gdp_linrec_bwd(const gdp_linrec_args *a, const gdp_linrec_grads *d, void *workspace,
